@@ -282,6 +282,229 @@ int xpress_latent_reserve(int64_t N, int64_t B, int64_t R, int64_t H, hipStream_
 int xpress_latent_set_tiles(int mix, int gate, int down);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Serving operators: a paged key-value cache, the append that fills it, the
+ * attention that reads it, and the sampled readout.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types. */
+#define XPRESS_BF16 0
+#define XPRESS_FP16 1
+#define XPRESS_E4M3 2 /* OCP 8-bit float, 4 exponent and 3 fraction bits; caches only */
+
+/*
+ * xpress_kv_cache -- a paged cache of keys and values and the page table of
+ * the sequences that live in it.  Token j of sequence n is on page
+ * page_table[n * stride_table + j / page_size], at place j % page_size;
+ * element (page, head, place, d) is at
+ *     page * stride_page + head * stride_head + place * stride_token + d
+ * in k and in v (elements; both caches share the strides).
+ *
+ *   k, v          device pointers.
+ *   k_scale,      device pointers, fp32 [heads], or null (1).  Only for
+ *   v_scale       XPRESS_E4M3: a stored code stands for code * scale[head].
+ *   page_table    device pointer, int32 [seqs, table_width].
+ *   pages         pages in the pool, >= 1; page ids outside [0, pages) name no page.
+ *   page_size     tokens of a page, >= 1 (any value; tiles may span pages).
+ *   heads         key-value heads, >= 1.
+ *   dim           elements of a head, >= 1.
+ *   stride_*      elements, >= 1; no two elements may share an address.
+ *   dtype         XPRESS_BF16, XPRESS_FP16 or XPRESS_E4M3.
+ *   seqs          rows of page_table, >= 0.
+ *   table_width   columns of page_table, >= 1 (table_width * page_size <= 2^31 - 1).
+ *   stride_table  row stride of page_table in elements, >= table_width
+ *                 (0 is allowed with one row).
+ */
+typedef struct xpress_kv_cache {
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* page_table;
+    int64_t pages, page_size, heads, dim;
+    int64_t stride_page, stride_head, stride_token;
+    int64_t dtype;
+    int64_t seqs, table_width, stride_table;
+} xpress_kv_cache;
+
+/*
+ * xpress_kv_append -- append the keys and values of T new tokens to a paged
+ * cache, with the position rotation applied on the way, and rotate the
+ * tokens' queries.  For token t of sequence n at position p, with c_i =
+ * cos_sin[p, i] and s_i = cos_sin[p, rot_dim/2 + i], i < rot_dim/2:
+ *
+ *     rot(x)[a_i] = x[a_i] c_i - x[b_i] s_i
+ *     rot(x)[b_i] = x[b_i] c_i + x[a_i] s_i        rot(x)[d] = x[d], d >= rot_dim
+ *     q_out[t, h]             = round(rot(q[t, h]))
+ *     K(page_table, n, p)[h]  = round(rot(k[t, h]) / k_scale[h])
+ *     V(page_table, n, p)[h]  = round(v[t, h] / v_scale[h])
+ *
+ * where (a_i, b_i) = (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved.
+ * The two products and their sum are formed in fp32, each rounded, and the
+ * result is rounded once to the stored type (ties to even); XPRESS_E4M3
+ * saturates at +-448 and keeps NaN.
+ *
+ *   q, k, v      device pointers, [T, Hq or heads, dim] of `dtype` (BF16 or
+ *                FP16) with token and head strides in elements (any, 0
+ *                included) and unit stride along dim: slices of one
+ *                projection's rows do.  q and q_out are ignored when Hq is 0.
+ *   q_out        device pointer, written whole.  May be q itself with q's
+ *                strides; must not share elements with k or v.
+ *   positions    device pointer, int32 [T].
+ *   seq_of       device pointer, int32 [T], the tokens' sequences; or null:
+ *                T is a multiple of cache.seqs and token t belongs to sequence
+ *                t / (T / seqs).
+ *   cos_sin      device pointer, fp32 [max_pos, rot_dim] contiguous; unused
+ *                when rot_dim is 0.
+ *   rot_dim      even, 0 <= rot_dim <= dim.
+ *
+ * A token whose sequence or position is out of range (negative, or past
+ * cache.seqs, table_width * page_size, or max_pos) is padding: nothing is
+ * stored and its q_out rows are 0.  A token whose page id is outside the
+ * pool is rotated but not stored.  Two tokens at one place of one sequence
+ * leave one of them there.  cache.dtype is `dtype` or XPRESS_E4M3.
+ *
+ * Asynchronous; one launch; no workspace.  T == 0 queues nothing.  Any
+ * alignment that suits the element types is accepted; 16-byte aligned rows
+ * with rot_dim a multiple of 16 and dim a multiple of 8 take the vector path,
+ * with identical results.  XPRESS_EINVAL: a size or type outside the above, a
+ * null pointer, a pointer not aligned to its element, a cache or q_out whose
+ * elements share addresses, or a cache whose span overlaps q, k, v, q_out or
+ * an index array.
+ */
+typedef struct xpress_kv_append_args {
+    xpress_kv_cache cache;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    const int32_t* positions;
+    const int32_t* seq_of;
+    const float* cos_sin;
+    int64_t T, Hq, dtype;
+    int64_t rot_dim, max_pos, interleaved;
+    int64_t stride_q_t, stride_q_h, stride_k_t, stride_k_h;
+    int64_t stride_v_t, stride_v_h, stride_o_t, stride_o_h;
+} xpress_kv_append_args;
+
+int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t stream);
+
+/*
+ * xpress_paged_attention -- attention of the Q newest tokens of every
+ * sequence over its paged cache (Q = 1: decoding; Q = B: verifying a drafted
+ * block).  With len = lens[n] (the new tokens included, already appended),
+ * query i of sequence n stands at position pos = len - Q + i and sees the
+ * keys 0 <= j <= pos, j > pos - window when window > 0; query head h reads
+ * key-value head h / (Hq / heads):
+ *
+ *     out[n, i, h] = sum_j softmax_j(scale * q[n, i, h] . K_j) V_j
+ *     lse[n, i, h] = log sum_j exp(scale * q[n, i, h] . K_j)
+ *
+ * A query that sees no key (pos < 0, or every page missing) gives out = 0,
+ * lse = -inf.  Keys on pages whose id is outside the pool take no part, and
+ * neither they nor cache places that no query sees influence the result,
+ * whatever they hold.
+ *
+ *   q, out       device pointers, [N, Q, Hq, dim] of `dtype` (BF16 or FP16),
+ *                strides in elements, unit stride along dim.  N = cache.seqs.
+ *   lse          device pointer, fp32 [N, Q, Hq] contiguous, or null.
+ *   lens         device pointer, int32 [N]; values are clamped to
+ *                [0, max_len].
+ *   max_len      1 <= max_len <= table_width * page_size: an upper bound on
+ *                lens that the split over the length is planned for.
+ *   scale        fp32 factor of the scores, finite.
+ *   dim          a multiple of 8 (of 16 with an XPRESS_E4M3 cache), at most
+ *                256; cache.dtype is `dtype` or XPRESS_E4M3; the cache rows
+ *                must start on 16-byte boundaries.
+ *
+ * Scores, softmax statistics and sums are fp32.  Asynchronous; one launch,
+ * or two when the length is split (partial results meet in the (device,
+ * stream) workspace; xpress_paged_attention_reserve grows it before a
+ * capture).  The result does not depend on the order in which workgroups
+ * run.  N == 0 or Q == 0 queues nothing.  Errors: XPRESS_EINVAL (sizes,
+ * types, strides, null or misaligned pointers, out or lse overlapping an
+ * input or the caches; nothing queued), XPRESS_ENOMEM / XPRESS_ECAPTURE
+ * (workspace), XPRESS_EHIP (launch).
+ */
+typedef struct xpress_paged_attention_args {
+    xpress_kv_cache cache;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* lens;
+    int64_t Q, Hq, dtype, max_len, window;
+    double scale;
+    int64_t stride_q_n, stride_q_i, stride_q_h;
+    int64_t stride_o_n, stride_o_i, stride_o_h;
+} xpress_paged_attention_args;
+
+int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t stream);
+
+/*
+ * xpress_paged_attention_reserve -- grow the (device, stream) workspace to
+ * what xpress_paged_attention needs for N sequences of up to max_len tokens,
+ * Q new ones each, and these heads, head size and window.  Synchronous.
+ * Returns XPRESS_OK, XPRESS_EINVAL, XPRESS_ENOMEM or XPRESS_EHIP.
+ */
+int xpress_paged_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t heads, int64_t dim,
+                                   int64_t max_len, int64_t window, hipStream_t stream);
+
+/*
+ * xpress_paged_attention_plan -- the launch that such a call would make:
+ * *chunk, the keys of one part of the split, *splits, the parts of the
+ * longest sequence, *rows, the (query, head) rows a workgroup holds, and
+ * *launches.  Any output may be null.  Pure host computation.  Returns
+ * XPRESS_OK or XPRESS_EINVAL.
+ */
+int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads, int64_t dim,
+                                int64_t max_len, int64_t window, int* chunk, int* splits,
+                                int* rows, int* launches);
+
+/*
+ * xpress_sample_to_blk -- the sampled readout: one token per draft row, drawn
+ * with a given uniform number, written where the argmax readout would write
+ * it.  For row r = n*(B-1) + b:
+ *
+ *     z_v = bf16(base[r, v] + bias[r, v])      (base[r, v] when bias is null)
+ *
+ * The ids are ordered by z (larger first; -0 equals +0; the lower id first
+ * among equals), with weights w_v = exp((z_v - max z) / temperature[r]).
+ * Three rules each keep a prefix of that order, and the shortest holds (at
+ * least one id always):
+ *
+ *     top_k[r] > 0        the first top_k ids (mass Z; without it Z is the whole);
+ *     top_p[r] < 1        ids before which less than top_p * Z has accumulated;
+ *     min_p[r] > 0        ids with w_v >= min_p.
+ *
+ * With M the mass of the kept ids, blk[n, 1 + b] is the first id in the order
+ * at which the accumulated mass exceeds u[r] * M, and prob[r] = w / M, its
+ * probability.  temperature[r] not above 0 (NaN included) takes the largest z,
+ * probability 1.  The masses are sums of counts times weights in 64 bits, so
+ * the draw does not depend on the order of the work.
+ *
+ * NaN logits and -inf are never drawn; a row with nothing else gives id 0,
+ * prob 0.  A +inf logit leaves only the +inf ones.  u is clamped to
+ * [0, 1 - 2^-24] (NaN: 0); a NaN top_p or min_p is as if not given.
+ *
+ *   base, bias     as for xpress_add_argmax_to_blk; bias may be null.
+ *   blk            device pointer to int64 [N, B]; slots 1..B-1 written.
+ *   prob           device pointer, fp32 [N*(B-1)], or null.
+ *   temperature,   device pointers, fp32 [N*(B-1)].
+ *   top_p, min_p,
+ *   u
+ *   top_k          device pointer, int32 [N*(B-1)].
+ *   N, B, V, strides, stream   as for xpress_add_argmax_to_blk.
+ *
+ * Asynchronous; one launch; no workspace.  Errors as for
+ * xpress_add_argmax_to_blk (stride_bias_r is not looked at without bias).
+ */
+int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, int64_t* blk, float* prob,
+                         const float* temperature, const int32_t* top_k, const float* top_p,
+                         const float* min_p, const float* u, int64_t N, int64_t B, int64_t V,
+                         int64_t stride_base_r, int64_t stride_bias_r, hipStream_t stream);
+
+/*
  * xpress_release -- free every workspace the library holds on the current
  * device, live and retired (after synchronising that device).  Optional; for
  * tests and for callers that want the memory back.  No other call of the

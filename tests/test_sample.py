@@ -1,0 +1,241 @@
+"""xpress_sample_to_blk against the definition in 64 bits: the ids have to be equal, the
+probability is rounded once to fp32 (2^-24, and 2^-40 for the 64-bit sums before it)."""
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as ref
+from gpu_util import say
+from vocab_wide_add_amd import native
+
+OPEN = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
+
+
+def settings(rows, rng, **given):
+    out = {}
+    for name, default in OPEN.items():
+        v = given.get(name, default)
+        out[name] = np.broadcast_to(np.asarray(v, np.int32 if name == "top_k" else np.float32), rows).copy()
+    u = given.get("u")
+    out["u"] = rng.random(rows, np.float32) if u is None else np.broadcast_to(np.float32(u), rows).copy()
+    return out
+
+
+def draw(base, bias, N, B, V, s, prob=True):
+    blk = torch.full((N, B), -5, dtype=torch.int64, device="cuda")
+    p = torch.full((N * (B - 1),), 7.0, device="cuda") if prob else None
+    dev = {k: torch.from_numpy(v).cuda() for k, v in s.items()}
+    native.xpress_sample_to_blk(base, bias, blk, dev["temperature"], dev["top_k"], dev["top_p"],
+                                dev["min_p"], dev["u"], N, B, V, base.stride(0),
+                                bias.stride(0) if bias is not None else 0, prob=p)
+    torch.cuda.synchronize()
+    assert (blk[:, 0] == -5).all()
+    return blk[:, 1:].reshape(-1).cpu().numpy(), p.cpu().numpy() if prob else None
+
+
+def verify(base, bias, N, B, V, s):
+    """base, bias: CPU bf16 tensors [rows, stride]."""
+    z = base[:, :V].double()
+    if bias is not None:
+        z = (base[:, :V].float() + bias[:, :V].float()).to(torch.bfloat16).double()
+    ids, probs = ref.sample64(z.numpy(), s["temperature"], s["top_k"], s["top_p"], s["min_p"], s["u"])
+    got, p = draw(base.cuda(), bias.cuda() if bias is not None else None, N, B, V, s)
+    assert np.array_equal(got, ids), (got, ids, s)
+    assert (np.abs(p - probs) <= probs * (2.0 ** -24 + 2.0 ** -40)).all(), (p, probs)
+    return ids, probs
+
+
+def normal(rng, rows, stride, sigma=4.0):
+    return torch.from_numpy((rng.standard_normal((rows, stride)) * sigma).astype(np.float32)).to(torch.bfloat16)
+
+
+FILTERS = {
+    "open": {},
+    "cold": dict(temperature=0.05),
+    "hot": dict(temperature=50.0),
+    "greedy": dict(temperature=0.0),
+    "k1": dict(top_k=1),
+    "k50": dict(top_k=50, temperature=2.0),
+    "p": dict(top_p=0.9),
+    "p_small": dict(top_p=1e-6),
+    "min_p": dict(min_p=0.02),
+    "k_p_min": dict(top_k=40, top_p=0.95, min_p=0.001, temperature=1.7),
+    "k_over": dict(top_k=10 ** 9),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("filters", sorted(FILTERS))
+@pytest.mark.parametrize("N,B,V,pad,with_bias", [
+    (1, 2, 1, 0, False), (2, 4, 7, 1, True), (3, 5, 1000, 0, True), (2, 16, 1003, 0, False),
+    (1, 9, 8192, 64, True), (1, 4, 32000, 0, False), (2, 3, 40961, 7, True), (1, 3, 152064, 0, True),
+    (1, 2, 200001, 0, False)])
+def test_against_64_bits(filters, N, B, V, pad, with_bias):
+    say("sample %s %d %d %d %d %s" % (filters, N, B, V, pad, with_bias))
+    rng = np.random.default_rng([V, sorted(FILTERS).index(filters)])
+    rows = N * (B - 1)
+    base, bias = normal(rng, rows, V + pad), normal(rng, rows, V + pad, 0.5) if with_bias else None
+    verify(base, bias, N, B, V, settings(rows, rng, **FILTERS[filters]))
+
+
+@pytest.mark.gpu
+def test_rows_have_settings_of_their_own():
+    rng = np.random.default_rng(11)
+    rows, V = 60, 5000
+    s = settings(rows, rng)
+    s["temperature"] = rng.choice([0.0, 0.3, 1.0, 4.0, -1.0, np.nan], rows).astype(np.float32)
+    s["top_k"] = rng.choice([-3, 0, 1, 2, 17, 600], rows).astype(np.int32)
+    s["top_p"] = rng.choice([0.0, -1.0, 0.5, 0.99, 1.0, 2.0, np.nan], rows).astype(np.float32)
+    s["min_p"] = rng.choice([0.0, 0.1, 1.0, 2.0, -1.0, np.nan], rows).astype(np.float32)
+    verify(normal(rng, rows, V), normal(rng, rows, V, 0.5), 15, 5, V, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("u", [0.0, 1.0, 1 - 2.0 ** -24, -1.0, 2.0, float("nan"), 0.5])
+def test_ends_of_the_uniform_number(u):
+    rng = np.random.default_rng(12)
+    base = normal(rng, 3, 500)
+    for f in ("open", "k50", "p", "min_p"):
+        verify(base, None, 1, 4, 500, settings(3, rng, u=u, **FILTERS[f]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1000, 70000, 152064])
+def test_ties(V):
+    """Integer logits: thousands of equal values, picked by id; all equal; two values."""
+    rng = np.random.default_rng([13, V])
+    ints = torch.from_numpy(rng.integers(-8, 9, (4, V)).astype(np.float32)).to(torch.bfloat16)
+    for f in ("open", "k50", "p", "k_p_min", "hot"):
+        verify(ints, None, 2, 3, V, settings(4, rng, **FILTERS[f]))
+    for value in (0.0, 3.5, -2.0):
+        flat = torch.full((4, V), value, dtype=torch.bfloat16)
+        for f in ("open", "k50", "p", "greedy", "min_p"):
+            verify(flat, None, 2, 3, V, settings(4, rng, **FILTERS[f]))
+    two = torch.where(torch.from_numpy(rng.random((4, V)) < 0.02), 1.0, -1.0).to(torch.bfloat16)
+    for f in ("open", "k50", "p", "greedy"):
+        verify(two, None, 2, 3, V, settings(4, rng, **FILTERS[f]))
+
+
+@pytest.mark.gpu
+def test_both_zeros_are_one_value():
+    rng = np.random.default_rng(14)
+    base = torch.from_numpy(np.where(rng.random((6, 900)) < 0.5, 0.0, -0.0).astype(np.float32)).to(torch.bfloat16)
+    base[:3, 5::7] = -1.0
+    base[3:, 5::7] = 2.0
+    for f in ("open", "k50", "p", "greedy"):
+        verify(base, None, 2, 4, 900, settings(6, rng, **FILTERS[f]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [300, 152064])
+def test_masked_logits(V):
+    """-inf, the type's lowest value, NaN of both signs and +inf among the logits."""
+    rng = np.random.default_rng([15, V])
+    low = torch.finfo(torch.bfloat16).min
+    nan = torch.tensor(float("nan"), dtype=torch.bfloat16)
+    rows = []
+    for mask in (float("-inf"), low, nan, -nan):
+        x = normal(rng, 1, V)[0]
+        keep = torch.from_numpy(rng.random(V) < 0.05)
+        keep[V // 2] = True
+        rows.append(torch.where(keep, x, torch.as_tensor(mask, dtype=torch.bfloat16)))
+    one = torch.full((V,), float("-inf"), dtype=torch.bfloat16)
+    one[V - 1] = -3.0
+    rows.append(one)
+    rows.append(torch.full((V,), low, dtype=torch.bfloat16))            # all alike
+    mixed = torch.full((V,), low, dtype=torch.bfloat16)
+    mixed[::3] = float("-inf")
+    rows.append(mixed)
+    huge = normal(rng, 1, V)[0]
+    huge[::11] = float("inf")
+    rows.append(huge)
+    steep = torch.from_numpy(rng.choice([low, low / 2, low / 256], V).astype(np.float32)).to(torch.bfloat16)
+    rows.append(steep)
+    base = torch.stack(rows)
+    for f in ("open", "k50", "p", "greedy", "min_p", "hot"):
+        verify(base, None, 3, 4, V, settings(9, rng, **FILTERS[f]))
+    verify(base[-1:], None, 1, 2, V, settings(1, rng, temperature=1e38))
+    verify(base[:2], None, 1, 3, V, settings(2, rng, temperature=float("inf"), top_k=20))
+
+
+@pytest.mark.gpu
+def test_rows_with_nothing_to_draw():
+    rng = np.random.default_rng(16)
+    base = torch.full((3, 1000), float("-inf"), dtype=torch.bfloat16)
+    base[1] = float("nan")
+    base[2, ::2] = float("nan")
+    for f in ("open", "greedy", "p"):
+        ids, probs = verify(base, None, 1, 4, 1000, settings(3, rng, **FILTERS[f]))
+        assert (ids == 0).all() and (probs == 0).all()
+
+
+@pytest.mark.gpu
+def test_extreme_temperatures():
+    rng = np.random.default_rng(17)
+    base = normal(rng, 4, 3001)
+    for t in (1e-45, 1e-30, 1e-3, 1e5, 1e27, 1e30, 3e38, float("inf")):
+        verify(base, None, 1, 5, 3001, settings(4, rng, temperature=t))
+    tiny = (normal(rng, 4, 3001).float() * 1e-38).to(torch.bfloat16)       # subnormal logits
+    for t in (1e-38, 1.0):
+        verify(tiny, None, 1, 5, 3001, settings(4, rng, temperature=t))
+
+
+@pytest.mark.gpu
+def test_frequencies_follow_the_softmax():
+    """A grid of u over one row reproduces the probabilities to the grid's step."""
+    rng = np.random.default_rng(18)
+    V, rows = 40, 4096
+    x = normal(rng, 1, V, 1.5)
+    s = settings(rows, rng)
+    s["u"] = ((np.arange(rows) + 0.5) / rows).astype(np.float32)
+    ids, _ = draw(x.expand(rows, V).contiguous().cuda(), None, rows, 2, V, s)
+    p = np.exp(x[0].double().numpy())
+    p /= p.sum()
+    assert (np.abs(np.bincount(ids, minlength=V) / rows - p) <= 1.01 / rows).all()
+
+
+@pytest.mark.gpu
+def test_greedy_is_the_argmax_readout():
+    rng = np.random.default_rng(19)
+    N, B, V = 4, 8, 32000
+    base, bias = normal(rng, N * (B - 1), V).cuda(), normal(rng, N * (B - 1), V, 1.0).cuda()
+    blk = torch.zeros(N, B, dtype=torch.int64, device="cuda")
+    native.xpress_add_argmax_to_blk(base, bias, blk, N, B, V, V, V)
+    ids, p = draw(base, bias, N, B, V, settings(N * (B - 1), rng, temperature=0.0))
+    assert np.array_equal(ids, blk[:, 1:].reshape(-1).cpu().numpy()) and (p == 1).all()
+
+
+@pytest.mark.gpu
+def test_misaligned_rows_draw_the_same():
+    rng = np.random.default_rng(20)
+    N, B, V = 2, 4, 5001
+    base, bias = normal(rng, 6, V).cuda(), normal(rng, 6, V, 0.5).cuda()
+    s = settings(6, rng, **FILTERS["p"])
+    want = draw(base, bias, N, B, V, s)
+    for off, stride in ((1, V + 2), (8, 5008)):
+        wide = [torch.full((6 * stride + 16,), 100.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        views = [w[off:off + 6 * stride].view(6, stride) for w in wide]
+        for v, x in zip(views, (base, bias)):
+            v[:, :V] = x
+        got = draw(views[0], views[1], N, B, V, s)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_without_probabilities_and_in_a_graph():
+    rng = np.random.default_rng(21)
+    N, B, V = 2, 4, 20000
+    base = normal(rng, 6, V).cuda()
+    s = settings(6, rng, **FILTERS["k_p_min"])
+    want, _ = draw(base, None, N, B, V, s, prob=False)
+    dev = {k: torch.from_numpy(v).cuda() for k, v in s.items()}
+    blk = torch.zeros(N, B, dtype=torch.int64, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        native.xpress_sample_to_blk(base, None, blk, dev["temperature"], dev["top_k"], dev["top_p"],
+                                    dev["min_p"], dev["u"], N, B, V, V)
+    for _ in range(3):
+        blk.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)

@@ -13,6 +13,9 @@ ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", "xpress_argmax.hip"),
         os.path.join(PKG, "csrc", "readout_gemm.hip"),
         os.path.join(PKG, "csrc", "latent.hip"),
+        os.path.join(PKG, "csrc", "kv_append.hip"),
+        os.path.join(PKG, "csrc", "paged_attention.hip"),
+        os.path.join(PKG, "csrc", "sample.hip"),
         os.path.join(PKG, "csrc", "read_probe.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libxpress_argmax.so")

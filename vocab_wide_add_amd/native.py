@@ -11,7 +11,9 @@ built, the first call raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +34,10 @@ XPRESS_COMBINE_BALANCED = 4
 
 COMBINE_NAMES = {XPRESS_COMBINE_SINGLE: "single", XPRESS_COMBINE_ATOMIC: "atomic",
                  XPRESS_COMBINE_TWO_PASS: "two_pass", XPRESS_COMBINE_BALANCED: "balanced"}
+
+XPRESS_BF16 = 0
+XPRESS_FP16 = 1
+XPRESS_E4M3 = 2
 
 _lock = threading.Lock()
 _lib = None
@@ -94,6 +100,17 @@ def load():
         lib.xpress_bf16_add_round_table.restype = i32
         lib.xpress_read_probe.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp]
         lib.xpress_read_probe.restype = i32
+        cp = ctypes.c_char_p
+        lib.xpress_kv_append.argtypes = [cp, vp]
+        lib.xpress_kv_append.restype = i32
+        lib.xpress_paged_attention.argtypes = [cp, vp]
+        lib.xpress_paged_attention.restype = i32
+        lib.xpress_paged_attention_reserve.argtypes = [i64] * 7 + [vp]
+        lib.xpress_paged_attention_reserve.restype = i32
+        lib.xpress_paged_attention_plan.argtypes = [i64] * 7 + [ip, ip, ip, ip]
+        lib.xpress_paged_attention_plan.restype = i32
+        lib.xpress_sample_to_blk.argtypes = [vp] * 9 + [i64] * 5 + [vp]
+        lib.xpress_sample_to_blk.restype = i32
         lib.xpress_last_hip_error.argtypes = []
         lib.xpress_last_hip_error.restype = i32
         lib.xpress_error_string.argtypes = [i32]
@@ -348,6 +365,192 @@ def xpress_read_probe(base, bias, rows: int, V: int, stride: int, mode: int, sin
     _check(load().xpress_read_probe(_ptr(base), _ptr(bias), int(rows), int(V), int(stride),
                                     int(mode), _ptr(sink), _stream(stream)),
            "xpress_read_probe")
+
+
+# ---------------------------------------------------------------------------
+# Serving operators.  The two over the paged cache take tensors only: sizes,
+# strides and types come from them.  Their C argument structs are 8-byte
+# fields throughout, packed here in declaration order.
+# ---------------------------------------------------------------------------
+
+_KV_CACHE = "5Q11q"
+_APPEND_ARGS = struct.Struct(_KV_CACHE + "7Q14q")
+_ATTENTION_ARGS = struct.Struct(_KV_CACHE + "4Q5qd6q")
+_types = {}
+
+
+def _dtype(t, what: str) -> int:
+    if not _types:
+        import torch
+        _types.update({torch.bfloat16: XPRESS_BF16, torch.float16: XPRESS_FP16,
+                       torch.float8_e4m3fn: XPRESS_E4M3})
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        raise ValueError("%s: bf16, fp16 or float8_e4m3fn expected, got %s" % (what, t.dtype)) from None
+
+
+def _plain(t, what: str, dtype: str, shape, like) -> int:
+    """Address of a contiguous tensor of the named type and shape on like's
+    device (0 for None)."""
+    if t is None:
+        return 0
+    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s expected, got %s of shape %s"
+                         % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    return _at(t, what, like)
+
+
+def _at(t, what: str, like) -> int:
+    if not t.is_cuda or t.get_device() != like.get_device():
+        raise ValueError("%s: expected a tensor on %s, got one on %s"
+                         % (what, like.device if like.is_cuda else "a GPU", t.device))
+    return t.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale):
+    """The fields of xpress_kv_cache from [pages, heads, page_size, dim] caches
+    (any strides with unit stride along dim) and an int32 [seqs, width] table."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype \
+            or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache, v_cache: [pages, heads, page_size, dim], one type, shape and "
+                         "stride expected")
+    pages, heads, size, dim = k_cache.shape
+    sp, sh, st, sd = k_cache.stride()
+    if sd != 1 and dim > 1:
+        raise ValueError("k_cache, v_cache: unit stride along dim expected")
+    if page_table.dim() != 2 or str(page_table.dtype) != "torch.int32" or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: int32 [seqs, width] with unit stride along width expected")
+    dtype = _dtype(k_cache, "k_cache")
+    seqs, width = page_table.shape
+    return (_at(k_cache, "k_cache", k_cache), _at(v_cache, "v_cache", k_cache),
+            _plain(k_scale, "k_scale", "torch.float32", (heads,), k_cache),
+            _plain(v_scale, "v_scale", "torch.float32", (heads,), k_cache),
+            _at(page_table, "page_table", k_cache), pages, size, heads, dim, sp, sh, st, dtype,
+            seqs, width, page_table.stride(0))
+
+
+def _rows(t, what: str, shape, dtype: int, like):
+    """(address, strides but the last) of a tensor with unit stride along its
+    last dimension and the given shape and type."""
+    if tuple(t.shape) != shape or _dtype(t, what) != dtype:
+        raise ValueError("%s: shape %s and q's type expected, got %s of %s"
+                         % (what, shape, tuple(t.shape), t.dtype))
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError("%s: unit stride along its last dimension expected" % what)
+    return _at(t, what, like), st[:-1]
+
+
+def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin,
+                     seq_of=None, k_scale=None, v_scale=None, interleaved: bool = False,
+                     stream=None) -> None:
+    """Rotate the keys of T new tokens to their positions and append them and
+    their values to the paged cache; write the rotated queries to q_out.
+
+    q, q_out [T, Hq, dim] (None, None: keys and values only), k, v [T, heads,
+    dim] bf16 or fp16; k_cache, v_cache [pages, heads, page_size, dim] of that
+    type or float8_e4m3fn (any strides, unit along dim); page_table int32
+    [seqs, width]; positions int32 [T]; cos_sin fp32 [max_pos, rot_dim]
+    (cosines, then sines; None: no rotation); seq_of int32 [T] (None: T / seqs
+    tokens of each sequence in order); k_scale, v_scale fp32 [heads].  See the
+    header for the definition.
+    """
+    T, heads, dim = k.shape
+    cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    if cache[7:9] != (heads, dim):
+        raise ValueError("k: [T, %d, %d] expected for this cache, got %s"
+                         % (cache[7], cache[8], tuple(k.shape)))
+    dtype = _dtype(k, "k")
+    kp, (kt, kh) = _rows(k, "k", (T, heads, dim), dtype, k_cache)
+    vp, (vt, vh) = _rows(v, "v", (T, heads, dim), dtype, k_cache)
+    if q is None:
+        hq, qp, qt, qh, op, ot, oh = 0, 0, 0, 0, 0, 0, 0
+    else:
+        hq = q.shape[1]
+        qp, (qt, qh) = _rows(q, "q", (T, hq, dim), dtype, k_cache)
+        op, (ot, oh) = _rows(q_out, "q_out", (T, hq, dim), dtype, k_cache)
+    if cos_sin is None:
+        cp, max_pos, rot = 0, 2 ** 31 - 1, 0
+    else:
+        max_pos, rot = cos_sin.shape
+        cp = _plain(cos_sin, "cos_sin", "torch.float32", (max_pos, rot), k_cache)
+    args = _APPEND_ARGS.pack(
+        *cache, qp, kp, vp, op, _plain(positions, "positions", "torch.int32", (T,), k_cache),
+        _plain(seq_of, "seq_of", "torch.int32", (T,), k_cache), cp, T, hq, dtype, rot, max_pos,
+        1 if interleaved else 0, qt, qh, kt, kh, vt, vh, ot, oh)
+    _check(load().xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
+
+
+def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: int, lse=None,
+                           scale: float = None, window: int = 0, k_scale=None, v_scale=None,
+                           stream=None) -> None:
+    """Attention of the Q newest tokens of each sequence over its paged cache.
+
+    q, out [N, Q, Hq, dim] bf16 or fp16 (any strides, unit along dim); caches,
+    page_table [N, width] and scales as for xpress_kv_append; lens int32 [N],
+    the sequences' lengths with the new tokens; max_len, their upper bound;
+    lse fp32 [N, Q, Hq] or None; scale, 1 / sqrt(dim) if None; window, the
+    keys a query sees back from itself (0: all).  See the header for the
+    definition.
+    """
+    N, Q, hq, dim = q.shape
+    cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    if cache[8] != dim or cache[13] != N:
+        raise ValueError("q: [%d, Q, Hq, %d] expected for this cache and page table, got %s"
+                         % (cache[13], cache[8], tuple(q.shape)))
+    dtype = _dtype(q, "q")
+    qp, qs = _rows(q, "q", (N, Q, hq, dim), dtype, k_cache)
+    op, os_ = _rows(out, "out", (N, Q, hq, dim), dtype, k_cache)
+    args = _ATTENTION_ARGS.pack(
+        *cache, qp, op, _plain(lse, "lse", "torch.float32", (N, Q, hq), k_cache),
+        _plain(lens, "lens", "torch.int32", (N,), k_cache), Q, hq, dtype, int(max_len),
+        int(window), 1.0 / math.sqrt(dim) if scale is None else float(scale), *qs, *os_)
+    _check(load().xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
+
+
+def xpress_paged_attention_reserve(N: int, Q: int, Hq: int, heads: int, dim: int, max_len: int,
+                                   window: int = 0, stream=None) -> None:
+    _check(load().xpress_paged_attention_reserve(int(N), int(Q), int(Hq), int(heads), int(dim),
+                                                 int(max_len), int(window), _stream(stream)),
+           "xpress_paged_attention_reserve")
+
+
+def xpress_paged_attention_plan(N: int, Q: int, Hq: int, heads: int, dim: int, max_len: int,
+                                window: int = 0) -> dict:
+    """The launch such a call would make (host only): keys of a part, parts of
+    the longest sequence, rows of a workgroup, launches."""
+    out = [ctypes.c_int(0) for _ in range(4)]
+    _check(load().xpress_paged_attention_plan(int(N), int(Q), int(Hq), int(heads), int(dim),
+                                              int(max_len), int(window),
+                                              *[ctypes.byref(o) for o in out]),
+           "xpress_paged_attention_plan")
+    return dict(zip(("chunk", "splits", "rows", "launches"), [o.value for o in out]))
+
+
+def xpress_sample_to_blk(base, bias, blk, temperature, top_k, top_p, min_p, u, N: int, B: int,
+                         V: int, stride_base_r: int, stride_bias_r: int = 0, prob=None,
+                         stream=None) -> None:
+    """blk[n, 1+b] = a token drawn from softmax(bf16(base + bias) / temperature)
+    of row r = n*(B-1) + b, cut by top_k, top_p and min_p, with the uniform
+    number u[r]; prob[r], its probability.  bias may be None.  temperature,
+    top_p, min_p, u, prob fp32 and top_k int32, one per row.
+    """
+    rows = int(N) * (int(B) - 1)
+    if rows > 0:
+        _span(base, ((rows - 1) * int(stride_base_r) + int(V)) * 2, "base")
+        if bias is not None:
+            _span(bias, ((rows - 1) * int(stride_bias_r) + int(V)) * 2, "bias")
+        _span(blk, int(N) * int(B) * 8, "blk")
+        for t, what in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"),
+                        (min_p, "min_p"), (u, "u"), (prob, "prob")):
+            _span(t, rows * 4, what)
+    _check(load().xpress_sample_to_blk(_ptr(base), _ptr(bias), _ptr(blk), _ptr(prob),
+                                       _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                                       _ptr(u), int(N), int(B), int(V), int(stride_base_r),
+                                       int(stride_bias_r), _stream(stream)),
+           "xpress_sample_to_blk")
 
 
 def xpress_last_hip_error() -> int:
