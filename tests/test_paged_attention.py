@@ -110,6 +110,29 @@ def test_against_64_bits(case, dtype, cache):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Q,heads", [(1, (4, 1)), (16, (8, 2))])
+def test_long_context_is_split_and_joined(Q, heads):
+    lens = [20011, 4097]
+    args, _ = made(40, lens, Q, *heads, 128, 64)
+    q, kc, vc, table, lens_t = args
+    plan = native.xpress_paged_attention_plan(2, Q, *heads, 128, 20011)
+    assert plan["splits"] > 1 and plan["launches"] == 2
+    # the reference is slow per query: look at the first and last one only
+    some = q[:, [0, Q - 1]] if Q > 1 else q
+    out, lse = call(up(q), up(kc), up(vc), up(table), up(lens_t), 20011)
+    torch.cuda.synchronize()
+    for i, at in enumerate([0, Q - 1] if Q > 1 else [0]):
+        want, want_lse, A, R = ref.attention64(some[:, i:i + 1], kc, vc, table,
+                                               [x - (Q - 1 - at) for x in lens], 20011,
+                                               float(np.float32(1 / math.sqrt(128))))
+        e = 132 * 2.0 ** -24 * R + 4 * 2.0 ** -24 + 3 * R * 2.0 ** -24 + (20011 / 32 + 40) * 2.0 ** -24
+        tol = 2.0 ** -8 * np.abs(want) + 2 * (e + 2.0 ** -16)[..., None] * A
+        assert (np.abs(out[:, at:at + 1].double().cpu().numpy() - want) <= tol * (1 + 2.0 ** -8)).all()
+        assert (np.abs(lse[:, at:at + 1].double().cpu().numpy() - want_lse) <= 2 * e +
+                2.0 ** -22 * np.abs(want_lse)).all()
+
+
+@pytest.mark.gpu
 def test_scores_far_apart_and_all_alike():
     """Scores of +-hundreds (weights underflow, the maximum comes late) and keys
     that are all the same (flat weights)."""

@@ -136,6 +136,9 @@ def test_plan_and_reserve_check_their_sizes():
     assert p["launches"] in (1, 2) and p["splits"] * p["chunk"] >= 4096
     assert native.xpress_paged_attention_plan(0, 1, 32, 8, 128, 4096)["launches"] == 0
     assert native.xpress_paged_attention_plan(1, 1, 8, 8, 64, 1)["launches"] == 1
+    # a window bounds what is planned for
+    w = native.xpress_paged_attention_plan(1, 1, 8, 8, 64, 100000, 100)
+    assert w["splits"] * w["chunk"] < 1000
     for bad in ((-1, 1, 8, 8, 64, 10), (1, -1, 8, 8, 64, 10), (1, 1, 8, 3, 64, 10), (1, 1, 0, 8, 64, 10),
                 (1, 1, 8, 8, 60, 10), (1, 1, 8, 8, 512, 10), (1, 1, 8, 8, 64, 0), (1, 1, 8, 8, 64, 10, -1)):
         with pytest.raises(native.XpressError):

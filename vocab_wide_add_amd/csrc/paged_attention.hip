@@ -1,10 +1,48 @@
 // paged_attention.hip -- attention of the newest tokens of every sequence
-// over a paged key-value cache (gfx950).
+// over a paged key-value cache (gfx950, wave64, MFMA).
 //
-// Simple form: one workgroup per (sequence, query, head).  Keys go by in
-// tiles of one per thread; the running maximum and sum of the softmax are
-// carried in fp32 from tile to tile, and each thread accumulates one output
-// element.
+// The Q new queries of a sequence and the G query heads of a key-value head
+// are Q * G rows that read the same keys: the cache goes by once for all of
+// them.  A workgroup (four waves) takes up to 16 * MT rows of one (sequence,
+// key-value head) and one part of the keys; its waves take 32-key tiles in
+// turn.  Per tile, with lane l = 16 g + c:
+//
+//   S^T = K Q^T   v_mfma_f32_16x16x32: A = keys (lane: key c, 8 dims of the
+//                 contraction), B = queries (lane: row c).  The lane gets the
+//                 scores of row c with keys 4 g + i of each 16-key half, so a
+//                 row's softmax state lives in the four lanes with its c.
+//   softmax       the running maximum m is only moved when a score passes it
+//                 by more than kRise (in base 2), so most tiles need neither a
+//                 cross-lane reduction nor a rescaling of the sums; weights
+//                 2^(s - m) then reach 2^kRise, which fp32 sums hold as well.
+//   O^T += V^T P  P^T is already in B's layout: slot 8 g + e of the contraction
+//                 is key 4 g + e of the first half (e < 4) or 4 g + e - 4 of
+//                 the second.  A = V^T: the lane reads eight dims 8 c .. 8 c + 7
+//                 of its eight keys (whole rows, 16 bytes a lane) and
+//                 transposes the 8 x 8 block in registers; dim 8 c + j is row c
+//                 of the j-th product.  No LDS round trip for K, V or P.
+//
+// Weights enter the product as two 16-bit parts (rounded weight, rounded
+// rest), 16 bits or more in all: with one part their rounding adds as much
+// error as the output's own, and the second product costs nothing that the
+// cache's bytes do not hide.  Scores, m, the sum l and O are fp32.  An fp16
+// weight is scaled by 2^kLift so that weights down to 2^-25 of the largest
+// stay normal numbers.
+//
+// Each key's place in the pool is worked out once per workgroup, into LDS
+// (one division by the page size per key, any page size).  A key on a missing
+// page, or past the part's end, has place -1: its score is masked and its
+// value row taken as zeros.
+//
+// A value that is not finite must not reach rows that do not see it, though 0
+// times it is NaN.  The product above does not care; a wave whose sums come
+// out non-finite runs its tiles again in a careful form, query by query, with
+// the value rows which that query does not see set to zero.
+//
+// The waves' sums meet in LDS.  A sequence of one part is written out
+// directly; with more parts (chosen on the host from the number of rows'
+// owners and the longest length, see plan_of) the parts' (m, l, O) go to the
+// workspace and a second kernel joins them in a fixed order.
 
 #include <hip/hip_runtime.h>
 
@@ -20,104 +58,612 @@ namespace {
 
 using namespace xpress;
 
-constexpr int kThreads = 256;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * 64;
+constexpr int kTile = 32;        // keys of one tile
+constexpr int kRound = kTile * kWaves;
+constexpr int kMaxChunk = 2048;  // keys of one part
+constexpr float kNone = -INFINITY;
 
 struct AttnArgs {
     const uint16_t* q;
     uint16_t* out;
     float* lse;
+    float* part;      // [rows of all, splits, D], then (m, l) [rows of all, splits]
+    float2* part_ml;
     const int32_t *lens, *page_table;
-    const void *kc, *vc;
+    const char *kc, *vc;
     const float *k_scale, *v_scale;
     int64_t q_n, q_i, q_h, o_n, o_i, o_h;
-    int64_t page, head, token, table;
+    int64_t page, head, token, table;  // cache strides in bytes; page table row stride
     uint32_t N, Q, Hq, Hk, G, D, pages, page_size;
+    uint32_t rows, groups, units, chunk, splits;
     int32_t max_len, window;
-    float scale;
+    float scale;      // times log2(e)
+    uint32_t wide;    // q and out rows are 16-byte aligned
 };
 
+// The keys that any query of a sequence sees, [lo, hi), and its parts.
+struct Keys {
+    int32_t len, lo, hi;
+    uint32_t parts;
+};
+
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, uint32_t n)
+{
+    Keys k;
+    k.len = a.lens[n];
+    k.len = k.len < 0 ? 0 : k.len > a.max_len ? a.max_len : k.len;
+    const int64_t lo = (int64_t)k.len - a.Q - a.window + 1;
+    k.lo = a.window > 0 && lo > 0 ? (int32_t)lo : 0;
+    k.hi = k.len;
+    k.parts = (uint32_t)(k.hi - k.lo + (int32_t)a.chunk - 1) / a.chunk;
+    return k;
+}
+
+// 16-bit arithmetic of the two query types.
 template <bool FP16>
-__device__ __forceinline__ float widen(uint16_t h)
-{
-    if constexpr (FP16) return (float)__builtin_bit_cast(_Float16, h);
-    return __uint_as_float((uint32_t)h << 16);
-}
-
-template <bool FP16, bool E4M3>
-__device__ __forceinline__ float element(const void* p, int64_t at)
-{
-    if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)p)[at], 0);
-    return widen<FP16>(((const uint16_t*)p)[at]);
-}
-
-__device__ __forceinline__ float block_reduce(float v, bool sum, float* tmp)
-{
-    for (int m = 32; m; m >>= 1) {
-        const float o = __shfl_xor(v, m);
-        v = sum ? v + o : fmaxf(v, o);
+struct Half {
+    using Vec = bf16x8;
+    static constexpr float kRise = 8.0f, kLift = 0.0f;
+    static __device__ __forceinline__ f32x4 mfma(u32x4 x, u32x4 y, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(Vec, x),
+                                                       __builtin_bit_cast(Vec, y), c, 0, 0, 0);
     }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x / 64] = v;
-    __syncthreads();
-    v = tmp[0];
-    for (int w = 1; w < kThreads / 64; ++w) v = sum ? v + tmp[w] : fmaxf(v, tmp[w]);
-    return v;
+    static __device__ __forceinline__ uint32_t pack(float x, float y)
+    {
+        f32x2 v = {x, y};
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
+    static constexpr uint32_t kExp = 0x7F807F80u;  // exponent bits of both
+    template <bool HIGH>
+    static __device__ __forceinline__ uint32_t from8(uint32_t w)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+    }
+};
+
+template <>
+struct Half<true> {
+    using Vec = f16x8;
+    static constexpr float kRise = 4.0f, kLift = 11.0f;
+    static __device__ __forceinline__ f32x4 mfma(u32x4 x, u32x4 y, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(Vec, x),
+                                                      __builtin_bit_cast(Vec, y), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y)
+    {
+        f16x2 v = {(_Float16)x, (_Float16)y};
+        return __builtin_bit_cast(uint32_t, v);
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w).x; }
+    static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w).y; }
+    static constexpr uint32_t kExp = 0x7C007C00u;
+    template <bool HIGH>
+    static __device__ __forceinline__ uint32_t from8(uint32_t w)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
+    }
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The four lanes of a row (same l % 16).
+__device__ __forceinline__ float row_max(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
 }
 
-template <bool FP16, bool E4M3>
-__global__ void __launch_bounds__(kThreads) attention_simple_kernel(AttnArgs a)
+__device__ __forceinline__ float row_sum(float v)
 {
-    __shared__ float sq[256], sp[kThreads], tmp[4];
-    __shared__ int64_t so[kThreads];
-    const uint32_t row = blockIdx.x;
-    const uint32_t h = row % a.Hq, i = row / a.Hq % a.Q, n = row / a.Hq / a.Q;
-    const uint32_t hk = h / a.G, tid = threadIdx.x;
-    int32_t len = a.lens[n];
-    len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
-    const int32_t pos = len - (int32_t)a.Q + (int32_t)i;
-    const int32_t lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-    if (tid < a.D) sq[tid] = widen<FP16>(a.q[n * a.q_n + i * a.q_i + h * a.q_h + tid]);
-    const float ks = a.scale * (a.k_scale ? a.k_scale[hk] : 1.0f);
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int32_t j0 = lo; j0 <= pos; j0 += kThreads) {
-        __syncthreads();
-        const int32_t j = j0 + (int32_t)tid;
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+template <bool FP16, bool E4M3, int DP, int MT>
+struct Tile {
+    static constexpr int kDims = DP / 32;              // products of the scores
+    static constexpr int kOuts = DP / 16;              // products of the output
+    static constexpr int kLoads = E4M3 ? DP / 64 : DP / 32;  // 16-byte loads of a key row per lane
+    static constexpr int kBlocks = DP > 128 ? DP / 128 : 1;
+    static constexpr int kEach = kOuts / kBlocks;      // dims of a value row per lane and block
+    static constexpr int kWords = E4M3 ? kEach / 4 : kEach / 2;
+    using H = Half<FP16>;
+    template <int W> struct Words { uint32_t w[W]; };
+
+    const AttnArgs& a;
+    const int64_t* place;   // LDS: byte offsets of the part's keys, -1: none
+    const char *kbase, *vbase;
+    uint32_t c, g;
+    u32x4 q[MT][kDims];
+    u32x4 k[2][kLoads];
+    Words<kWords> v[8][kBlocks];
+    f32x4 o[MT][kOuts];
+    float m[MT], l[MT];
+    int32_t pos[MT];        // position of the lane's row's query; INT32_MIN: no row
+    float scale;
+
+    // First of the eight dims that lane group g supplies to product i.
+    __device__ __forceinline__ uint32_t dim_of(int i) const
+    {
+        return E4M3 ? (uint32_t)(i / 2) * 64 + g * 16 + (uint32_t)(i % 2) * 8 : (uint32_t)i * 32 + g * 8;
+    }
+
+    __device__ __forceinline__ void load_keys(uint32_t t)
+    {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int64_t at = place[t + s * 16 + c];
+            const char* p = kbase + (at < 0 ? 0 : at);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint32_t d = E4M3 ? (uint32_t)i * 64 + g * 16 : (uint32_t)i * 32 + g * 8;
+                const uint32_t b = d < a.D ? d * (E4M3 ? 1 : 2) : 0;
+                k[s][i] = *reinterpret_cast<const u32x4*>(p + b);
+            }
+        }
+    }
+
+    __device__ __forceinline__ uint32_t key_of(int e) const { return (uint32_t)(e / 4) * 16 + g * 4 + e % 4; }
+
+    __device__ __forceinline__ void load_values(uint32_t t)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t at = place[t + key_of(e)];
+            const char* p = vbase + (at < 0 ? 0 : at);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const uint32_t d = (uint32_t)b * 128 + c * kEach;
+                v[e][b] = *reinterpret_cast<const Words<kWords>*>(p + (d < a.D ? d * (E4M3 ? 1 : 2) : 0));
+            }
+        }
+    }
+
+    // Dims past the head's end were loads of its first ones: zeros instead.
+    __device__ __forceinline__ void trim_keys()
+    {
+        if (a.D == DP) return;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if ((uint32_t)i * (E4M3 ? 64 : 32) + g * (E4M3 ? 16 : 8) >= a.D) k[0][i] = k[1][i] = u32x4{0, 0, 0, 0};
+        }
+    }
+
+    __device__ __forceinline__ u32x4 key_part(int s, int i) const
+    {
+        u32x4 x;
+        if constexpr (E4M3) {
+            const uint32_t w0 = k[s][i / 2][(i % 2) * 2], w1 = k[s][i / 2][(i % 2) * 2 + 1];
+            x = u32x4{H::template from8<false>(w0), H::template from8<true>(w0),
+                      H::template from8<false>(w1), H::template from8<true>(w1)};
+        } else {
+            x = k[s][i];
+        }
+        return x;
+    }
+
+    // A operands of output products (j, j + 1): dims 2 of the lane's, 8 keys.
+    __device__ __forceinline__ void value_parts(int j, u32x4* even, u32x4* odd) const
+    {
+        const int b = j / kEach, w = j % kEach;
+        uint32_t x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (E4M3) {
+                const uint32_t y = v[e][b].w[w / 4];
+                x[e] = (w / 2) % 2 ? H::template from8<true>(y) : H::template from8<false>(y);
+            } else {
+                x[e] = v[e][b].w[w / 2];
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            (*even)[p] = __builtin_amdgcn_perm(x[2 * p + 1], x[2 * p], 0x05040100u);
+            (*odd)[p] = __builtin_amdgcn_perm(x[2 * p + 1], x[2 * p], 0x07060302u);
+        }
+    }
+
+    __device__ __forceinline__ bool sees(int mt, int32_t key) const
+    {
+        return key <= pos[mt] && (a.window == 0 || (int64_t)key > (int64_t)pos[mt] - a.window);
+    }
+
+    // Scores and weights of one tile: P as two 16-bit parts.
+    template <bool MASKED>
+    __device__ __forceinline__ void weigh(int mt, uint32_t t, int32_t key0, u32x4* big, u32x4* rest)
+    {
+        f32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) {
+            s0 = H::mfma(key_part(0, i), q[mt][i], s0);
+            s1 = H::mfma(key_part(1, i), q[mt][i], s1);
+        }
+        float s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s[e] = (e < 4 ? s0[e] : s1[e - 4]) * scale;
+            if constexpr (MASKED) {
+                const bool on = place[t + key_of(e)] >= 0 && sees(mt, key0 + (int32_t)(t + key_of(e)));
+                s[e] = on ? s[e] : kNone;
+            }
+        }
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+        if (__any(top > m[mt] + H::kRise)) {
+            const float to = fmaxf(m[mt], row_max(top));
+            const float f = to == m[mt] ? 1.0f : exp2_fast(m[mt] - to);
+            m[mt] = to;
+            l[mt] *= f;
+#pragma unroll
+            for (int j = 0; j < kOuts; ++j) o[mt][j] *= f;
+        }
+        const float from = (m[mt] == kNone ? 0.0f : m[mt]) - H::kLift;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float x = exp2_fast(s[2 * p] - from), y = exp2_fast(s[2 * p + 1] - from);
+            l[mt] += x + y;
+            const uint32_t w = H::pack(x, y);
+            (*big)[p] = w;
+            (*rest)[p] = H::pack(x - H::lo(w), y - H::hi(w));
+        }
+    }
+
+    __device__ __forceinline__ void reset()
+    {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            m[mt] = kNone;
+            l[mt] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kOuts; ++j) o[mt][j] = f32x4{0, 0, 0, 0};
+        }
+    }
+
+    // Value rows that are not there become zeros.
+    __device__ __forceinline__ void drop_missing(uint32_t t)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (place[t + key_of(e)] < 0) {
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) v[e][b].w[w] = 0;
+            }
+        }
+    }
+
+    template <bool MASKED>
+    __device__ __forceinline__ void tile(uint32_t t, uint32_t next, uint32_t end, int32_t key0)
+    {
+        u32x4 big[MT], rest[MT];
+        trim_keys();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) weigh<MASKED>(mt, t, key0, &big[mt], &rest[mt]);
+        if (next < end) load_keys(next);
+        if constexpr (MASKED) drop_missing(t);
+#pragma unroll
+        for (int j = 0; j < kOuts; j += 2) {
+            u32x4 even, odd;
+            value_parts(j, &even, &odd);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                o[mt][j] = H::mfma(even, big[mt], o[mt][j]);
+                o[mt][j + 1] = H::mfma(odd, big[mt], o[mt][j + 1]);
+                o[mt][j] = H::mfma(even, rest[mt], o[mt][j]);
+                o[mt][j + 1] = H::mfma(odd, rest[mt], o[mt][j + 1]);
+            }
+        }
+        if (next < end) load_values(next);
+    }
+
+    // The careful form of a tile (see the top of the file): positions
+    // [first, last] of the workgroup's queries one after the other.
+    __device__ __forceinline__ void tile_careful(uint32_t t, int32_t key0, int32_t first, int32_t last)
+    {
+        load_keys(t);
+        trim_keys();
+        u32x4 big[MT], rest[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) weigh<true>(mt, t, key0, &big[mt], &rest[mt]);
+        for (int32_t at = first; at <= last; ++at) {
+            load_values(t);
+            drop_missing(t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int32_t key = key0 + (int32_t)(t + key_of(e));
+                if (key > at || (a.window > 0 && (int64_t)key <= (int64_t)at - a.window)) {
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w) v[e][b].w[w] = 0;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kOuts; j += 2) {
+                u32x4 x[2];
+                value_parts(j, &x[0], &x[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // the weights' second part meets finite values only
+                    u32x4 y;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t z = x[h][w];
+                        y[w] = ((z & H::kExp & 0xFFFFu) == (H::kExp & 0xFFFFu) ? 0 : z & 0xFFFFu) |
+                               ((z & H::kExp & 0xFFFF0000u) == (H::kExp & 0xFFFF0000u) ? 0 : z & 0xFFFF0000u);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        f32x4 r = H::mfma(x[h], big[mt], f32x4{0, 0, 0, 0});
+                        r = H::mfma(y, rest[mt], r);
+                        if (pos[mt] == at) o[mt][j + h] += r;
+                    }
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ bool finite() const
+    {
+        bool ok = true;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < kOuts; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ok &= __builtin_fabsf(o[mt][j][i]) < INFINITY;
+        return ok;
+    }
+};
+
+// Rows of 16 fp32 sums of a wave, padded against bank conflicts.
+template <int DP>
+constexpr int row_stride() { return DP + 4; }
+
+// One row's result: 8 dims from its sums over the waves.
+__device__ __forceinline__ void store8(const AttnArgs& a, bool fp16, uint16_t* dst, const float* y)
+{
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = fp16 ? Half<true>::pack(y[2 * i], y[2 * i + 1]) : Half<false>::pack(y[2 * i], y[2 * i + 1]);
+    }
+    if (a.wide) {
+        *reinterpret_cast<u32x4*>(dst) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+template <bool FP16, bool E4M3, int DP, int MT>
+__global__ void __launch_bounds__(kThreads, MT >= 4 || DP == 256 ? 1 : 2) attention_kernel(AttnArgs a)
+{
+    using T = Tile<FP16, E4M3, DP, MT>;
+    using H = Half<FP16>;
+    constexpr int kRow = row_stride<DP>();
+    __shared__ int64_t place[kMaxChunk];
+    __shared__ float sums[kWaves][16][kRow];
+    __shared__ float sm[kWaves][16 * MT], sl[kWaves][16 * MT];
+    __shared__ uint32_t holes;
+
+    // Workgroup i runs on XCD i % 8: the row groups that read the same keys
+    // follow each other on one XCD.
+    const uint32_t id = blockIdx.x;
+    const uint32_t unit = id / (8 * a.groups) * 8 + id % 8, group = id / 8 % a.groups;
+    if (unit >= a.units) return;
+    const uint32_t owner = unit % (a.N * a.Hk), split = unit / (a.N * a.Hk);
+    const uint32_t n = owner / a.Hk, hk = owner % a.Hk;
+    const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
+    const Keys keys = keys_of(a, n);
+    if (split > 0 && split >= keys.parts) return;
+    const int32_t key0 = keys.lo + (int32_t)(split * a.chunk);
+    const uint32_t count = (uint32_t)min(keys.hi - key0, (int32_t)a.chunk);  // 0: an empty sequence
+    const uint32_t row0 = group * (16 * MT);
+
+    // places of the part's keys
+    if (tid == 0) holes = 0;
+    __syncthreads();
+    const uint32_t padded = (count + kTile - 1) / kTile * kTile;
+    for (uint32_t j = tid; j < padded; j += kThreads) {
         int64_t at = -1;
-        if (j <= pos) {
-            const uint32_t slot = (uint32_t)j / a.page_size;
+        if (j < count) {
+            const uint32_t key = (uint32_t)key0 + j, slot = key / a.page_size;
             const uint32_t page = (uint32_t)a.page_table[(int64_t)n * a.table + slot];
             if (page < a.pages) {
-                at = (int64_t)page * a.page + (int64_t)((uint32_t)j - slot * a.page_size) * a.token +
-                     (int64_t)hk * a.head;
+                at = (int64_t)page * a.page + (int64_t)(key - slot * a.page_size) * a.token;
+            } else {
+                holes = 1;
             }
         }
-        float s = -INFINITY;
-        if (at >= 0) {
-            s = 0.0f;
-            for (uint32_t d = 0; d < a.D; ++d) s += sq[d] * element<FP16, E4M3>(a.kc, at + d);
-            s *= ks;
+        place[j] = at;
+    }
+
+    T t{a, place, a.kc + hk * a.head, a.vc + hk * a.head, lane & 15, lane / 16};
+    t.scale = a.scale * (a.k_scale ? a.k_scale[hk] : 1.0f);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const uint32_t r = row0 + mt * 16 + t.c;
+        const bool on = r < a.rows;
+        const uint32_t i = on ? r / a.G : 0, h = hk * a.G + (on ? r - i * a.G : 0);
+        t.pos[mt] = on ? keys.len - (int32_t)a.Q + (int32_t)i : INT32_MIN;
+        const uint16_t* src = a.q + n * a.q_n + i * a.q_i + h * a.q_h;
+#pragma unroll
+        for (int x = 0; x < T::kDims; ++x) {
+            const uint32_t d = t.dim_of(x);
+            u32x4 w = {0, 0, 0, 0};
+            if (on && d < a.D) {
+                if (a.wide) {
+                    w = *reinterpret_cast<const u32x4*>(src + d);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = src[d + 2 * e] | (uint32_t)src[d + 2 * e + 1] << 16;
+                }
+            }
+            t.q[mt][x] = w;
         }
-        const float mt = fmaxf(m, block_reduce(s, false, tmp));
-        const float base = mt == -INFINITY ? 0.0f : mt;
-        const float p = at >= 0 ? expf(s - base) : 0.0f;
-        sp[tid] = p;
-        so[tid] = at;
-        const float f = m == -INFINITY ? 0.0f : expf(m - base);
-        l = l * f + block_reduce(p, true, tmp);
-        m = mt;
-        if (tid < a.D) {
-            o *= f;
-            for (int32_t t = 0; t < kThreads && j0 + t <= pos; ++t) {
-                if (so[t] >= 0) o += sp[t] * element<FP16, E4M3>(a.vc, so[t] + tid);
+    }
+    t.reset();
+    __syncthreads();
+
+    // positions of the workgroup's first and last query
+    const uint32_t last_row = min(row0 + 16 * MT, a.rows) - 1;
+    const int32_t first = keys.len - (int32_t)a.Q + (int32_t)(row0 / a.G);
+    const int32_t last = keys.len - (int32_t)a.Q + (int32_t)(last_row / a.G);
+    const uint32_t begin = wave * kTile;
+    if (begin < padded) {
+        const bool whole = holes == 0;
+        t.load_keys(begin);
+        t.load_values(begin);
+        for (uint32_t at = begin; at < padded; at += kRound) {
+            const int32_t k0 = key0 + (int32_t)at;
+            // every row sees every key of the tile
+            const bool all = whole && at + kTile <= count && k0 + kTile - 1 <= first &&
+                             (a.window == 0 || (int64_t)k0 > (int64_t)last - a.window);
+            if (all) {
+                t.template tile<false>(at, at + kRound, padded, key0);
+            } else {
+                t.template tile<true>(at, at + kRound, padded, key0);
+            }
+        }
+        if (__any(!t.finite())) {
+            t.reset();
+            for (uint32_t at = begin; at < padded; at += kRound) t.tile_careful(at, key0, first, last);
+        }
+    }
+
+    // the waves' statistics, then their sums, 16 rows at a time
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        t.l[mt] = row_sum(t.l[mt]);
+        if (lane < 16) {
+            sm[wave][mt * 16 + lane] = t.m[mt];
+            sl[wave][mt * 16 + lane] = t.l[mt];
+        }
+    }
+    const bool direct = keys.parts <= 1;
+    const float vs = a.v_scale ? a.v_scale[hk] : 1.0f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        __syncthreads();
+        float top = kNone;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][mt * 16 + t.c]);
+        const float f = t.m[mt] == top ? 1.0f : exp2_fast(t.m[mt] - top);
+#pragma unroll
+        for (int b = 0; b < T::kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < T::kEach; ++j) {
+                    sums[wave][t.c][b * 128 + (t.g * 4 + i) * T::kEach + j] =
+                        t.o[mt][b * T::kEach + j][i] * f;
+                }
+        __syncthreads();
+        constexpr int kPieces = DP / 8;   // of a row
+        for (uint32_t x = tid; x < 16 * kPieces; x += kThreads) {
+            const uint32_t lr = x / kPieces, d = x % kPieces * 8, r = row0 + mt * 16 + lr;
+            if (r >= a.rows || d >= a.D) continue;
+            float hi = kNone, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) hi = fmaxf(hi, sm[w][mt * 16 + lr]);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float mw = sm[w][mt * 16 + lr];
+                sum += sl[w][mt * 16 + lr] * (mw == hi ? 1.0f : exp2_fast(mw - hi));
+            }
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = sums[0][lr][d + e];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) y[e] += sums[w][lr][d + e];
+            }
+            const uint32_t i = r / a.G, h = hk * a.G + (r - i * a.G);
+            if (direct) {
+                const float inv = sum == 0.0f ? 0.0f : vs / sum;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] * inv;
+                store8(a, FP16, a.out + n * a.o_n + i * a.o_i + h * a.o_h + d, y);
+                if (d == 0 && a.lse) {
+                    a.lse[((int64_t)n * a.Q + i) * a.Hq + h] =
+                        sum == 0.0f ? kNone : (hi - H::kLift + log2f(sum)) * 0.693147180559945309f;
+                }
+            } else {
+                const int64_t at = ((int64_t)owner * a.rows + r) * a.splits + split;
+                f32x4* dst = reinterpret_cast<f32x4*>(a.part + at * a.D + d);
+                dst[0] = f32x4{y[0], y[1], y[2], y[3]};
+                dst[1] = f32x4{y[4], y[5], y[6], y[7]};
+                if (d == 0) a.part_ml[at] = float2{hi, sum};
             }
         }
     }
-    if (tid < a.D) {
-        float y = l == 0.0f ? 0.0f : o / l * (a.v_scale ? a.v_scale[hk] : 1.0f);
-        a.out[n * a.o_n + i * a.o_i + h * a.o_h + tid] =
-            FP16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : __builtin_bit_cast(uint16_t, (__bf16)y);
+}
+
+// Joins the parts of rows that have several: TPR threads a row, a lane per
+// four dims, the parts dealt to TPR / (D / 4) lane groups in order.
+template <bool FP16, int TPR>
+__global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
+{
+    constexpr int kRows = 256 / TPR;
+    __shared__ f32x4 so[256];
+    __shared__ float sl[256];
+    const uint32_t sub = threadIdx.x / TPR, tid = threadIdx.x % TPR;
+    const uint32_t all = blockIdx.x * kRows + sub;   // (owner, row)
+    const uint32_t lanes = a.D / 4, groups = TPR / lanes;
+    const uint32_t d = tid % lanes * 4, grp = tid / lanes;
+    const uint32_t owner = all / a.rows, r = all - owner * a.rows;
+    const uint32_t n = owner / a.Hk, hk = owner - n * a.Hk;
+    const bool on = owner < a.N * a.Hk;
+    const uint32_t parts = on ? keys_of(a, n).parts : 0;
+    const int64_t at = (int64_t)all * a.splits;
+    f32x4 y = {0, 0, 0, 0};
+    float l = 0.0f, top = kNone;
+    if (parts > 1) {
+        for (uint32_t s = 0; s < parts; ++s) top = fmaxf(top, a.part_ml[at + s].x);
+        if (grp < groups) {
+            for (uint32_t s = grp; s < parts; s += groups) {
+                const float2 ml = a.part_ml[at + s];
+                const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+                l += ml.y * f;
+                y += *reinterpret_cast<const f32x4*>(a.part + (at + s) * a.D + d) * f;
+            }
+        }
     }
-    if (tid == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m + logf(l);
+    so[threadIdx.x] = y;
+    sl[threadIdx.x] = l;
+    __syncthreads();
+    if (parts <= 1 || tid >= lanes) return;
+    for (uint32_t x = 1; x < groups; ++x) {
+        y += so[threadIdx.x + x * lanes];
+        l += sl[threadIdx.x + x * lanes];
+    }
+    const uint32_t i = r / a.G, h = hk * a.G + (r - i * a.G);
+    const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[hk] : 1.0f) / l;
+    uint16_t* dst = a.out + n * a.o_n + i * a.o_i + h * a.o_h + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float z = l == 0.0f ? 0.0f : y[e] * inv;
+        dst[e] = (uint16_t)Half<FP16>::pack(z, 0.0f);
+    }
+    if (d == 0 && a.lse) {
+        a.lse[((int64_t)n * a.Q + i) * a.Hq + h] =
+            l == 0.0f ? kNone : (top - Half<FP16>::kLift + log2f(l)) * 0.693147180559945309f;
+    }
 }
 
 struct Shape {
@@ -131,6 +677,90 @@ bool shape_ok(const Shape& s)
            s.Hq <= 65536 && s.Hq % s.heads == 0 && s.dim >= 8 && s.dim <= 256 && s.dim % 8 == 0 &&
            s.max_len >= 1 && s.max_len <= most && s.window >= 0 && s.window <= most &&
            (s.N == 0 || s.Q == 0 || s.Q <= most / s.Hq / s.N);
+}
+
+struct Plan {
+    int mt;                        // 16-row tiles of a workgroup
+    int64_t rows, groups, chunk, splits, units;
+};
+
+// Rows: as many 16-row tiles per workgroup as hold them, up to 4 (2 at 256
+// dims, whose sums fill the registers), so that a block of queries reads the
+// cache once.  Parts: enough workgroups to fill the chip several times over
+// (kTarget), each with whole rounds of its four waves; never more than
+// kMaxChunk keys.
+constexpr int64_t kTarget = 2048;
+
+Plan plan_of(const Shape& s)
+{
+    Plan p;
+    p.rows = s.Q * (s.Hq / s.heads);
+    const int64_t tiles = (p.rows + 15) / 16;
+    p.mt = tiles <= 1 ? 1 : (tiles <= 2 || s.dim > 128) ? 2 : 4;
+    p.groups = (tiles + p.mt - 1) / p.mt;
+    int64_t span = s.max_len;
+    if (s.window > 0 && s.window + s.Q - 1 < span) span = s.window + s.Q - 1;
+    const int64_t owners = s.N * s.heads;
+    const int64_t want = (kTarget + owners * p.groups - 1) / (owners * p.groups);
+    int64_t chunk = (span + want - 1) / want;
+    chunk = (chunk + kRound - 1) / kRound * kRound;
+    p.chunk = chunk > kMaxChunk ? kMaxChunk : chunk;
+    p.splits = (span + p.chunk - 1) / p.chunk;
+    p.units = owners * p.splits;
+    return p;
+}
+
+// Workgroups and part sums in 32 bits.
+bool plan_ok(const Shape& s, const Plan& p)
+{
+    return p.units <= 0x7FFFFFFFll / p.groups / 8;
+}
+
+// Workspace words (8 bytes): sums and (m, l) of every part of every row.
+int64_t plan_words(const Shape& s, const Plan& p)
+{
+    return p.splits > 1 ? s.N * s.Q * s.Hq * p.splits * (s.dim + 2) / 2 : 0;
+}
+
+template <bool FP16, bool E4M3, int DP, int MT>
+void launch_tiles(const AttnArgs& a, hipStream_t stream)
+{
+    const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
+    hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, MT>), dim3(grid), dim3(kThreads), 0, stream, a);
+}
+
+template <bool FP16, bool E4M3, int DP>
+void launch_rows(const AttnArgs& a, int mt, hipStream_t stream)
+{
+    if (mt == 1) return launch_tiles<FP16, E4M3, DP, 1>(a, stream);
+    if constexpr (DP <= 128) {
+        if (mt == 4) return launch_tiles<FP16, E4M3, DP, 4>(a, stream);
+    }
+    return launch_tiles<FP16, E4M3, DP, 2>(a, stream);
+}
+
+template <bool FP16, bool E4M3>
+void launch_dims(const AttnArgs& a, int mt, hipStream_t stream)
+{
+    if (a.D <= 64) return launch_rows<FP16, E4M3, 64>(a, mt, stream);
+    if (a.D <= 128) return launch_rows<FP16, E4M3, 128>(a, mt, stream);
+    return launch_rows<FP16, E4M3, 256>(a, mt, stream);
+}
+
+template <bool FP16>
+hipError_t launch_attention(const AttnArgs& a, bool e4m3, int mt, hipStream_t stream)
+{
+    if (e4m3) launch_dims<FP16, true>(a, mt, stream);
+    else launch_dims<FP16, false>(a, mt, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const uint32_t rows = a.N * a.Hk * a.rows;
+    if (a.splits <= 16) {
+        hipLaunchKernelGGL((join_kernel<FP16, 64>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((join_kernel<FP16, 256>), dim3(rows), dim3(256), 0, stream, a);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -183,14 +813,19 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
         return XPRESS_EINVAL;
     }
 
+    const Plan p = plan_of(s);
+    if (!plan_ok(s, p)) return XPRESS_EINVAL;
+
     AttnArgs a;
     a.q = (const uint16_t*)x.q;
     a.out = (uint16_t*)x.out;
     a.lse = x.lse;
+    a.part = nullptr;
+    a.part_ml = nullptr;
     a.lens = x.lens;
     a.page_table = c.page_table;
-    a.kc = c.k;
-    a.vc = c.v;
+    a.kc = (const char*)c.k;
+    a.vc = (const char*)c.v;
     a.k_scale = c.k_scale;
     a.v_scale = c.v_scale;
     a.q_n = x.stride_q_n;
@@ -199,9 +834,9 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
     a.o_n = x.stride_o_n;
     a.o_i = x.stride_o_i;
     a.o_h = x.stride_o_h;
-    a.page = c.stride_page;
-    a.head = c.stride_head;
-    a.token = c.stride_token;
+    a.page = c.stride_page * e;
+    a.head = c.stride_head * e;
+    a.token = c.stride_token * e;
     a.table = c.stride_table;
     a.N = (uint32_t)s.N;
     a.Q = (uint32_t)s.Q;
@@ -211,21 +846,26 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
     a.D = (uint32_t)s.dim;
     a.pages = (uint32_t)c.pages;
     a.page_size = (uint32_t)c.page_size;
+    a.rows = (uint32_t)p.rows;
+    a.groups = (uint32_t)p.groups;
+    a.units = (uint32_t)p.units;
+    a.chunk = (uint32_t)p.chunk;
+    a.splits = (uint32_t)p.splits;
     a.max_len = (int32_t)x.max_len;
     a.window = (int32_t)x.window;
-    a.scale = (float)x.scale;
-    const dim3 grid((uint32_t)(s.N * s.Q * s.Hq));
-    const bool f16 = x.dtype == XPRESS_FP16, e8 = c.dtype == XPRESS_E4M3;
-    if (f16 && e8) {
-        hipLaunchKernelGGL((attention_simple_kernel<true, true>), grid, dim3(kThreads), 0, stream, a);
-    } else if (f16) {
-        hipLaunchKernelGGL((attention_simple_kernel<true, false>), grid, dim3(kThreads), 0, stream, a);
-    } else if (e8) {
-        hipLaunchKernelGGL((attention_simple_kernel<false, true>), grid, dim3(kThreads), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((attention_simple_kernel<false, false>), grid, dim3(kThreads), 0, stream, a);
+    a.scale = (float)(x.scale * 1.4426950408889634);
+    a.wide = is_aligned16(x.q) && is_aligned16(x.out) &&
+             (x.stride_q_n | x.stride_q_i | x.stride_q_h | x.stride_o_n | x.stride_o_i | x.stride_o_h) % 8 == 0;
+    if (p.splits > 1) {
+        uint64_t* table = nullptr;
+        const int rc = workspace_table(stream, plan_words(s, p), &table);
+        if (rc != XPRESS_OK) return rc;
+        a.part = reinterpret_cast<float*>(table);
+        a.part_ml = reinterpret_cast<float2*>(a.part + s.N * s.Q * s.Hq * p.splits * s.dim);
     }
-    const hipError_t err = hipGetLastError();
+    const hipError_t err = x.dtype == XPRESS_FP16
+                               ? launch_attention<true>(a, c.dtype == XPRESS_E4M3, p.mt, stream)
+                               : launch_attention<false>(a, c.dtype == XPRESS_E4M3, p.mt, stream);
     return err == hipSuccess ? XPRESS_OK : hip_fail(err);
 }
 
@@ -233,8 +873,13 @@ int xpress_paged_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t hea
                                    int64_t max_len, int64_t window, hipStream_t stream)
 {
     const Shape s = {N, Q, Hq, heads, dim, max_len, window};
-    (void)stream;
-    return shape_ok(s) ? XPRESS_OK : XPRESS_EINVAL;
+    if (!shape_ok(s)) return XPRESS_EINVAL;
+    if (N == 0 || Q == 0) return XPRESS_OK;
+    const Plan p = plan_of(s);
+    if (!plan_ok(s, p)) return XPRESS_EINVAL;
+    if (p.splits == 1) return XPRESS_OK;
+    uint64_t* table = nullptr;
+    return workspace_table(stream, plan_words(s, p), &table);
 }
 
 int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads, int64_t dim,
@@ -243,10 +888,15 @@ int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads,
 {
     const Shape s = {N, Q, Hq, heads, dim, max_len, window};
     if (!shape_ok(s)) return XPRESS_EINVAL;
-    if (chunk) *chunk = (int)max_len;
-    if (splits) *splits = 1;
-    if (rows) *rows = 1;
-    if (launches) *launches = (N == 0 || Q == 0) ? 0 : 1;
+    Plan p = {1, 0, 0, 0, 0, 0};
+    if (N > 0 && Q > 0) {
+        p = plan_of(s);
+        if (!plan_ok(s, p)) return XPRESS_EINVAL;
+    }
+    if (chunk) *chunk = (int)p.chunk;
+    if (splits) *splits = (int)p.splits;
+    if (rows) *rows = 16 * p.mt;
+    if (launches) *launches = p.splits > 1 ? 2 : (int)p.splits;
     return XPRESS_OK;
 }
 
