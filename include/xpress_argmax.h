@@ -366,9 +366,9 @@ typedef struct xpress_kv_cache {
  * leave one of them there.  cache.dtype is `dtype` or XPRESS_E4M3.
  *
  * Asynchronous; one launch; no workspace.  T == 0 queues nothing.  Any
- * alignment that suits the element types is accepted; 16-byte aligned rows
- * with rot_dim a multiple of 16 and dim a multiple of 8 take the vector path,
- * with identical results.  XPRESS_EINVAL: a size or type outside the above, a
+ * alignment that suits the element types is accepted; accesses are of 8
+ * elements where dim, the strides and the pointers allow it and rot_dim is a
+ * multiple of 16, of 4 at half of that, else single, with identical results.  XPRESS_EINVAL: a size or type outside the above, a
  * null pointer, a pointer not aligned to its element, a cache or q_out whose
  * elements share addresses, or a cache whose span overlaps q, k, v, q_out or
  * an index array.

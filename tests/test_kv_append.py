@@ -185,3 +185,25 @@ def test_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,rot", [(80, 40), (12, 8), (12, 12), (20, 8), (7, 2), (24, 0), (1, 0), (520, 512)])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_head_sizes_of_every_access_width(D, rot, cache, interleaved):
+    """Pieces of 8, 4 and 1 elements, with and without a half piece at a head's end."""
+    say("append widths %d %d %s %s" % (D, rot, cache, interleaved))
+    rng = np.random.default_rng([D, rot])
+    made = build(rng, [20, 40], [4, 9], 5, 2, D, rot, 16, "bf16", cache)
+    check(*made, 5, 2, D, interleaved)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache,layout", [("bf16", "token"), ("e4m3", "head")])
+def test_prompts_with_more_work_than_threads(cache, layout):
+    """Past the size at which a workgroup takes a whole token."""
+    rng = np.random.default_rng([8, 1])
+    made = build(rng, [700, 1, 901], [700, 1, 901], 32, 8, 128, 32, 16, "bf16", cache, layout)
+    assert sum((700, 1, 901)) * 48 * 8 > 1 << 19
+    check(*made, 32, 8, 128, True)
