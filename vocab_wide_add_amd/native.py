@@ -55,6 +55,8 @@ class XpressError(RuntimeError):
 def load():
     """Load the library (once).  Raises ImportError when it is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -149,8 +151,11 @@ def _span(t, nbytes: int, what: str):
 def _stream(stream):
     """HIP stream handle: None means torch's current stream on the current device."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch or _use_torch()
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        # the same handle, without building the Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -376,71 +381,87 @@ def xpress_read_probe(base, bias, rows: int, V: int, stride: int, mode: int, sin
 _KV_CACHE = "5Q11q"
 _APPEND_ARGS = struct.Struct(_KV_CACHE + "7Q14q")
 _ATTENTION_ARGS = struct.Struct(_KV_CACHE + "4Q5qd6q")
+_torch = None
 _types = {}
 
 
-def _dtype(t, what: str) -> int:
-    if not _types:
+def _use_torch():
+    """torch, imported by the first call that takes tensors only."""
+    global _torch
+    if _torch is None:
         import torch
         _types.update({torch.bfloat16: XPRESS_BF16, torch.float16: XPRESS_FP16,
                        torch.float8_e4m3fn: XPRESS_E4M3})
+        _torch = torch
+    return _torch
+
+
+def _dtype(t, what: str) -> int:
     try:
         return _types[t.dtype]
     except KeyError:
         raise ValueError("%s: bf16, fp16 or float8_e4m3fn expected, got %s" % (what, t.dtype)) from None
 
 
-def _plain(t, what: str, dtype: str, shape, like) -> int:
-    """Address of a contiguous tensor of the named type and shape on like's
-    device (0 for None)."""
+def _plain(t, what: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of the given type and shape on device
+    dev (0 for None)."""
     if t is None:
         return 0
-    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: a contiguous %s tensor of shape %s expected, got %s of shape %s"
                          % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    return _at(t, what, like)
-
-
-def _at(t, what: str, like) -> int:
-    if not t.is_cuda or t.get_device() != like.get_device():
-        raise ValueError("%s: expected a tensor on %s, got one on %s"
-                         % (what, like.device if like.is_cuda else "a GPU", t.device))
+    if t.get_device() != dev:
+        _elsewhere(t, what, dev)
     return t.data_ptr()
 
 
-def _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale):
+def _elsewhere(t, what: str, dev: int):
+    raise ValueError("%s: expected a tensor on %s, got one on %s"
+                     % (what, "a GPU" if dev < 0 else "cuda:%d" % dev, t.device))
+
+
+def _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev: int):
     """The fields of xpress_kv_cache from [pages, heads, page_size, dim] caches
-    (any strides with unit stride along dim) and an int32 [seqs, width] table."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype \
-            or k_cache.stride() != v_cache.stride():
+    (any strides with unit stride along dim) on device dev and an int32
+    [seqs, width] table."""
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype \
+            or v_cache.stride() != strides:
         raise ValueError("k_cache, v_cache: [pages, heads, page_size, dim], one type, shape and "
                          "stride expected")
-    pages, heads, size, dim = k_cache.shape
-    sp, sh, st, sd = k_cache.stride()
+    pages, heads, size, dim = shape
+    sp, sh, st, sd = strides
     if sd != 1 and dim > 1:
         raise ValueError("k_cache, v_cache: unit stride along dim expected")
-    if page_table.dim() != 2 or str(page_table.dtype) != "torch.int32" or (
-            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    table, rows = page_table.shape, page_table.stride()
+    if len(table) != 2 or page_table.dtype is not _torch.int32 or (table[1] > 1 and rows[1] != 1):
         raise ValueError("page_table: int32 [seqs, width] with unit stride along width expected")
-    dtype = _dtype(k_cache, "k_cache")
-    seqs, width = page_table.shape
-    return (_at(k_cache, "k_cache", k_cache), _at(v_cache, "v_cache", k_cache),
-            _plain(k_scale, "k_scale", "torch.float32", (heads,), k_cache),
-            _plain(v_scale, "v_scale", "torch.float32", (heads,), k_cache),
-            _at(page_table, "page_table", k_cache), pages, size, heads, dim, sp, sh, st, dtype,
-            seqs, width, page_table.stride(0))
+    code = _dtype(k_cache, "k_cache")
+    if dev < 0:
+        _elsewhere(k_cache, "k_cache", dev)
+    if v_cache.get_device() != dev:
+        _elsewhere(v_cache, "v_cache", dev)
+    if page_table.get_device() != dev:
+        _elsewhere(page_table, "page_table", dev)
+    f32 = _torch.float32
+    return (k_cache.data_ptr(), v_cache.data_ptr(), _plain(k_scale, "k_scale", f32, (heads,), dev),
+            _plain(v_scale, "v_scale", f32, (heads,), dev), page_table.data_ptr(), pages, size, heads,
+            dim, sp, sh, st, code, table[0], table[1], rows[0])
 
 
-def _rows(t, what: str, shape, dtype: int, like):
-    """(address, strides but the last) of a tensor with unit stride along its
-    last dimension and the given shape and type."""
-    if tuple(t.shape) != shape or _dtype(t, what) != dtype:
-        raise ValueError("%s: shape %s and q's type expected, got %s of %s"
-                         % (what, shape, tuple(t.shape), t.dtype))
+def _rows(t, what: str, shape, dtype, dev: int):
+    """(address, strides) of a tensor with unit stride along its last dimension
+    and the given shape and type."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError("%s: shape %s and type %s expected, got %s of %s"
+                         % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s: unit stride along its last dimension expected" % what)
-    return _at(t, what, like), st[:-1]
+    if t.get_device() != dev:
+        _elsewhere(t, what, dev)
+    return t.data_ptr(), st
 
 
 def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin,
@@ -457,30 +478,32 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
     tokens of each sequence in order); k_scale, v_scale fp32 [heads].  See the
     header for the definition.
     """
-    T, heads, dim = k.shape
-    cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale)
-    if cache[7:9] != (heads, dim):
+    torch = _use_torch()
+    shape, dev = k.shape, k_cache.get_device()
+    T, heads, dim = shape
+    cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
+    if cache[7] != heads or cache[8] != dim:
         raise ValueError("k: [T, %d, %d] expected for this cache, got %s"
-                         % (cache[7], cache[8], tuple(k.shape)))
-    dtype = _dtype(k, "k")
-    kp, (kt, kh) = _rows(k, "k", (T, heads, dim), dtype, k_cache)
-    vp, (vt, vh) = _rows(v, "v", (T, heads, dim), dtype, k_cache)
+                         % (cache[7], cache[8], tuple(shape)))
+    code, dtype, i32 = _dtype(k, "k"), k.dtype, torch.int32
+    kp, (kt, kh, _) = _rows(k, "k", shape, dtype, dev)
+    vp, (vt, vh, _) = _rows(v, "v", shape, dtype, dev)
     if q is None:
         hq, qp, qt, qh, op, ot, oh = 0, 0, 0, 0, 0, 0, 0
     else:
         hq = q.shape[1]
-        qp, (qt, qh) = _rows(q, "q", (T, hq, dim), dtype, k_cache)
-        op, (ot, oh) = _rows(q_out, "q_out", (T, hq, dim), dtype, k_cache)
+        qp, (qt, qh, _) = _rows(q, "q", (T, hq, dim), dtype, dev)
+        op, (ot, oh, _) = _rows(q_out, "q_out", (T, hq, dim), dtype, dev)
     if cos_sin is None:
         cp, max_pos, rot = 0, 2 ** 31 - 1, 0
     else:
         max_pos, rot = cos_sin.shape
-        cp = _plain(cos_sin, "cos_sin", "torch.float32", (max_pos, rot), k_cache)
+        cp = _plain(cos_sin, "cos_sin", torch.float32, (max_pos, rot), dev)
     args = _APPEND_ARGS.pack(
-        *cache, qp, kp, vp, op, _plain(positions, "positions", "torch.int32", (T,), k_cache),
-        _plain(seq_of, "seq_of", "torch.int32", (T,), k_cache), cp, T, hq, dtype, rot, max_pos,
+        *cache, qp, kp, vp, op, _plain(positions, "positions", i32, (T,), dev),
+        _plain(seq_of, "seq_of", i32, (T,), dev), cp, T, hq, code, rot, max_pos,
         1 if interleaved else 0, qt, qh, kt, kh, vt, vh, ot, oh)
-    _check(load().xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
+    _check((_lib or load()).xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
 
 
 def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: int, lse=None,
@@ -495,19 +518,21 @@ def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: 
     keys a query sees back from itself (0: all).  See the header for the
     definition.
     """
-    N, Q, hq, dim = q.shape
-    cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    torch = _use_torch()
+    shape, dev = q.shape, k_cache.get_device()
+    N, Q, hq, dim = shape
+    cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
     if cache[8] != dim or cache[13] != N:
         raise ValueError("q: [%d, Q, Hq, %d] expected for this cache and page table, got %s"
-                         % (cache[13], cache[8], tuple(q.shape)))
-    dtype = _dtype(q, "q")
-    qp, qs = _rows(q, "q", (N, Q, hq, dim), dtype, k_cache)
-    op, os_ = _rows(out, "out", (N, Q, hq, dim), dtype, k_cache)
+                         % (cache[13], cache[8], tuple(shape)))
+    code, dtype = _dtype(q, "q"), q.dtype
+    qp, (qn, qi, qh, _) = _rows(q, "q", shape, dtype, dev)
+    op, (on, oi, oh, _) = _rows(out, "out", shape, dtype, dev)
     args = _ATTENTION_ARGS.pack(
-        *cache, qp, op, _plain(lse, "lse", "torch.float32", (N, Q, hq), k_cache),
-        _plain(lens, "lens", "torch.int32", (N,), k_cache), Q, hq, dtype, int(max_len),
-        int(window), 1.0 / math.sqrt(dim) if scale is None else float(scale), *qs, *os_)
-    _check(load().xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
+        *cache, qp, op, _plain(lse, "lse", torch.float32, (N, Q, hq), dev),
+        _plain(lens, "lens", torch.int32, (N,), dev), Q, hq, code, int(max_len), int(window),
+        1.0 / math.sqrt(dim) if scale is None else float(scale), qn, qi, qh, on, oi, oh)
+    _check((_lib or load()).xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
 
 
 def xpress_paged_attention_reserve(N: int, Q: int, Hq: int, heads: int, dim: int, max_len: int,
