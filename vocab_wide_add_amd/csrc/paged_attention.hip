@@ -3,9 +3,12 @@
 //
 // The Q new queries of a sequence and the G query heads of a key-value head
 // are Q * G rows that read the same keys: the cache goes by once for all of
-// them.  A workgroup (four waves) takes up to 16 * MT rows of one (sequence,
-// key-value head) and one part of the keys; its waves take 32-key tiles in
-// turn.  Per tile, with lane l = 16 g + c:
+// them.  A workgroup (four waves) takes up to 64 rows of one (sequence,
+// key-value head) and one part of the keys.  Up to 16 rows, its waves take
+// 32-key tiles in turn, straight to registers; more rows are 16 to a wave, and
+// the waves take the tiles from LDS, where they are staged once for all of them
+// (a wave with four times the rows in its registers spilled 1.4 KB a lane: 350
+// us where this form takes 81).  Per tile, with lane l = 16 g + c:
 //
 //   S^T = K Q^T   v_mfma_f32_16x16x32: A = keys (lane: key c, 8 dims of the
 //                 contraction), B = queries (lane: row c).  The lane gets the
@@ -20,7 +23,7 @@
 //                 the second.  A = V^T: the lane reads eight dims 8 c .. 8 c + 7
 //                 of its eight keys (whole rows, 16 bytes a lane) and
 //                 transposes the 8 x 8 block in registers; dim 8 c + j is row c
-//                 of the j-th product.  No LDS round trip for K, V or P.
+//                 of the j-th product.  No LDS round trip for P.
 //
 // Weights enter the product as two 16-bit parts (rounded weight, rounded
 // rest), 16 bits or more in all: with one part their rounding adds as much
@@ -69,6 +72,7 @@ constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 32;        // keys of one tile
 constexpr int kRound = kTile * kWaves;
 constexpr int kMaxChunk = 2048;  // keys of one part
+constexpr int kMaxChunkStaged = 1024;  // the same where LDS also holds the keys
 constexpr float kNone = -INFINITY;
 
 struct AttnArgs {
@@ -171,7 +175,52 @@ __device__ __forceinline__ float row_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-template <bool FP16, bool E4M3, int DP, int MT>
+// Keys of a part in LDS, for workgroups of several row waves: kStage rows of
+// keys and of values, copied there as they are in the pool, 16 bytes a lane.
+// A piece of a key row goes to place piece ^ turn(row), so that the sixteen
+// rows which a quarter wave reads at one piece lie in different banks; value
+// rows, read whole, change places within four so that the four quarters do.
+constexpr int kStage = 64;
+
+template <bool E4M3, int DP>
+struct Stage {
+    static constexpr uint32_t kRow = DP * (E4M3 ? 1 : 2);  // bytes
+    static constexpr uint32_t kPieces = kRow / 16;
+    static constexpr uint32_t kBytes = kStage * kRow;
+    static constexpr uint32_t kCopies = kStage * kPieces / kThreads;  // of a thread, keys or values
+
+    static __device__ __forceinline__ uint32_t turn(uint32_t row)
+    {
+        return kPieces >= 16 ? row & 15 : row / (16 / kPieces) & (kPieces - 1);
+    }
+    static __device__ __forceinline__ uint32_t slot(uint32_t row)
+    {
+        return kRow >= 256 ? row : row ^ (row >> 2 & (256 / kRow - 1));
+    }
+
+    // Queues the copies of keys [t, t + kStage); the same number in every wave.
+    static __device__ __forceinline__ void copy(const AttnArgs& a, const int64_t* place, uint32_t t,
+                                                const char* kbase, const char* vbase, const char* lds)
+    {
+        const uint32_t wave = threadIdx.x / 64, used = a.D * (E4M3 ? 1 : 2);
+#pragma unroll
+        for (uint32_t x = 0; x < kCopies; ++x) {
+            const uint32_t at = x * kThreads + threadIdx.x, row = at / kPieces, piece = at % kPieces;
+            const uint32_t kd = (piece ^ turn(row)) * 16, vd = piece * 16;
+            const int64_t kp = place[t + row], vp = place[t + slot(row)];
+            // rows that are not there and pieces past the head's end: any bytes
+            // of the pool, masked or dropped after
+            const char* ks = kbase + (kp < 0 ? 0 : kp) + (kd < used ? kd : 0);
+            const char* vs = vbase + (vp < 0 ? 0 : vp) + (vd < used ? vd : 0);
+            const char* to = lds + (x * kThreads + wave * 64) * 16;
+            dma16(reinterpret_cast<const uint16_t*>(ks), lds_addr(reinterpret_cast<const uint16_t*>(to)));
+            dma16(reinterpret_cast<const uint16_t*>(vs),
+                  lds_addr(reinterpret_cast<const uint16_t*>(to + kBytes)));
+        }
+    }
+};
+
+template <bool FP16, bool E4M3, int DP>
 struct Tile {
     static constexpr int kDims = DP / 32;              // products of the scores
     static constexpr int kOuts = DP / 16;              // products of the output
@@ -186,12 +235,12 @@ struct Tile {
     const int64_t* place;   // LDS: byte offsets of the part's keys, -1: none
     const char *kbase, *vbase;
     uint32_t c, g;
-    u32x4 q[MT][kDims];
+    u32x4 q[kDims];
     u32x4 k[2][kLoads];
     Words<kWords> v[8][kBlocks];
-    f32x4 o[MT][kOuts];
-    float m[MT], l[MT];
-    int32_t pos[MT];        // position of the lane's row's query; INT32_MIN: no row
+    f32x4 o[kOuts];
+    float m, l;
+    int32_t pos;            // position of the lane's row's query; INT32_MIN: no row
     float scale;
 
     // First of the eight dims that lane group g supplies to product i.
@@ -275,46 +324,46 @@ struct Tile {
         }
     }
 
-    __device__ __forceinline__ bool sees(int mt, int32_t key) const
+    __device__ __forceinline__ bool sees(int32_t key) const
     {
-        return key <= pos[mt] && (a.window == 0 || (int64_t)key > (int64_t)pos[mt] - a.window);
+        return key <= pos && (a.window == 0 || (int64_t)key > (int64_t)pos - a.window);
     }
 
     // Scores and weights of one tile: P as two 16-bit parts.
     template <bool MASKED>
-    __device__ __forceinline__ void weigh(int mt, uint32_t t, int32_t key0, u32x4* big, u32x4* rest)
+    __device__ __forceinline__ void weigh(uint32_t t, int32_t key0, u32x4* big, u32x4* rest)
     {
         f32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < kDims; ++i) {
-            s0 = H::mfma(key_part(0, i), q[mt][i], s0);
-            s1 = H::mfma(key_part(1, i), q[mt][i], s1);
+            s0 = H::mfma(key_part(0, i), q[i], s0);
+            s1 = H::mfma(key_part(1, i), q[i], s1);
         }
         float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             s[e] = (e < 4 ? s0[e] : s1[e - 4]) * scale;
             if constexpr (MASKED) {
-                const bool on = place[t + key_of(e)] >= 0 && sees(mt, key0 + (int32_t)(t + key_of(e)));
+                const bool on = place[t + key_of(e)] >= 0 && sees(key0 + (int32_t)(t + key_of(e)));
                 s[e] = on ? s[e] : kNone;
             }
         }
         float top = s[0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
-        if (__any(top > m[mt] + H::kRise)) {
-            const float to = fmaxf(m[mt], row_max(top));
-            const float f = to == m[mt] ? 1.0f : exp2_fast(m[mt] - to);
-            m[mt] = to;
-            l[mt] *= f;
+        if (__any(top > m + H::kRise)) {
+            const float to = fmaxf(m, row_max(top));
+            const float f = to == m ? 1.0f : exp2_fast(m - to);
+            m = to;
+            l *= f;
 #pragma unroll
-            for (int j = 0; j < kOuts; ++j) o[mt][j] *= f;
+            for (int j = 0; j < kOuts; ++j) o[j] *= f;
         }
-        const float from = (m[mt] == kNone ? 0.0f : m[mt]) - H::kLift;
+        const float from = (m == kNone ? 0.0f : m) - H::kLift;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const float x = exp2_fast(s[2 * p] - from), y = exp2_fast(s[2 * p + 1] - from);
-            l[mt] += x + y;
+            l += x + y;
             const uint32_t w = H::pack(x, y);
             (*big)[p] = w;
             (*rest)[p] = H::pack(x - H::lo(w), y - H::hi(w));
@@ -323,13 +372,10 @@ struct Tile {
 
     __device__ __forceinline__ void reset()
     {
+        m = kNone;
+        l = 0.0f;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            m[mt] = kNone;
-            l[mt] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kOuts; ++j) o[mt][j] = f32x4{0, 0, 0, 0};
-        }
+        for (int j = 0; j < kOuts; ++j) o[j] = f32x4{0, 0, 0, 0};
     }
 
     // Value rows that are not there become zeros.
@@ -346,28 +392,58 @@ struct Tile {
         }
     }
 
-    template <bool MASKED>
-    __device__ __forceinline__ void tile(uint32_t t, uint32_t next, uint32_t end, int32_t key0)
+    // The output products of one tile, whose values are in v.
+    __device__ __forceinline__ void gather(u32x4 big, u32x4 rest)
     {
-        u32x4 big[MT], rest[MT];
-        trim_keys();
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) weigh<MASKED>(mt, t, key0, &big[mt], &rest[mt]);
-        if (next < end) load_keys(next);
-        if constexpr (MASKED) drop_missing(t);
 #pragma unroll
         for (int j = 0; j < kOuts; j += 2) {
             u32x4 even, odd;
             value_parts(j, &even, &odd);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                o[mt][j] = H::mfma(even, big[mt], o[mt][j]);
-                o[mt][j + 1] = H::mfma(odd, big[mt], o[mt][j + 1]);
-                o[mt][j] = H::mfma(even, rest[mt], o[mt][j]);
-                o[mt][j + 1] = H::mfma(odd, rest[mt], o[mt][j + 1]);
-            }
+            o[j] = H::mfma(even, big, o[j]);
+            o[j + 1] = H::mfma(odd, big, o[j + 1]);
+            o[j] = H::mfma(even, rest, o[j]);
+            o[j + 1] = H::mfma(odd, rest, o[j + 1]);
         }
+    }
+
+    // One tile from the registers; the loads of the wave's next one follow as
+    // soon as the registers are free.
+    template <bool MASKED>
+    __device__ __forceinline__ void tile(uint32_t t, uint32_t next, uint32_t end, int32_t key0)
+    {
+        u32x4 big, rest;
+        trim_keys();
+        weigh<MASKED>(t, key0, &big, &rest);
+        if (next < end) load_keys(next);
+        if constexpr (MASKED) drop_missing(t);
+        gather(big, rest);
         if (next < end) load_values(next);
+    }
+
+    // One tile from LDS (see Stage).
+    template <bool MASKED>
+    __device__ __forceinline__ void tile_staged(const char* ks, const char* vs, uint32_t t, int32_t key0)
+    {
+        using S = Stage<E4M3, DP>;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                k[s][i] = *reinterpret_cast<const u32x4*>(
+                    ks + (s * 16 + c) * S::kRow + (((uint32_t)i * 4 + g) ^ S::turn(c)) * 16);
+            }
+        trim_keys();
+        u32x4 big, rest;
+        weigh<MASKED>(t, key0, &big, &rest);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                v[e][b] = *reinterpret_cast<const Words<kWords>*>(
+                    vs + S::slot(key_of(e)) * S::kRow + (b * 128 + c * kEach) * (E4M3 ? 1 : 2));
+            }
+        if constexpr (MASKED) drop_missing(t);
+        gather(big, rest);
     }
 
     // The careful form of a tile (see the top of the file): positions
@@ -376,9 +452,8 @@ struct Tile {
     {
         load_keys(t);
         trim_keys();
-        u32x4 big[MT], rest[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) weigh<true>(mt, t, key0, &big[mt], &rest[mt]);
+        u32x4 big, rest;
+        weigh<true>(t, key0, &big, &rest);
         for (int32_t at = first; at <= last; ++at) {
             load_values(t);
             drop_missing(t);
@@ -406,12 +481,9 @@ struct Tile {
                         y[w] = ((z & H::kExp & 0xFFFFu) == (H::kExp & 0xFFFFu) ? 0 : z & 0xFFFFu) |
                                ((z & H::kExp & 0xFFFF0000u) == (H::kExp & 0xFFFF0000u) ? 0 : z & 0xFFFF0000u);
                     }
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        f32x4 r = H::mfma(x[h], big[mt], f32x4{0, 0, 0, 0});
-                        r = H::mfma(y, rest[mt], r);
-                        if (pos[mt] == at) o[mt][j + h] += r;
-                    }
+                    f32x4 r = H::mfma(x[h], big, f32x4{0, 0, 0, 0});
+                    r = H::mfma(y, rest, r);
+                    if (pos == at) o[j + h] += r;
                 }
             }
         }
@@ -421,11 +493,9 @@ struct Tile {
     {
         bool ok = true;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int j = 0; j < kOuts; ++j)
 #pragma unroll
-            for (int j = 0; j < kOuts; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ok &= __builtin_fabsf(o[mt][j][i]) < INFINITY;
+            for (int i = 0; i < 4; ++i) ok &= __builtin_fabsf(o[j][i]) < INFINITY;
         return ok;
     }
 };
@@ -450,16 +520,24 @@ __device__ __forceinline__ void store8(const AttnArgs& a, bool fp16, uint16_t* d
     }
 }
 
-template <bool FP16, bool E4M3, int DP, int MT>
-__global__ void __launch_bounds__(kThreads, MT >= 4 || DP == 256 ? 1 : 2) attention_kernel(AttnArgs a)
+// RW waves of the workgroup hold 16 rows each, KW = kWaves / RW waves share a
+// row's keys.  RW = 1: each wave loads its own tiles to registers, one tile
+// ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.
+template <bool FP16, bool E4M3, int DP, int RW>
+__global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a)
 {
-    using T = Tile<FP16, E4M3, DP, MT>;
+    using T = Tile<FP16, E4M3, DP>;
+    using S = Stage<E4M3, DP>;
     using H = Half<FP16>;
+    constexpr int KW = kWaves / RW;
     constexpr int kRow = row_stride<DP>();
-    __shared__ int64_t place[kMaxChunk];
-    __shared__ float sums[kWaves][16][kRow];
-    __shared__ float sm[kWaves][16 * MT], sl[kWaves][16 * MT];
+    constexpr int kSums = kWaves * 16 * kRow * 4, kStages = RW > 1 ? 4 * S::kBytes : 0;
+    __shared__ int64_t place[RW > 1 ? kMaxChunkStaged : kMaxChunk];
+    // the stages, then the waves' sums
+    __shared__ __align__(16) char pool[kSums > kStages ? kSums : kStages];
+    __shared__ float sm[kWaves][16], sl[kWaves][16];
     __shared__ uint32_t holes;
+    float(*sums)[16][kRow] = reinterpret_cast<float(*)[16][kRow]>(pool);
 
     // Workgroup i runs on XCD i % 8: the row groups that read the same keys
     // follow each other on one XCD.
@@ -469,16 +547,18 @@ __global__ void __launch_bounds__(kThreads, MT >= 4 || DP == 256 ? 1 : 2) attent
     const uint32_t owner = unit % (a.N * a.Hk), split = unit / (a.N * a.Hk);
     const uint32_t n = owner / a.Hk, hk = owner % a.Hk;
     const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
+    const uint32_t rw = wave % RW, kw = wave / RW;
     const Keys keys = keys_of(a, n);
     if (split > 0 && split >= keys.parts) return;
     const int32_t key0 = keys.lo + (int32_t)(split * a.chunk);
     const uint32_t count = (uint32_t)min(keys.hi - key0, (int32_t)a.chunk);  // 0: an empty sequence
-    const uint32_t row0 = group * (16 * MT);
+    const uint32_t row0 = group * (16 * RW);
 
     // places of the part's keys
     if (tid == 0) holes = 0;
     __syncthreads();
-    const uint32_t padded = (count + kTile - 1) / kTile * kTile;
+    constexpr uint32_t kPad = RW > 1 ? kStage : kTile;
+    const uint32_t padded = (count + kPad - 1) / kPad * kPad;
     for (uint32_t j = tid; j < padded; j += kThreads) {
         int64_t at = -1;
         if (j < count) {
@@ -495,12 +575,11 @@ __global__ void __launch_bounds__(kThreads, MT >= 4 || DP == 256 ? 1 : 2) attent
 
     T t{a, place, a.kc + hk * a.head, a.vc + hk * a.head, lane & 15, lane / 16};
     t.scale = a.scale * (a.k_scale ? a.k_scale[hk] : 1.0f);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t r = row0 + mt * 16 + t.c;
+    {
+        const uint32_t r = row0 + rw * 16 + t.c;
         const bool on = r < a.rows;
         const uint32_t i = on ? r / a.G : 0, h = hk * a.G + (on ? r - i * a.G : 0);
-        t.pos[mt] = on ? keys.len - (int32_t)a.Q + (int32_t)i : INT32_MIN;
+        t.pos = on ? keys.len - (int32_t)a.Q + (int32_t)i : INT32_MIN;
         const uint16_t* src = a.q + n * a.q_n + i * a.q_i + h * a.q_h;
 #pragma unroll
         for (int x = 0; x < T::kDims; ++x) {
@@ -514,102 +593,121 @@ __global__ void __launch_bounds__(kThreads, MT >= 4 || DP == 256 ? 1 : 2) attent
                     for (int e = 0; e < 4; ++e) w[e] = src[d + 2 * e] | (uint32_t)src[d + 2 * e + 1] << 16;
                 }
             }
-            t.q[mt][x] = w;
+            t.q[x] = w;
         }
     }
     t.reset();
     __syncthreads();
 
-    // positions of the workgroup's first and last query
-    const uint32_t last_row = min(row0 + 16 * MT, a.rows) - 1;
-    const int32_t first = keys.len - (int32_t)a.Q + (int32_t)(row0 / a.G);
+    // positions of the wave's first and last query; a wave may have no rows
+    const uint32_t first_row = row0 + rw * 16, last_row = min(first_row + 16, a.rows) - 1;
+    const bool some = first_row < a.rows;
+    const int32_t first = keys.len - (int32_t)a.Q + (int32_t)(first_row / a.G);
     const int32_t last = keys.len - (int32_t)a.Q + (int32_t)(last_row / a.G);
-    const uint32_t begin = wave * kTile;
-    if (begin < padded) {
-        const bool whole = holes == 0;
-        t.load_keys(begin);
-        t.load_values(begin);
-        for (uint32_t at = begin; at < padded; at += kRound) {
-            const int32_t k0 = key0 + (int32_t)at;
-            // every row sees every key of the tile
-            const bool all = whole && at + kTile <= count && k0 + kTile - 1 <= first &&
-                             (a.window == 0 || (int64_t)k0 > (int64_t)last - a.window);
-            if (all) {
-                t.template tile<false>(at, at + kRound, padded, key0);
-            } else {
-                t.template tile<true>(at, at + kRound, padded, key0);
+    const bool whole = holes == 0;
+    // every row sees every key of the tile at t
+    auto all_seen = [&](uint32_t at) {
+        const int32_t k0 = key0 + (int32_t)at;
+        return whole && at + kTile <= count && k0 + kTile - 1 <= first &&
+               (a.window == 0 || (int64_t)k0 > (int64_t)last - a.window);
+    };
+    if constexpr (RW == 1) {
+        const uint32_t begin = kw * kTile;
+        if (begin < padded) {
+            t.load_keys(begin);
+            t.load_values(begin);
+            for (uint32_t at = begin; at < padded; at += kRound) {
+                if (all_seen(at)) t.template tile<false>(at, at + kRound, padded, key0);
+                else t.template tile<true>(at, at + kRound, padded, key0);
             }
         }
-        if (__any(!t.finite())) {
-            t.reset();
-            for (uint32_t at = begin; at < padded; at += kRound) t.tile_careful(at, key0, first, last);
+    } else {
+        if (padded > 0) S::copy(a, place, 0, t.kbase, t.vbase, pool);
+        for (uint32_t at = 0; at < padded; at += kStage) {
+            // this stage's copies have landed, and every wave is through with
+            // the stage before, whose half the next copies fill
+            wait_vmcnt<0>();
+            __syncthreads();
+            const char* here = pool + at / kStage % 2 * (2 * S::kBytes);
+            if (at + kStage < padded) {
+                S::copy(a, place, at + kStage, t.kbase, t.vbase,
+                        pool + (at / kStage + 1) % 2 * (2 * S::kBytes));
+            }
+            if (!some) continue;
+#pragma unroll
+            for (uint32_t x = 0; x < kStage / kTile / KW; ++x) {
+                const uint32_t off = (x * KW + kw) * kTile;
+                const char *ks = here + off * S::kRow, *vs = ks + S::kBytes;
+                if (all_seen(at + off)) t.template tile_staged<false>(ks, vs, at + off, key0);
+                else t.template tile_staged<true>(ks, vs, at + off, key0);
+            }
         }
+    }
+    if (some && __any(!t.finite())) {
+        t.reset();
+        for (uint32_t at = kw * kTile; at < padded; at += KW * kTile) t.tile_careful(at, key0, first, last);
     }
 
-    // the waves' statistics, then their sums, 16 rows at a time
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        t.l[mt] = row_sum(t.l[mt]);
-        if (lane < 16) {
-            sm[wave][mt * 16 + lane] = t.m[mt];
-            sl[wave][mt * 16 + lane] = t.l[mt];
-        }
+    // the waves' statistics and sums meet in LDS
+    t.l = row_sum(t.l);
+    if (lane < 16) {
+        sm[wave][lane] = t.m;
+        sl[wave][lane] = t.l;
     }
+    __syncthreads();
     const bool direct = keys.parts <= 1;
     const float vs = a.v_scale ? a.v_scale[hk] : 1.0f;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        __syncthreads();
+    {
         float top = kNone;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][mt * 16 + t.c]);
-        const float f = t.m[mt] == top ? 1.0f : exp2_fast(t.m[mt] - top);
+        for (int w = 0; w < KW; ++w) top = fmaxf(top, sm[w * RW + rw][t.c]);
+        const float f = t.m == top ? 1.0f : exp2_fast(t.m - top);
 #pragma unroll
         for (int b = 0; b < T::kBlocks; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < T::kEach; ++j) {
-                    sums[wave][t.c][b * 128 + (t.g * 4 + i) * T::kEach + j] =
-                        t.o[mt][b * T::kEach + j][i] * f;
+                    sums[wave][t.c][b * 128 + (t.g * 4 + i) * T::kEach + j] = t.o[b * T::kEach + j][i] * f;
                 }
-        __syncthreads();
-        constexpr int kPieces = DP / 8;   // of a row
-        for (uint32_t x = tid; x < 16 * kPieces; x += kThreads) {
-            const uint32_t lr = x / kPieces, d = x % kPieces * 8, r = row0 + mt * 16 + lr;
-            if (r >= a.rows || d >= a.D) continue;
-            float hi = kNone, sum = 0.0f;
+    }
+    __syncthreads();
+    constexpr int kPieces = DP / 8;   // of a row
+    for (uint32_t x = tid; x < RW * 16 * kPieces; x += kThreads) {
+        const uint32_t lr = x / kPieces, d = x % kPieces * 8, r = row0 + lr;
+        if (r >= a.rows || d >= a.D) continue;
+        const uint32_t w0 = lr / 16, at16 = lr % 16;
+        float hi = kNone, sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) hi = fmaxf(hi, sm[w][mt * 16 + lr]);
+        for (int w = 0; w < KW; ++w) hi = fmaxf(hi, sm[w * RW + w0][at16]);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float mw = sm[w][mt * 16 + lr];
-                sum += sl[w][mt * 16 + lr] * (mw == hi ? 1.0f : exp2_fast(mw - hi));
+        for (int w = 0; w < KW; ++w) {
+            const float mw = sm[w * RW + w0][at16];
+            sum += sl[w * RW + w0][at16] * (mw == hi ? 1.0f : exp2_fast(mw - hi));
+        }
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            y[e] = sums[w0][at16][d + e];
+#pragma unroll
+            for (int w = 1; w < KW; ++w) y[e] += sums[w * RW + w0][at16][d + e];
+        }
+        const uint32_t i = r / a.G, h = hk * a.G + (r - i * a.G);
+        if (direct) {
+            const float inv = sum == 0.0f ? 0.0f : vs / sum;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] * inv;
+            store8(a, FP16, a.out + n * a.o_n + i * a.o_i + h * a.o_h + d, y);
+            if (d == 0 && a.lse) {
+                a.lse[((int64_t)n * a.Q + i) * a.Hq + h] =
+                    sum == 0.0f ? kNone : (hi - H::kLift + log2f(sum)) * 0.693147180559945309f;
             }
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[e] = sums[0][lr][d + e];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w) y[e] += sums[w][lr][d + e];
-            }
-            const uint32_t i = r / a.G, h = hk * a.G + (r - i * a.G);
-            if (direct) {
-                const float inv = sum == 0.0f ? 0.0f : vs / sum;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] * inv;
-                store8(a, FP16, a.out + n * a.o_n + i * a.o_i + h * a.o_h + d, y);
-                if (d == 0 && a.lse) {
-                    a.lse[((int64_t)n * a.Q + i) * a.Hq + h] =
-                        sum == 0.0f ? kNone : (hi - H::kLift + log2f(sum)) * 0.693147180559945309f;
-                }
-            } else {
-                const int64_t at = ((int64_t)owner * a.rows + r) * a.splits + split;
-                f32x4* dst = reinterpret_cast<f32x4*>(a.part + at * a.D + d);
-                dst[0] = f32x4{y[0], y[1], y[2], y[3]};
-                dst[1] = f32x4{y[4], y[5], y[6], y[7]};
-                if (d == 0) a.part_ml[at] = float2{hi, sum};
-            }
+        } else {
+            const int64_t at = ((int64_t)owner * a.rows + r) * a.splits + split;
+            f32x4* dst = reinterpret_cast<f32x4*>(a.part + at * a.D + d);
+            dst[0] = f32x4{y[0], y[1], y[2], y[3]};
+            dst[1] = f32x4{y[4], y[5], y[6], y[7]};
+            if (d == 0) a.part_ml[at] = float2{hi, sum};
         }
     }
 }
@@ -634,8 +732,20 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
     f32x4 y = {0, 0, 0, 0};
     float l = 0.0f, top = kNone;
     if (parts > 1) {
-        for (uint32_t s = 0; s < parts; ++s) top = fmaxf(top, a.part_ml[at + s].x);
+        for (uint32_t s = tid; s < parts; s += TPR) top = fmaxf(top, a.part_ml[at + s].x);
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+    if constexpr (TPR > 64) {
+        sl[threadIdx.x] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) top = fmaxf(top, sl[w * 64]);
+        __syncthreads();
+    }
+    if (parts > 1) {
         if (grp < groups) {
+#pragma unroll 4
             for (uint32_t s = grp; s < parts; s += groups) {
                 const float2 ml = a.part_ml[at + s];
                 const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
@@ -680,15 +790,15 @@ bool shape_ok(const Shape& s)
 }
 
 struct Plan {
-    int mt;                        // 16-row tiles of a workgroup
+    int rw;                        // waves of 16 rows in a workgroup
     int64_t rows, groups, chunk, splits, units;
 };
 
-// Rows: as many 16-row tiles per workgroup as hold them, up to 4 (2 at 256
-// dims, whose sums fill the registers), so that a block of queries reads the
-// cache once.  Parts: enough workgroups to fill the chip several times over
-// (kTarget), each with whole rounds of its four waves; never more than
-// kMaxChunk keys.
+// Rows: as many waves of 16 as hold them, up to the workgroup's 4, so that a
+// block of queries reads the cache once; more go to further workgroups, which
+// find the keys in their XCD's L2.  Parts: enough workgroups to fill the chip
+// several times over (kTarget), each with whole rounds of its four waves;
+// never more than kMaxChunk keys.
 constexpr int64_t kTarget = 2048;
 
 Plan plan_of(const Shape& s)
@@ -696,15 +806,16 @@ Plan plan_of(const Shape& s)
     Plan p;
     p.rows = s.Q * (s.Hq / s.heads);
     const int64_t tiles = (p.rows + 15) / 16;
-    p.mt = tiles <= 1 ? 1 : (tiles <= 2 || s.dim > 128) ? 2 : 4;
-    p.groups = (tiles + p.mt - 1) / p.mt;
+    p.rw = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;
+    p.groups = (tiles + p.rw - 1) / p.rw;
     int64_t span = s.max_len;
     if (s.window > 0 && s.window + s.Q - 1 < span) span = s.window + s.Q - 1;
     const int64_t owners = s.N * s.heads;
     const int64_t want = (kTarget + owners * p.groups - 1) / (owners * p.groups);
+    const int64_t most = p.rw > 1 ? kMaxChunkStaged : kMaxChunk;
     int64_t chunk = (span + want - 1) / want;
     chunk = (chunk + kRound - 1) / kRound * kRound;
-    p.chunk = chunk > kMaxChunk ? kMaxChunk : chunk;
+    p.chunk = chunk > most ? most : chunk;
     p.splits = (span + p.chunk - 1) / p.chunk;
     p.units = owners * p.splits;
     return p;
@@ -722,36 +833,34 @@ int64_t plan_words(const Shape& s, const Plan& p)
     return p.splits > 1 ? s.N * s.Q * s.Hq * p.splits * (s.dim + 2) / 2 : 0;
 }
 
-template <bool FP16, bool E4M3, int DP, int MT>
-void launch_tiles(const AttnArgs& a, hipStream_t stream)
+template <bool FP16, bool E4M3, int DP, int RW>
+void launch_waves(const AttnArgs& a, hipStream_t stream)
 {
     const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
-    hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, MT>), dim3(grid), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW>), dim3(grid), dim3(kThreads), 0, stream, a);
 }
 
 template <bool FP16, bool E4M3, int DP>
-void launch_rows(const AttnArgs& a, int mt, hipStream_t stream)
+void launch_rows(const AttnArgs& a, int rw, hipStream_t stream)
 {
-    if (mt == 1) return launch_tiles<FP16, E4M3, DP, 1>(a, stream);
-    if constexpr (DP <= 128) {
-        if (mt == 4) return launch_tiles<FP16, E4M3, DP, 4>(a, stream);
-    }
-    return launch_tiles<FP16, E4M3, DP, 2>(a, stream);
+    if (rw == 1) launch_waves<FP16, E4M3, DP, 1>(a, stream);
+    else if (rw == 2) launch_waves<FP16, E4M3, DP, 2>(a, stream);
+    else launch_waves<FP16, E4M3, DP, 4>(a, stream);
 }
 
 template <bool FP16, bool E4M3>
-void launch_dims(const AttnArgs& a, int mt, hipStream_t stream)
+void launch_dims(const AttnArgs& a, int rw, hipStream_t stream)
 {
-    if (a.D <= 64) return launch_rows<FP16, E4M3, 64>(a, mt, stream);
-    if (a.D <= 128) return launch_rows<FP16, E4M3, 128>(a, mt, stream);
-    return launch_rows<FP16, E4M3, 256>(a, mt, stream);
+    if (a.D <= 64) return launch_rows<FP16, E4M3, 64>(a, rw, stream);
+    if (a.D <= 128) return launch_rows<FP16, E4M3, 128>(a, rw, stream);
+    return launch_rows<FP16, E4M3, 256>(a, rw, stream);
 }
 
 template <bool FP16>
-hipError_t launch_attention(const AttnArgs& a, bool e4m3, int mt, hipStream_t stream)
+hipError_t launch_attention(const AttnArgs& a, bool e4m3, int rw, hipStream_t stream)
 {
-    if (e4m3) launch_dims<FP16, true>(a, mt, stream);
-    else launch_dims<FP16, false>(a, mt, stream);
+    if (e4m3) launch_dims<FP16, true>(a, rw, stream);
+    else launch_dims<FP16, false>(a, rw, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const uint32_t rows = a.N * a.Hk * a.rows;
@@ -864,8 +973,8 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
         a.part_ml = reinterpret_cast<float2*>(a.part + s.N * s.Q * s.Hq * p.splits * s.dim);
     }
     const hipError_t err = x.dtype == XPRESS_FP16
-                               ? launch_attention<true>(a, c.dtype == XPRESS_E4M3, p.mt, stream)
-                               : launch_attention<false>(a, c.dtype == XPRESS_E4M3, p.mt, stream);
+                               ? launch_attention<true>(a, c.dtype == XPRESS_E4M3, p.rw, stream)
+                               : launch_attention<false>(a, c.dtype == XPRESS_E4M3, p.rw, stream);
     return err == hipSuccess ? XPRESS_OK : hip_fail(err);
 }
 
@@ -895,7 +1004,7 @@ int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads,
     }
     if (chunk) *chunk = (int)p.chunk;
     if (splits) *splits = (int)p.splits;
-    if (rows) *rows = 16 * p.mt;
+    if (rows) *rows = 16 * p.rw;
     if (launches) *launches = p.splits > 1 ? 2 : (int)p.splits;
     return XPRESS_OK;
 }
