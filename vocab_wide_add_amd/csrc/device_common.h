@@ -162,12 +162,24 @@ __device__ __forceinline__ void wait_vmcnt()
 // wait-count pass does not add a wait for every pending load before each LDS
 // read; the contraction loop waits for exactly the chunk it is about to read
 // (wait_vmcnt), and extra loads the compiler places after these only make
-// its own waits stricter.
+// its own waits stricter.  ONCE: the bytes are read once and pass the caches by.
+template <bool ONCE = false>
 __device__ __forceinline__ void dma16(const uint16_t* gsrc, uint32_t lds_base)
 {
     // M0 is read when the load issues; it is restored right after so that no
     // other use of M0 sees the LDS address
     uint32_t saved;
+    if constexpr (ONCE) {
+        asm volatile(
+            "s_mov_b32 %0, m0\n\t"
+            "s_mov_b32 m0, %2\n\t"
+            "global_load_lds_dwordx4 %1, off nt\n\t"
+            "s_mov_b32 m0, %0"
+            : "=&s"(saved)
+            : "v"(gsrc), "s"(lds_base)
+            : "memory");
+        return;
+    }
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %2\n\t"

@@ -33,9 +33,10 @@
 // stay normal numbers.
 //
 // Each key's place in the pool is worked out once per workgroup, into LDS
-// (one division by the page size per key, any page size).  A key on a missing
-// page, or past the part's end, has place -1: its score is masked and its
-// value row taken as zeros.
+// (one division by the page size per key, any page size), and a bit says
+// whether it exists.  A key on a missing page, or past the part's end, does
+// not: its place is the pool's first row, its score is masked and its value row
+// taken as zeros.
 //
 // A value that is not finite must not reach rows that do not see it, though 0
 // times it is NaN.  The product above does not care; a wave whose sums come
@@ -175,52 +176,77 @@ __device__ __forceinline__ float row_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-// Keys of a part in LDS, for workgroups of several row waves: kStage rows of
-// keys and of values, copied there as they are in the pool, 16 bytes a lane.
-// A piece of a key row goes to place piece ^ turn(row), so that the sixteen
-// rows which a quarter wave reads at one piece lie in different banks; value
-// rows, read whole, change places within four so that the four quarters do.
-constexpr int kStage = 64;
-
+// Cache rows in LDS as they are in the pool.  A piece (16 bytes) of a key row
+// goes to place piece ^ turn(row), so that the sixteen rows which a quarter wave
+// reads at one piece lie in different banks; value rows, read whole, change
+// places within four so that the four quarters do.
 template <bool E4M3, int DP>
-struct Stage {
+struct Lines {
     static constexpr uint32_t kRow = DP * (E4M3 ? 1 : 2);  // bytes
     static constexpr uint32_t kPieces = kRow / 16;
-    static constexpr uint32_t kBytes = kStage * kRow;
-    static constexpr uint32_t kCopies = kStage * kPieces / kThreads;  // of a thread, keys or values
 
     static __device__ __forceinline__ uint32_t turn(uint32_t row)
     {
-        return kPieces >= 16 ? row & 15 : row / (16 / kPieces) & (kPieces - 1);
+        return kPieces >= 16 ? row & 15 : row * kPieces / 16 & (kPieces - 1);
     }
     static __device__ __forceinline__ uint32_t slot(uint32_t row)
     {
         return kRow >= 256 ? row : row ^ (row >> 2 & (256 / kRow - 1));
     }
+};
 
-    // Queues the copies of keys [t, t + kStage); the same number in every wave.
+// Two stages of kKeys keys and values in LDS, for workgroups of several row
+// waves; two such workgroups (one at 256 dims) share a compute unit's LDS.  (Four
+// stages of 32 keys, the same LDS: 104 us where these take 86; the barriers are
+// twice as many.)
+template <bool E4M3, int DP>
+struct Stage : Lines<E4M3, DP> {
+    using L = Lines<E4M3, DP>;
+    static constexpr uint32_t kKeys = 64;
+    static constexpr uint32_t kBytes = kKeys * L::kRow;                  // keys or values
+    static constexpr uint32_t kCopies = kKeys * L::kPieces / kThreads;   // of a thread, keys or values
+
+    // Queues the copies of keys [t, t + kKeys).
+    // ONCE: no other workgroup reads them, so they pass the caches by.
+    template <bool ONCE>
     static __device__ __forceinline__ void copy(const AttnArgs& a, const int64_t* place, uint32_t t,
                                                 const char* kbase, const char* vbase, const char* lds)
     {
         const uint32_t wave = threadIdx.x / 64, used = a.D * (E4M3 ? 1 : 2);
 #pragma unroll
         for (uint32_t x = 0; x < kCopies; ++x) {
-            const uint32_t at = x * kThreads + threadIdx.x, row = at / kPieces, piece = at % kPieces;
-            const uint32_t kd = (piece ^ turn(row)) * 16, vd = piece * 16;
-            const int64_t kp = place[t + row], vp = place[t + slot(row)];
+            const uint32_t at = x * kThreads + threadIdx.x, row = at / L::kPieces, piece = at % L::kPieces;
+            const uint32_t kd = (piece ^ L::turn(row)) * 16, vd = piece * 16;
+            const int64_t kp = place[t + row], vp = place[t + L::slot(row)];
             // rows that are not there and pieces past the head's end: any bytes
             // of the pool, masked or dropped after
-            const char* ks = kbase + (kp < 0 ? 0 : kp) + (kd < used ? kd : 0);
-            const char* vs = vbase + (vp < 0 ? 0 : vp) + (vd < used ? vd : 0);
+            const char* ks = kbase + kp + (kd < used ? kd : 0);
+            const char* vs = vbase + vp + (vd < used ? vd : 0);
             const char* to = lds + (x * kThreads + wave * 64) * 16;
-            dma16(reinterpret_cast<const uint16_t*>(ks), lds_addr(reinterpret_cast<const uint16_t*>(to)));
-            dma16(reinterpret_cast<const uint16_t*>(vs),
-                  lds_addr(reinterpret_cast<const uint16_t*>(to + kBytes)));
+            const uint32_t at_k = lds_addr(reinterpret_cast<const uint16_t*>(to));
+            const uint32_t at_v = lds_addr(reinterpret_cast<const uint16_t*>(to + kBytes));
+            dma16<ONCE>(reinterpret_cast<const uint16_t*>(ks), at_k);
+            dma16<ONCE>(reinterpret_cast<const uint16_t*>(vs), at_v);
         }
     }
 };
 
-template <bool FP16, bool E4M3, int DP>
+// ONCE: the bytes are read once and pass the caches by.
+template <bool ONCE, typename T>
+__device__ __forceinline__ T load(const char* p)
+{
+    if constexpr (!ONCE) {
+        return *reinterpret_cast<const T*>(p);
+    } else if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)));
+    } else if constexpr (sizeof(T) == 8) {
+        return __builtin_bit_cast(T, __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p)));
+    } else {
+        return __builtin_bit_cast(T, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+    }
+}
+
+template <bool FP16, bool E4M3, int DP, int DEEP, bool BOUNCE, bool ONCE>
 struct Tile {
     static constexpr int kDims = DP / 32;              // products of the scores
     static constexpr int kOuts = DP / 16;              // products of the output
@@ -228,16 +254,21 @@ struct Tile {
     static constexpr int kBlocks = DP > 128 ? DP / 128 : 1;
     static constexpr int kEach = kOuts / kBlocks;      // dims of a value row per lane and block
     static constexpr int kWords = E4M3 ? kEach / 4 : kEach / 2;
+    static constexpr int kDeep = DEEP;
+    static constexpr bool kBounce = BOUNCE;
     using H = Half<FP16>;
+    using S = Lines<E4M3, DP>;
     template <int W> struct Words { uint32_t w[W]; };
 
     const AttnArgs& a;
-    const int64_t* place;   // LDS: byte offsets of the part's keys, -1: none
+    const int64_t* place;   // LDS: byte offsets of the part's keys
+    const uint32_t* there;  // LDS: which of a tile's keys exist
     const char *kbase, *vbase;
     uint32_t c, g;
     u32x4 q[kDims];
     u32x4 k[2][kLoads];
-    Words<kWords> v[8][kBlocks];
+    u32x4 k_in[kDeep][2 * kLoads];      // on their way, a slot a tile
+    Words<kWords> v[kDeep][8][kBlocks];
     f32x4 o[kOuts];
     float m, l;
     int32_t pos;            // position of the lane's row's query; INT32_MIN: no row
@@ -249,35 +280,90 @@ struct Tile {
         return E4M3 ? (uint32_t)(i / 2) * 64 + g * 16 + (uint32_t)(i % 2) * 8 : (uint32_t)i * 32 + g * 8;
     }
 
-    __device__ __forceinline__ void load_keys(uint32_t t)
+    __device__ __forceinline__ uint32_t key_of(int e) const { return (uint32_t)(e / 4) * 16 + g * 4 + e % 4; }
+
+    // The tile's key rows, whole rows after each other over the lanes (a load of
+    // 64 bytes of 16 rows each, the product's own layout, reached 4.6 TB/s where
+    // this one reaches 5.4).
+    template <bool PASS>
+    __device__ __forceinline__ void load_rows(u32x4* in, uint32_t t)
+    {
+        const uint32_t used = a.D * (E4M3 ? 1 : 2), lane = g * 16 + c;
+#pragma unroll
+        for (int i = 0; i < 2 * kLoads; ++i) {
+            const uint32_t at = i * 64 + lane, row = at / S::kPieces, d = at % S::kPieces * 16;
+            in[i] = load<PASS, u32x4>(kbase + place[t + row] + (d < used ? d : 0));
+        }
+    }
+
+    // From the registers to the wave's own part of LDS.
+    __device__ __forceinline__ void put(const u32x4* in, char* to)
+    {
+        const uint32_t lane = g * 16 + c;
+#pragma unroll
+        for (int i = 0; i < 2 * kLoads; ++i) {
+            const uint32_t at = i * 64 + lane, row = at / S::kPieces, piece = at % S::kPieces;
+            *reinterpret_cast<u32x4*>(to + row * S::kRow + (piece ^ S::turn(row & 15)) * 16) = in[i];
+        }
+    }
+
+    // The products' operands of a tile from its rows in LDS.
+    __device__ __forceinline__ void take_keys(const char* ks)
+    {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                k[s][i] = *reinterpret_cast<const u32x4*>(
+                    ks + (s * 16 + c) * S::kRow + (((uint32_t)i * 4 + g) ^ S::turn(c)) * 16);
+            }
+        trim_keys();
+    }
+
+    __device__ __forceinline__ void take_values(const char* vs)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                v[0][e][b] = *reinterpret_cast<const Words<kWords>*>(
+                    vs + S::slot(key_of(e)) * S::kRow + (b * 128 + c * kEach) * (E4M3 ? 1 : 2));
+            }
+    }
+
+    // The same straight from the pool.
+    template <bool PASS>
+    __device__ __forceinline__ void load_keys(u32x4* in, uint32_t t)
     {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int64_t at = place[t + s * 16 + c];
-            const char* p = kbase + (at < 0 ? 0 : at);
+            const char* p = kbase + place[t + s * 16 + c];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const uint32_t d = E4M3 ? (uint32_t)i * 64 + g * 16 : (uint32_t)i * 32 + g * 8;
-                const uint32_t b = d < a.D ? d * (E4M3 ? 1 : 2) : 0;
-                k[s][i] = *reinterpret_cast<const u32x4*>(p + b);
+                in[s * kLoads + i] = load<PASS, u32x4>(p + (d < a.D ? d * (E4M3 ? 1 : 2) : 0));
             }
         }
     }
 
-    __device__ __forceinline__ uint32_t key_of(int e) const { return (uint32_t)(e / 4) * 16 + g * 4 + e % 4; }
-
-    __device__ __forceinline__ void load_values(uint32_t t)
+    template <bool PASS>
+    __device__ __forceinline__ void load_values(int x, uint32_t t)
     {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t at = place[t + key_of(e)];
-            const char* p = vbase + (at < 0 ? 0 : at);
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const uint32_t d = (uint32_t)b * 128 + c * kEach;
-                v[e][b] = *reinterpret_cast<const Words<kWords>*>(p + (d < a.D ? d * (E4M3 ? 1 : 2) : 0));
+                v[x][e][b] = load<PASS, Words<kWords>>(vbase + place[t + key_of(e)] +
+                                                       (d < a.D ? d * (E4M3 ? 1 : 2) : 0));
             }
-        }
+    }
+
+    // Fills slot x.
+    __device__ __forceinline__ void fetch_keys(int x, uint32_t t)
+    {
+        if constexpr (kBounce) load_rows<ONCE>(k_in[x], t);
+        else load_keys<ONCE>(k_in[x], t);
     }
 
     // Dims past the head's end were loads of its first ones: zeros instead.
@@ -292,29 +378,29 @@ struct Tile {
 
     __device__ __forceinline__ u32x4 key_part(int s, int i) const
     {
-        u32x4 x;
+        u32x4 y;
         if constexpr (E4M3) {
             const uint32_t w0 = k[s][i / 2][(i % 2) * 2], w1 = k[s][i / 2][(i % 2) * 2 + 1];
-            x = u32x4{H::template from8<false>(w0), H::template from8<true>(w0),
+            y = u32x4{H::template from8<false>(w0), H::template from8<true>(w0),
                       H::template from8<false>(w1), H::template from8<true>(w1)};
         } else {
-            x = k[s][i];
+            y = k[s][i];
         }
-        return x;
+        return y;
     }
 
     // A operands of output products (j, j + 1): dims 2 of the lane's, 8 keys.
-    __device__ __forceinline__ void value_parts(int j, u32x4* even, u32x4* odd) const
+    __device__ __forceinline__ void value_parts(int slot, int j, u32x4* even, u32x4* odd) const
     {
         const int b = j / kEach, w = j % kEach;
         uint32_t x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if constexpr (E4M3) {
-                const uint32_t y = v[e][b].w[w / 4];
+                const uint32_t y = v[slot][e][b].w[w / 4];
                 x[e] = (w / 2) % 2 ? H::template from8<true>(y) : H::template from8<false>(y);
             } else {
-                x[e] = v[e][b].w[w / 2];
+                x[e] = v[slot][e][b].w[w / 2];
             }
         }
 #pragma unroll
@@ -339,12 +425,13 @@ struct Tile {
             s0 = H::mfma(key_part(0, i), q[i], s0);
             s1 = H::mfma(key_part(1, i), q[i], s1);
         }
+        const uint32_t exist = MASKED ? there[t / kTile] : 0;
         float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             s[e] = (e < 4 ? s0[e] : s1[e - 4]) * scale;
             if constexpr (MASKED) {
-                const bool on = place[t + key_of(e)] >= 0 && sees(key0 + (int32_t)(t + key_of(e)));
+                const bool on = (exist >> key_of(e) & 1) && sees(key0 + (int32_t)(t + key_of(e)));
                 s[e] = on ? s[e] : kNone;
             }
         }
@@ -362,11 +449,11 @@ struct Tile {
         const float from = (m == kNone ? 0.0f : m) - H::kLift;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const float x = exp2_fast(s[2 * p] - from), y = exp2_fast(s[2 * p + 1] - from);
-            l += x + y;
-            const uint32_t w = H::pack(x, y);
+            const float w0 = exp2_fast(s[2 * p] - from), w1 = exp2_fast(s[2 * p + 1] - from);
+            l += w0 + w1;
+            const uint32_t w = H::pack(w0, w1);
             (*big)[p] = w;
-            (*rest)[p] = H::pack(x - H::lo(w), y - H::hi(w));
+            (*rest)[p] = H::pack(w0 - H::lo(w), w1 - H::hi(w));
         }
     }
 
@@ -379,26 +466,26 @@ struct Tile {
     }
 
     // Value rows that are not there become zeros.
-    __device__ __forceinline__ void drop_missing(uint32_t t)
+    __device__ __forceinline__ void drop_missing(int x, uint32_t t)
     {
+        const uint32_t exist = there[t / kTile];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (place[t + key_of(e)] < 0) {
+            const uint32_t keep = exist >> key_of(e) & 1 ? ~0u : 0u;
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b)
+            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w) v[e][b].w[w] = 0;
-            }
+                for (int w = 0; w < kWords; ++w) v[x][e][b].w[w] &= keep;
         }
     }
 
     // The output products of one tile, whose values are in v.
-    __device__ __forceinline__ void gather(u32x4 big, u32x4 rest)
+    __device__ __forceinline__ void gather(int x, u32x4 big, u32x4 rest)
     {
 #pragma unroll
         for (int j = 0; j < kOuts; j += 2) {
             u32x4 even, odd;
-            value_parts(j, &even, &odd);
+            value_parts(x, j, &even, &odd);
             o[j] = H::mfma(even, big, o[j]);
             o[j + 1] = H::mfma(odd, big, o[j + 1]);
             o[j] = H::mfma(even, rest, o[j]);
@@ -406,57 +493,65 @@ struct Tile {
         }
     }
 
-    // One tile from the registers; the loads of the wave's next one follow as
-    // soon as the registers are free.
+    // One tile whose rows are in LDS.
     template <bool MASKED>
-    __device__ __forceinline__ void tile(uint32_t t, uint32_t next, uint32_t end, int32_t key0)
+    __device__ __forceinline__ void tile(const char* ks, const char* vs, uint32_t t, int32_t key0)
     {
         u32x4 big, rest;
-        trim_keys();
+        take_keys(ks);
         weigh<MASKED>(t, key0, &big, &rest);
-        if (next < end) load_keys(next);
-        if constexpr (MASKED) drop_missing(t);
-        gather(big, rest);
-        if (next < end) load_values(next);
+        take_values(vs);
+        if constexpr (MASKED) drop_missing(0, t);
+        gather(0, big, rest);
     }
 
-    // One tile from LDS (see Stage).
-    template <bool MASKED>
-    __device__ __forceinline__ void tile_staged(const char* ks, const char* vs, uint32_t t, int32_t key0)
+    // A wave's LDS accesses are carried out in order: only the compiler has to
+    // be kept from moving one lane's reads past another's writes.
+    static __device__ __forceinline__ void in_order()
     {
-        using S = Stage<E4M3, DP>;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                k[s][i] = *reinterpret_cast<const u32x4*>(
-                    ks + (s * 16 + c) * S::kRow + (((uint32_t)i * 4 + g) ^ S::turn(c)) * 16);
-            }
-        trim_keys();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    // The tile of slot x; the loads of the tile that takes the slot next are
+    // queued as soon as its registers are free.  They are queued always (past
+    // the part's end they read the pool's first row): the number of loads in
+    // flight is then known, and a wait is for its own loads only.
+    template <bool MASKED>
+    __device__ __forceinline__ void tile_own(int x, char* own, uint32_t t, uint32_t next, int32_t key0)
+    {
         u32x4 big, rest;
+        if constexpr (kBounce) {
+            in_order();
+            put(k_in[x], own);
+            fetch_keys(x, next);
+            in_order();
+            take_keys(own);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * kLoads; ++i) k[i / kLoads][i % kLoads] = k_in[x][i];
+            trim_keys();
+        }
         weigh<MASKED>(t, key0, &big, &rest);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                v[e][b] = *reinterpret_cast<const Words<kWords>*>(
-                    vs + S::slot(key_of(e)) * S::kRow + (b * 128 + c * kEach) * (E4M3 ? 1 : 2));
-            }
-        if constexpr (MASKED) drop_missing(t);
-        gather(big, rest);
+        if constexpr (!kBounce) fetch_keys(x, next);
+        if constexpr (MASKED) drop_missing(x, t);
+        gather(x, big, rest);
+        load_values<ONCE>(x, next);
     }
 
     // The careful form of a tile (see the top of the file): positions
     // [first, last] of the workgroup's queries one after the other.
     __device__ __forceinline__ void tile_careful(uint32_t t, int32_t key0, int32_t first, int32_t last)
     {
-        load_keys(t);
+        load_keys<false>(k_in[0], t);
+#pragma unroll
+        for (int i = 0; i < 2 * kLoads; ++i) k[i / kLoads][i % kLoads] = k_in[0][i];
         trim_keys();
         u32x4 big, rest;
         weigh<true>(t, key0, &big, &rest);
         for (int32_t at = first; at <= last; ++at) {
-            load_values(t);
-            drop_missing(t);
+            load_values<false>(0, t);
+            drop_missing(0, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int32_t key = key0 + (int32_t)(t + key_of(e));
@@ -464,13 +559,13 @@ struct Tile {
 #pragma unroll
                     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                        for (int w = 0; w < kWords; ++w) v[e][b].w[w] = 0;
+                        for (int w = 0; w < kWords; ++w) v[0][e][b].w[w] = 0;
                 }
             }
 #pragma unroll
             for (int j = 0; j < kOuts; j += 2) {
                 u32x4 x[2];
-                value_parts(j, &x[0], &x[1]);
+                value_parts(0, j, &x[0], &x[1]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // the weights' second part meets finite values only
@@ -520,19 +615,38 @@ __device__ __forceinline__ void store8(const AttnArgs& a, bool fp16, uint16_t* d
     }
 }
 
+// Whether key rows go through LDS: all but the shortest rows, whose tiles are
+// too little work beside that (e4m3 rows of 64: 97 us direct, 109 by LDS), and
+// the longest, for which the registers do not suffice.
+template <bool E4M3, int DP>
+constexpr bool keys_bounce()
+{
+    return E4M3 ? DP == 128 : DP <= 128;
+}
+
+// Tiles that a wave loads ahead, as its registers allow.
+template <bool E4M3, int DP>
+constexpr int tiles_ahead()
+{
+    return DP * (E4M3 ? 1 : 2) <= 64 ? 3 : DP * (E4M3 ? 1 : 2) <= 128 ? 2 : 1;
+}
+
 // RW waves of the workgroup hold 16 rows each, KW = kWaves / RW waves share a
 // row's keys.  RW = 1: each wave loads its own tiles to registers, one tile
 // ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.
-template <bool FP16, bool E4M3, int DP, int RW>
+template <bool FP16, bool E4M3, int DP, int RW, bool ONCE>
 __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a)
 {
-    using T = Tile<FP16, E4M3, DP>;
+    constexpr int kDeep = RW > 1 ? 1 : tiles_ahead<E4M3, DP>();
+    using T = Tile<FP16, E4M3, DP, kDeep, keys_bounce<E4M3, DP>(), ONCE>;
     using S = Stage<E4M3, DP>;
     using H = Half<FP16>;
     constexpr int KW = kWaves / RW;
     constexpr int kRow = row_stride<DP>();
-    constexpr int kSums = kWaves * 16 * kRow * 4, kStages = RW > 1 ? 4 * S::kBytes : 0;
-    __shared__ int64_t place[RW > 1 ? kMaxChunkStaged : kMaxChunk];
+    constexpr int kSums = kWaves * 16 * kRow * 4, kStages = RW > 1 ? 4 * S::kBytes : kWaves * kTile * S::kRow;
+    constexpr int kPlaces = RW > 1 ? kMaxChunkStaged : kMaxChunk + kDeep * kRound;
+    __shared__ __align__(16) int64_t place[kPlaces];
+    __shared__ uint32_t there[kPlaces / kTile];
     // the stages, then the waves' sums
     __shared__ __align__(16) char pool[kSums > kStages ? kSums : kStages];
     __shared__ float sm[kWaves][16], sl[kWaves][16];
@@ -557,9 +671,11 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     // places of the part's keys
     if (tid == 0) holes = 0;
     __syncthreads();
-    constexpr uint32_t kPad = RW > 1 ? kStage : kTile;
+    constexpr uint32_t kPad = RW > 1 ? S::kKeys : kTile;
     const uint32_t padded = (count + kPad - 1) / kPad * kPad;
-    for (uint32_t j = tid; j < padded; j += kThreads) {
+    const uint32_t filled = RW > 1 ? padded : padded + kDeep * kRound;
+    for (uint32_t j0 = wave * 64; j0 < filled; j0 += kThreads) {
+        const uint32_t j = j0 + lane;
         int64_t at = -1;
         if (j < count) {
             const uint32_t key = (uint32_t)key0 + j, slot = key / a.page_size;
@@ -570,10 +686,12 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
                 holes = 1;
             }
         }
-        place[j] = at;
+        const uint64_t on = __ballot(at >= 0);
+        if (j < filled) place[j] = at < 0 ? 0 : at;
+        if (lane < 2 && j0 + lane * kTile < filled) there[j0 / kTile + lane] = (uint32_t)(on >> (lane * kTile));
     }
 
-    T t{a, place, a.kc + hk * a.head, a.vc + hk * a.head, lane & 15, lane / 16};
+    T t{a, place, there, a.kc + hk * a.head, a.vc + hk * a.head, lane & 15, lane / 16};
     t.scale = a.scale * (a.k_scale ? a.k_scale[hk] : 1.0f);
     {
         const uint32_t r = row0 + rw * 16 + t.c;
@@ -613,33 +731,45 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     };
     if constexpr (RW == 1) {
         const uint32_t begin = kw * kTile;
+        char* own = pool + kw * (kTile * S::kRow);
         if (begin < padded) {
-            t.load_keys(begin);
-            t.load_values(begin);
-            for (uint32_t at = begin; at < padded; at += kRound) {
-                if (all_seen(at)) t.template tile<false>(at, at + kRound, padded, key0);
-                else t.template tile<true>(at, at + kRound, padded, key0);
+#pragma unroll
+            for (int x = 0; x < kDeep; ++x) {
+                t.fetch_keys(x, begin + x * kRound);
+                t.template load_values<ONCE>(x, begin + x * kRound);
             }
+            for (uint32_t at = begin;;) {
+#pragma unroll
+                for (int x = 0; x < kDeep; ++x) {
+                    const uint32_t next = at + kDeep * kRound;
+                    if (all_seen(at)) t.template tile_own<false>(x, own, at, next, key0);
+                    else t.template tile_own<true>(x, own, at, next, key0);
+                    at += kRound;
+                    if (at >= padded) goto through;
+                }
+            }
+        through:;
         }
     } else {
-        if (padded > 0) S::copy(a, place, 0, t.kbase, t.vbase, pool);
-        for (uint32_t at = 0; at < padded; at += kStage) {
+        auto copy = [&](uint32_t at, uint32_t half) {
+            S::template copy<ONCE>(a, place, at, t.kbase, t.vbase, pool + half * (2 * S::kBytes));
+        };
+        if (padded > 0) copy(0, 0);
+        for (uint32_t at = 0; at < padded; at += S::kKeys) {
             // this stage's copies have landed, and every wave is through with
             // the stage before, whose half the next copies fill
+            const uint32_t half = at / S::kKeys % 2;
             wait_vmcnt<0>();
             __syncthreads();
-            const char* here = pool + at / kStage % 2 * (2 * S::kBytes);
-            if (at + kStage < padded) {
-                S::copy(a, place, at + kStage, t.kbase, t.vbase,
-                        pool + (at / kStage + 1) % 2 * (2 * S::kBytes));
-            }
+            const char* here = pool + half * (2 * S::kBytes);
+            if (at + S::kKeys < padded) copy(at + S::kKeys, 1 - half);
             if (!some) continue;
 #pragma unroll
-            for (uint32_t x = 0; x < kStage / kTile / KW; ++x) {
+            for (uint32_t x = 0; x < S::kKeys / kTile / KW; ++x) {
                 const uint32_t off = (x * KW + kw) * kTile;
                 const char *ks = here + off * S::kRow, *vs = ks + S::kBytes;
-                if (all_seen(at + off)) t.template tile_staged<false>(ks, vs, at + off, key0);
-                else t.template tile_staged<true>(ks, vs, at + off, key0);
+                if (all_seen(at + off)) t.template tile<false>(ks, vs, at + off, key0);
+                else t.template tile<true>(ks, vs, at + off, key0);
             }
         }
     }
@@ -712,22 +842,23 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     }
 }
 
-// Joins the parts of rows that have several: TPR threads a row, a lane per
-// four dims, the parts dealt to TPR / (D / 4) lane groups in order.
-template <bool FP16, int TPR>
+// Joins the parts of rows that have several: a workgroup takes 256 / TPR
+// pieces of a row, DIMS dims of it, four to a lane, the parts dealt to the
+// piece's TPR / (DIMS / 4) lane groups in order.
+template <bool FP16, int TPR, int DIMS>
 __global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
 {
-    constexpr int kRows = 256 / TPR;
+    constexpr uint32_t kLanes = DIMS / 4, kGroups = TPR / kLanes;
     __shared__ f32x4 so[256];
     __shared__ float sl[256];
-    const uint32_t sub = threadIdx.x / TPR, tid = threadIdx.x % TPR;
-    const uint32_t all = blockIdx.x * kRows + sub;   // (owner, row)
-    const uint32_t lanes = a.D / 4, groups = TPR / lanes;
-    const uint32_t d = tid % lanes * 4, grp = tid / lanes;
+    const uint32_t tid = threadIdx.x % TPR, first = threadIdx.x - tid;
+    const uint32_t cuts = (a.D + DIMS - 1) / DIMS;
+    const uint32_t piece = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+    const uint32_t all = piece / cuts;   // (owner, row)
+    const uint32_t d = (piece - all * cuts) * DIMS + tid % kLanes * 4, grp = tid / kLanes;
     const uint32_t owner = all / a.rows, r = all - owner * a.rows;
     const uint32_t n = owner / a.Hk, hk = owner - n * a.Hk;
-    const bool on = owner < a.N * a.Hk;
-    const uint32_t parts = on ? keys_of(a, n).parts : 0;
+    const uint32_t parts = owner < a.N * a.Hk ? keys_of(a, n).parts : 0;
     const int64_t at = (int64_t)all * a.splits;
     f32x4 y = {0, 0, 0, 0};
     float l = 0.0f, top = kNone;
@@ -740,27 +871,26 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
         sl[threadIdx.x] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < TPR / 64; ++w) top = fmaxf(top, sl[w * 64]);
+        for (int w = 0; w < TPR / 64; ++w) top = fmaxf(top, sl[first + w * 64]);
         __syncthreads();
     }
     if (parts > 1) {
-        if (grp < groups) {
 #pragma unroll 4
-            for (uint32_t s = grp; s < parts; s += groups) {
-                const float2 ml = a.part_ml[at + s];
-                const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-                l += ml.y * f;
-                y += *reinterpret_cast<const f32x4*>(a.part + (at + s) * a.D + d) * f;
-            }
+        for (uint32_t s = grp; s < parts; s += kGroups) {
+            const float2 ml = a.part_ml[at + s];
+            const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+            l += ml.y * f;
+            if (d < a.D) y += *reinterpret_cast<const f32x4*>(a.part + (at + s) * a.D + d) * f;
         }
     }
     so[threadIdx.x] = y;
     sl[threadIdx.x] = l;
     __syncthreads();
-    if (parts <= 1 || tid >= lanes) return;
-    for (uint32_t x = 1; x < groups; ++x) {
-        y += so[threadIdx.x + x * lanes];
-        l += sl[threadIdx.x + x * lanes];
+    if (parts <= 1 || tid >= kLanes || d >= a.D) return;
+#pragma unroll
+    for (uint32_t x = 1; x < kGroups; ++x) {
+        y += so[threadIdx.x + x * kLanes];
+        l += sl[threadIdx.x + x * kLanes];
     }
     const uint32_t i = r / a.G, h = hk * a.G + (r - i * a.G);
     const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[hk] : 1.0f) / l;
@@ -775,6 +905,12 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
             l == 0.0f ? kNone : (top - Half<FP16>::kLift + log2f(l)) * 0.693147180559945309f;
     }
 }
+
+// Which of the kernels.
+struct Way {
+    int rw;
+    bool e4m3, once;
+};
 
 struct Shape {
     int64_t N, Q, Hq, heads, dim, max_len, window;
@@ -799,7 +935,7 @@ struct Plan {
 // find the keys in their XCD's L2.  Parts: enough workgroups to fill the chip
 // several times over (kTarget), each with whole rounds of its four waves;
 // never more than kMaxChunk keys.
-constexpr int64_t kTarget = 2048;
+constexpr int64_t kTarget = 768;
 
 Plan plan_of(const Shape& s)
 {
@@ -834,40 +970,49 @@ int64_t plan_words(const Shape& s, const Plan& p)
 }
 
 template <bool FP16, bool E4M3, int DP, int RW>
-void launch_waves(const AttnArgs& a, hipStream_t stream)
+void launch_waves(const AttnArgs& a, bool once, hipStream_t stream)
 {
     const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
-    hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW>), dim3(grid), dim3(kThreads), 0, stream, a);
+    if (once) {
+        hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, true>), dim3(grid), dim3(kThreads), 0,
+                           stream, a);
+    } else {
+        hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, false>), dim3(grid), dim3(kThreads), 0,
+                           stream, a);
+    }
 }
 
 template <bool FP16, bool E4M3, int DP>
-void launch_rows(const AttnArgs& a, int rw, hipStream_t stream)
+void launch_rows(const AttnArgs& a, const Way& way, hipStream_t stream)
 {
-    if (rw == 1) launch_waves<FP16, E4M3, DP, 1>(a, stream);
-    else if (rw == 2) launch_waves<FP16, E4M3, DP, 2>(a, stream);
-    else launch_waves<FP16, E4M3, DP, 4>(a, stream);
+    if (way.rw == 1) launch_waves<FP16, E4M3, DP, 1>(a, way.once, stream);
+    else if (way.rw == 2) launch_waves<FP16, E4M3, DP, 2>(a, way.once, stream);
+    else launch_waves<FP16, E4M3, DP, 4>(a, way.once, stream);
 }
 
 template <bool FP16, bool E4M3>
-void launch_dims(const AttnArgs& a, int rw, hipStream_t stream)
+void launch_dims(const AttnArgs& a, const Way& way, hipStream_t stream)
 {
-    if (a.D <= 64) return launch_rows<FP16, E4M3, 64>(a, rw, stream);
-    if (a.D <= 128) return launch_rows<FP16, E4M3, 128>(a, rw, stream);
-    return launch_rows<FP16, E4M3, 256>(a, rw, stream);
+    if (a.D <= 64) return launch_rows<FP16, E4M3, 64>(a, way, stream);
+    if (a.D <= 128) return launch_rows<FP16, E4M3, 128>(a, way, stream);
+    return launch_rows<FP16, E4M3, 256>(a, way, stream);
 }
 
 template <bool FP16>
-hipError_t launch_attention(const AttnArgs& a, bool e4m3, int rw, hipStream_t stream)
+hipError_t launch_attention(const AttnArgs& a, const Way& way, hipStream_t stream)
 {
-    if (e4m3) launch_dims<FP16, true>(a, rw, stream);
-    else launch_dims<FP16, false>(a, rw, stream);
+    if (way.e4m3) launch_dims<FP16, true>(a, way, stream);
+    else launch_dims<FP16, false>(a, way, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const uint32_t rows = a.N * a.Hk * a.rows;
+    // few parts: a wave a row's 128 dims; many: a workgroup 32 dims
     if (a.splits <= 16) {
-        hipLaunchKernelGGL((join_kernel<FP16, 64>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
+        const uint32_t pieces = rows * ((a.D + 127) / 128);
+        hipLaunchKernelGGL((join_kernel<FP16, 64, 128>), dim3((pieces + 3) / 4), dim3(256), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((join_kernel<FP16, 256>), dim3(rows), dim3(256), 0, stream, a);
+        const uint32_t pieces = rows * ((a.D + 31) / 32);
+        hipLaunchKernelGGL((join_kernel<FP16, 256, 32>), dim3(pieces), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -972,9 +1117,14 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
         a.part = reinterpret_cast<float*>(table);
         a.part_ml = reinterpret_cast<float2*>(a.part + s.N * s.Q * s.Hq * p.splits * s.dim);
     }
-    const hipError_t err = x.dtype == XPRESS_FP16
-                               ? launch_attention<true>(a, c.dtype == XPRESS_E4M3, p.rw, stream)
-                               : launch_attention<false>(a, c.dtype == XPRESS_E4M3, p.rw, stream);
+    // Loads pass the caches by where each 128-byte line is read by one workgroup:
+    // whole lines in a head's row or run of rows, and no second group of rows
+    // (token-major rows of 160 bytes: 62 us through the caches, 80 past them;
+    // head-major rows of 256 bytes: 69 and 63).
+    const Way way = {p.rw, c.dtype == XPRESS_E4M3,
+                     p.groups == 1 && (c.stride_token == c.dim || c.dim * e % 128 == 0)};
+    const hipError_t err = x.dtype == XPRESS_FP16 ? launch_attention<true>(a, way, stream)
+                                                  : launch_attention<false>(a, way, stream);
     return err == hipSuccess ? XPRESS_OK : hip_fail(err);
 }
 
