@@ -8,22 +8,28 @@
 // masses are sums of count * exp((value - max) / temperature).  One pass over
 // the row counts the values in LDS (exact, whatever the order of the atomics);
 // the exponentials are then taken once per distinct value, in 64 bits; and
-// the drawn token is the j-th id holding one known value, found by a second
-// look at the row.  No sort, no prefix sum over the vocabulary.
+// the drawn token is the j-th id holding one known value.  No sort, no prefix
+// sum over the vocabulary.  A workgroup of 512 threads takes a row.
 //
-// Bins.  Value bits h = (sign, 15 magnitude bits): the counts of +m and -m
-// share LDS word m, the positive one in the low 16 bits.  128 KiB of LDS hold
-// all 32768 words.  A 16-bit count overflows when more than 65535 logits of
-// a row are equal; the words' total then falls short of the number counted,
-// and the row is done again in two half-passes (positive, negative) of 32-bit
-// counts.  Logits below -2^101 (-inf and the type's lowest value, the usual
-// masks) are not counted at first: next to a maximum above -2^100, at a
-// temperature below 2^90, their weight exp(-1024) is 0 in 64 bits; otherwise
-// the half-passes run instead.
+// Bins.  Magnitudes of 2^-26 to 2^16 have a 32-bit count each, for either sign:
+// 43 KB, so that two workgroups share a compute unit and one streams its row
+// while the other draws.  Values below -c are not counted, c = 2^12 or more by
+// the temperature: next to a maximum above -c / 2 their weight is at most
+// exp(-746), 0 in 64 bits (masks are such values, and counting them would send
+// every lane to one word).  A row with anything else (a tinier value that is
+// not 0, 2^16 or more, a maximum too low, a temperature above 43) is counted
+// again over all 65536 values, in seven windows of the order, a pass for each.
 //
-// The order's walk goes by 1024 segments of 64 values: positive magnitudes
-// downwards, then negative ones upwards.  A wave takes a segment at a time,
-// one value per lane.
+// The j-th id.  While the row goes by, the largest of each 16 logits is kept
+// (in 16 bits; a run doubles with every doubling of the row past 163840): only
+// runs that reach the drawn value are read again, for a likely token a few
+// hundredths of the row.
+//
+// The order's walk goes by segments of 64 values, largest first.  A wave takes
+// a segment at a time, one value per lane.
+//
+// Measured (V = 152064): 480 rows with bias 88 us, 3.3 TB/s; 15 rows 57 us; one row
+// without bias 37 us, the time of one workgroup from load to draw.
 
 #include <hip/hip_runtime.h>
 
@@ -38,13 +44,21 @@ namespace {
 
 using namespace xpress;
 
-constexpr int kThreads = 1024;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr uint32_t kWords = 32768;           // magnitudes
-constexpr uint32_t kSegs = 1024;             // segments of 64 values, both signs
-constexpr uint32_t kInf = 0x7F80u;           // magnitude bits of infinity
-constexpr uint32_t kLow = 0x8000u | (0x7F80u - 27u * 128u);     // bits of -2^101
-constexpr uint32_t kTopLow = 0x8000u | (0x7F80u - 28u * 128u);  // bits of -2^100
+constexpr uint32_t kInf = 0x7F80u;               // magnitude bits of infinity
+constexpr uint32_t kOne = 0x3F80u;               // of 1
+constexpr uint32_t kLeast = kOne - 26u * 128u;   // of 2^-26
+constexpr uint32_t kRels = 42u * 128u;           // magnitudes up to 2^16: 1 .. kRels; 0 is zero
+constexpr uint32_t kHuge = kRels + 1;            // all from 2^16 on
+constexpr uint32_t kSide = 5440;                 // bins of a sign, whole segments
+constexpr uint32_t kWindow = 10240;              // of the 65536 values, whole segments
+constexpr uint32_t kKeys = 10240;
+constexpr uint32_t kSegs = 1024;
+static_assert(kSide % 64 == 0 && kSide > kHuge && kWindow <= 2 * kSide && kWindow % 64 == 0, "bins");
 
 struct SampleArgs {
     const uint16_t *base, *bias;
@@ -57,140 +71,199 @@ struct SampleArgs {
 };
 
 struct Shared {
-    uint32_t bins[kWords];
-    uint32_t count[kSegs];   // logits of a segment; then: of all segments before it
-    double mass[kSegs];      // their mass; then: of all segments before it
-    double mass_min[kWaves];
+    uint32_t bins[2 * kSide];
+    uint16_t keys[kKeys];    // largest logit of a run, as int16 bits
+    double mass[kSegs];      // mass of a segment; then: of all segments before it
+    uint32_t count[kSegs];   // the same for logits
     double wave_mass[kWaves];
+    double wave_min[kWaves];
     uint32_t wave_count[kWaves];
-    uint32_t wave_total[kWaves];
-    uint32_t top;            // order position of the largest value counted
-    uint32_t found;
+    uint32_t wave_low[kWaves];
     double f64;
-    uint32_t counted;
+    uint32_t found, counted, rank;
 };
 
 __device__ __forceinline__ float value_of(uint32_t h) { return __uint_as_float(h << 16); }
 
-// Value bits at position i of the descending order (i = 0: the largest
-// positive magnitude 0x7FFF; 32767: +0; 32768: -0; 65535: magnitude 0x7FFF).
-__device__ __forceinline__ uint32_t bits_at(uint32_t i) { return i < kWords ? kWords - 1 - i : i; }
-__device__ __forceinline__ uint32_t order_of(uint32_t h) { return h < kWords ? kWords - 1 - h : h; }
+// Value bits at position i of the descending order of all values (i = 0: the
+// largest positive magnitude 0x7FFF; 32767: +0; 32768: -0; 65535: magnitude
+// 0x7FFF), and the reverse.
+__device__ __forceinline__ uint32_t all_bits_at(uint32_t i) { return i < 32768u ? 32767u - i : i; }
+__device__ __forceinline__ uint32_t all_order_of(uint32_t h) { return h < 32768u ? 32767u - h : h; }
 
-// Eight summed logits of a row from element e on; bits past the row are NaN.
 template <bool VEC, bool BIAS>
-__device__ __forceinline__ u32x4 logits8(const uint16_t* base, const uint16_t* bias, uint32_t e,
-                                         uint32_t V)
-{
-    u32x4 z;
-    if (VEC && e + 8 <= V) {
-        z = *reinterpret_cast<const u32x4*>(base + e);
-        if constexpr (BIAS) {
-            const u32x4 b = *reinterpret_cast<const u32x4*>(bias + e);
-            for (int w = 0; w < 4; ++w) z[w] = add_round2(z[w], b[w]);
+struct Logits {
+    const uint16_t *base, *bias;
+    uint32_t V;
+
+    // Eight summed logits of a row from element e on; bits past the row are NaN.
+    __device__ __forceinline__ u32x4 at(uint32_t e) const
+    {
+        u32x4 z;
+        if (VEC && e + 8 <= V) {
+            z = *reinterpret_cast<const u32x4*>(base + e);
+            if constexpr (BIAS) {
+                const u32x4 b = *reinterpret_cast<const u32x4*>(bias + e);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) z[w] = add_round2(z[w], b[w]);
+            }
+            return z;
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t two = 0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t i = e + 2 * w + s;
+                uint32_t h = 0xFFFFu;
+                if (i < V) {
+                    h = base[i];
+                    if constexpr (BIAS) h = add_round2(h, bias[i]) & 0xFFFFu;
+                }
+                two |= h << (16 * s);
+            }
+            z[w] = two;
         }
         return z;
     }
-    for (int w = 0; w < 4; ++w) {
-        uint32_t two = 0;
-        for (int s = 0; s < 2; ++s) {
-            const uint32_t i = e + 2 * w + s;
-            uint32_t h = 0xFFFFu;
-            if (i < V) {
-                h = base[i];
-                if constexpr (BIAS) h = add_round2(h, bias[i]) & 0xFFFFu;
-            }
-            two |= h << (16 * s);
-        }
-        z[w] = two;
-    }
-    return z;
-}
+};
 
-// What is counted: 0 both signs in 16-bit halves; 1 / 2 the positive / the
-// negative logits in 32-bit words.
-template <bool VEC, bool BIAS>
-__device__ void count_row(Shared& s, const uint16_t* base, const uint16_t* bias, uint32_t V, int what)
+__device__ __forceinline__ uint32_t half_of(const u32x4& z, int i)
 {
-    for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) s.bins[i] = 0;
-    __syncthreads();
-    uint32_t mine = 0;
-    for (uint32_t e = threadIdx.x * 8; e < V; e += kThreads * 8) {
-        const u32x4 z = logits8<VEC, BIAS>(base, bias, e, V);
-        for (int w = 0; w < 8; ++w) {
-            const uint32_t h = w & 1 ? z[w / 2] >> 16 : z[w / 2] & 0xFFFFu;
-            const uint32_t sign = h >> 15;
-            if (what == 0) {
-                if (h <= kLow) {
-                    atomicAdd(&s.bins[h & 0x7FFFu], 1u + sign * 65535u);
-                    ++mine;
-                }
-            } else if (sign == (uint32_t)(what - 1)) {
-                atomicAdd(&s.bins[h & 0x7FFFu], 1u);
-            }
-        }
-    }
-    if (what == 0) {
-        for (int m = 32; m; m >>= 1) mine += __shfl_xor(mine, m);
-        if ((threadIdx.x & 63) == 0) s.wave_total[threadIdx.x / 64] = mine;
-    }
-    __syncthreads();
-    // -0 counts as +0 (in the half-passes the two words are in different
-    // passes; count_at puts them together)
-    if (what == 0 && threadIdx.x == 0) s.bins[0] = (s.bins[0] & 0xFFFFu) + (s.bins[0] >> 16);
-    __syncthreads();
+    return i & 1 ? z[i / 2] >> 16 : z[i / 2] & 0xFFFFu;
 }
 
-// The draw of one row.
-template <bool VEC, bool BIAS>
+// Whether a vector's eight halves are one value.
+__device__ __forceinline__ bool all_alike(const u32x4& z)
+{
+    return z[0] == z[1] && z[0] == z[2] && z[0] == z[3] && z[0] >> 16 == (z[0] & 0xFFFFu);
+}
+
+// Counts one vector into the bins; logits with bits from cut on are left out.
+// Returns its largest logit as an int16 (right where it is not negative);
+// *least: the smallest magnitude less 1 (so that zero does not count).
+__device__ __forceinline__ int32_t tally(Shared& s, const u32x4& z, uint32_t cut, u16x2* least)
+{
+    u32x4 rel;
+    i16x2 top = {INT16_MIN, INT16_MIN};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t two = z[w];
+        const u16x2 mag = __builtin_bit_cast(u16x2, two & 0x7FFF7FFFu);
+        *least = __builtin_elementwise_min(*least, (u16x2)(mag - (u16x2)1));
+        u16x2 r = __builtin_elementwise_sub_sat(mag, (u16x2)(uint16_t)(kLeast - 1));
+        r = __builtin_elementwise_min(r, (u16x2)(uint16_t)kHuge);
+        rel[w] = __builtin_bit_cast(uint32_t, r);
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(i16x2, two));
+    }
+    if (all_alike(z)) {
+        const uint32_t h = z[0] & 0xFFFFu;
+        if (h < cut) atomicAdd(&s.bins[(rel[0] & 0xFFFFu) + (h >> 15) * kSide], 8u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = half_of(z, i);
+            if (h < cut) atomicAdd(&s.bins[half_of(rel, i) + (h >> 15) * kSide], 1u);
+        }
+    }
+    return max((int32_t)top.x, (int32_t)top.y);
+}
+
+// The draw of one row.  FULL: over all values, a window of whose counts the bins
+// hold; else the bins hold the counts of all values that can be drawn.
+template <bool VEC, bool BIAS, bool FULL>
 struct Row {
     Shared& s;
-    const uint16_t *base, *bias;
-    uint32_t V;
-    int state;          // what the bins hold now (see count_row)
-    bool halves;        // 32-bit half-passes
-    uint32_t zeros;     // half-passes: the number of -0 and +0 logits
+    const Logits<VEC, BIAS>& z;
+    uint32_t window;    // FULL: whose counts the bins hold
     uint32_t top;       // order position of the largest value
     double zmax, t;
 
-    // Number of logits at order position i, whose sign's bins are loaded.
-    __device__ uint32_t count_at(uint32_t i) const
+    static constexpr uint32_t kOrder = FULL ? 65536u : 2 * kSide;   // positions
+
+    __device__ __forceinline__ uint32_t bits_at(uint32_t i) const
     {
-        const uint32_t h = bits_at(i), w = s.bins[h & 0x7FFFu];
-        if (!halves) {
-            if (h == 0) return w;
-            if (h == 0x8000u) return 0;
-            return i < kWords ? w & 0xFFFFu : w >> 16;
+        if constexpr (FULL) return all_bits_at(i);
+        const uint32_t rel = i < kSide ? kSide - 1 - i : i - kSide;
+        return (rel ? kLeast - 1 + rel : 0) | (i < kSide ? 0 : 0x8000u);
+    }
+
+    // Number of logits at order position i (FULL: of the window); both zeros
+    // count at +0.
+    __device__ __forceinline__ uint32_t count_at(uint32_t i) const
+    {
+        if constexpr (FULL) return s.bins[i - window * kWindow];
+        if (i == kSide - 1) return s.bins[0] + s.bins[kSide];
+        if (i == kSide) return 0;
+        return i < kSide ? s.bins[kSide - 1 - i] : s.bins[i];
+    }
+
+    // Whether order position i may be drawn: a value at or below the top, not
+    // NaN, not -inf.
+    __device__ __forceinline__ bool real(uint32_t i) const
+    {
+        if (i < top) return false;
+        if constexpr (FULL) {
+            const uint32_t h = all_bits_at(i);
+            return (h & 0x7FFFu) <= kInf && h != (0x8000u | kInf);
         }
-        if (h == 0) return zeros;
-        if (h == 0x8000u) return 0;
-        return w;
+        return (i < kSide ? kSide - 1 - i : i - kSide) <= kRels;
     }
 
-    __device__ void load_half(uint32_t i)
+    // FULL: counts the window of segment seg.
+    __device__ void load(uint32_t seg)
     {
-        const int want = i < kWords ? 1 : 2;
-        if (!halves || state == want) return;
-        __syncthreads();
-        count_row<VEC, BIAS>(s, base, bias, V, want);
-        state = want;
+        if constexpr (FULL) {
+            const uint32_t want = seg / (kWindow / 64);
+            if (window == want) return;
+            __syncthreads();
+            window = want;
+            for (uint32_t i = threadIdx.x; i < kWindow; i += kThreads) s.bins[i] = 0;
+            __syncthreads();
+            for (uint32_t e = threadIdx.x * 8; e < z.V; e += kThreads * 8) {
+                const u32x4 v = z.at(e);
+                const bool alike = all_alike(v);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t h = half_of(v, i);
+                    const uint32_t at = (h == 0x8000u ? 32767u : all_order_of(h)) - want * kWindow;
+                    if (at < kWindow && (!alike || i == 0)) atomicAdd(&s.bins[at], alike ? 8u : 1u);
+                }
+            }
+            __syncthreads();
+        }
     }
 
-    __device__ double weight_at(uint32_t i) const
+    // The first position of the order that holds a value, or kOrder.
+    __device__ uint32_t find_top()
+    {
+        const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+        uint32_t best = kOrder;
+        top = 0;
+        constexpr uint32_t kSpan = FULL ? kWindow : kOrder;
+        for (uint32_t from = 0; from < kOrder && best == kOrder; from += kSpan) {
+            load(from / 64);
+            for (uint32_t i = from + threadIdx.x; i < min(from + kSpan, kOrder); i += kThreads) {
+                if (real(i) && count_at(i) != 0) {
+                    best = i;
+                    break;
+                }
+            }
+            for (int m = 32; m; m >>= 1) best = min(best, __shfl_xor(best, m));
+            if (lane == 0) s.wave_count[wave] = best;
+            __syncthreads();
+            for (uint32_t w = 0; w < kWaves; ++w) best = min(best, s.wave_count[w]);
+            __syncthreads();
+        }
+        return best;
+    }
+
+    __device__ __forceinline__ double weight_at(uint32_t i) const
     {
         if (i == top) return 1.0;
         return exp(((double)value_of(bits_at(i)) - zmax) / t);
     }
 
-    // Whether order position i may be drawn: a value below or at the top, not
-    // NaN, not -inf.
-    __device__ bool real(uint32_t i) const
-    {
-        const uint32_t h = bits_at(i);
-        return i >= top && (h & 0x7FFFu) <= kInf && h != (0x8000u | kInf);
-    }
-
-    // The wave's lanes look at one segment: its count and mass, in order,
+    // The wave's lanes look at one segment: its counts and masses, in order,
     // inclusive up to each lane.
     __device__ void segment(uint32_t seg, uint32_t* n, double* w, uint32_t* n_to, double* m_to) const
     {
@@ -210,297 +283,418 @@ struct Row {
         *n_to = c;
         *m_to = m;
     }
+
+    // Chooses the value: its bits in *want, which of its ids in *nth, the number
+    // of logits not below it in *rank; returns the probability.
+    __device__ double choose(const SampleArgs& a, uint32_t r, bool greedy, uint32_t* want, uint32_t* nth,
+                             uint32_t* rank)
+    {
+        const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+        if (greedy) {
+            load(top / 64);
+            *want = bits_at(top);
+            *nth = 0;
+            *rank = count_at(top);
+            return 1.0;
+        }
+        // counts and masses of the segments, and the mass that min-p keeps
+        constexpr uint32_t kUsed = kOrder / 64;
+        const float min_p = a.min_p[r], top_p = a.top_p[r];
+        const bool by_min = min_p > 0.0f;
+        double kept_min = 0.0;
+        for (uint32_t seg0 = 0; seg0 < kUsed; seg0 += kWaves) {
+            if (FULL && seg0 % (kWindow / 64) == 0) load(seg0);
+            const uint32_t seg = seg0 + wave, i = seg * 64 + lane;
+            if (seg >= kUsed) continue;
+            const uint32_t n = real(i) ? count_at(i) : 0;
+            uint32_t c = 0;
+            double m = 0.0;
+            if (__any(n != 0)) {
+                const double w = n ? weight_at(i) : 0.0;
+                m = (double)n * w;
+                if (w >= (double)min_p) kept_min += m;
+                c = n;
+                for (int d = 32; d; d >>= 1) {
+                    m += __shfl_xor(m, d);
+                    c += __shfl_xor(c, d);
+                }
+            }
+            if (lane == 0) {
+                s.count[seg] = c;
+                s.mass[seg] = m;
+            }
+        }
+        if (by_min) {
+            for (int d = 32; d; d >>= 1) kept_min += __shfl_xor(kept_min, d);
+            if (lane == 0) s.wave_min[wave] = kept_min;
+        }
+        __syncthreads();
+        // exclusive prefix over the segments, kEach to a thread
+        constexpr uint32_t kEach = (kUsed + kThreads - 1) / kThreads;
+        constexpr uint32_t kHold = (kUsed + 64 * kEach - 1) / (64 * kEach);  // waves that have segments
+        uint32_t c_own[kEach], c_before[kEach], c = 0, c_all = 0;
+        double m_own[kEach], m_before[kEach], m = 0.0, m_all = 0.0, m_min = 0.0;
+#pragma unroll
+        for (uint32_t x = 0; x < kEach; ++x) {
+            const uint32_t seg = tid * kEach + x;
+            c_own[x] = seg < kUsed ? s.count[seg] : 0;
+            m_own[x] = seg < kUsed ? s.mass[seg] : 0.0;
+            c += c_own[x];
+            m += m_own[x];
+        }
+        const uint32_t c_thread = c;
+        const double m_thread = m;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t c2 = __shfl_up(c, d);
+            const double m2 = __shfl_up(m, d);
+            if ((int)lane >= d) {
+                c += c2;
+                m += m2;
+            }
+        }
+        if (lane == 63) {
+            s.wave_count[wave] = c;
+            s.wave_mass[wave] = m;
+        }
+        __syncthreads();
+        c -= c_thread;
+        m -= m_thread;
+        for (uint32_t w = 0; w < kHold; ++w) {
+            if (w < wave) {
+                c += s.wave_count[w];
+                m += s.wave_mass[w];
+            }
+            c_all += s.wave_count[w];
+            m_all += s.wave_mass[w];
+        }
+        if (by_min) {
+            for (uint32_t w = 0; w < kWaves; ++w) m_min += s.wave_min[w];
+        }
+#pragma unroll
+        for (uint32_t x = 0; x < kEach; ++x) {
+            const uint32_t seg = tid * kEach + x;
+            c_before[x] = c;
+            m_before[x] = m;
+            if (seg < kUsed) {
+                s.count[seg] = c;
+                s.mass[seg] = m;
+            }
+            c += c_own[x];
+            m += m_own[x];
+        }
+        __syncthreads();
+        // the kept mass: the least of the rules' (each keeps a prefix)
+        const int32_t k = a.top_k[r];
+        double z_mass = m_all;
+        if (k > 0 && (uint32_t)k < c_all) {
+            // the segment in which the k-th id lies
+#pragma unroll
+            for (uint32_t x = 0; x < kEach; ++x) {
+                if (c_own[x] && c_before[x] < (uint32_t)k && (uint32_t)k <= c_before[x] + c_own[x]) {
+                    s.found = tid * kEach + x;
+                }
+            }
+            __syncthreads();
+            const uint32_t seg = s.found;
+            load(seg);
+            if (wave == 0) {
+                uint32_t n, n_to;
+                double w, m_to;
+                segment(seg, &n, &w, &n_to, &m_to);
+                const uint32_t need = (uint32_t)k - s.count[seg];  // ids of this segment kept
+                if (n && n_to - n < need && need <= n_to) {
+                    s.f64 = s.mass[seg] + (m_to - (double)n * w) + (double)(need - (n_to - n)) * w;
+                }
+            }
+            __syncthreads();
+            z_mass = s.f64;
+            __syncthreads();
+        }
+        double kept = z_mass;
+        if (top_p < 1.0f) {
+            const double goal = (double)top_p * z_mass;
+            // the segment holding the last id before which less than goal has gathered
+            if (tid == 0) s.found = top / 64;
+            __syncthreads();
+#pragma unroll
+            for (uint32_t x = 0; x < kEach; ++x) {
+                if (c_own[x] && m_before[x] < goal) atomicMax(&s.found, tid * kEach + x);
+            }
+            __syncthreads();
+            const uint32_t seg = s.found;
+            load(seg);
+            if (wave == 0) {
+                uint32_t n, n_to;
+                double w, m_to;
+                segment(seg, &n, &w, &n_to, &m_to);
+                const double before = s.mass[seg] + (m_to - (double)n * w);
+                double got = 0.0;
+                if (n && before < goal) {
+                    double j = w > 0.0 ? ceil((goal - before) / w) : (double)n;
+                    j = j < 1.0 ? 1.0 : j > (double)n ? (double)n : j;
+                    got = before + j * w;
+                }
+                for (int d = 32; d; d >>= 1) got = fmax(got, __shfl_xor(got, d));
+                if (lane == 0) s.f64 = got;
+            }
+            __syncthreads();
+            kept = fmin(kept, s.f64);
+            __syncthreads();
+        }
+        if (by_min) kept = fmin(kept, m_min);
+        kept = fmax(kept, 1.0);  // the first id's weight
+        // the first id at which the mass passes u * kept
+        float u = a.u[r];
+        u = u > 0.0f ? u : 0.0f;
+        u = u < 1.0f ? u : 0x1.fffffep-1f;
+        const double goal = (double)u * kept;
+        if (tid == 0) s.found = top / 64;
+        __syncthreads();
+#pragma unroll
+        for (uint32_t x = 0; x < kEach; ++x) {
+            if (c_own[x] && m_own[x] > 0.0 && m_before[x] <= goal) atomicMax(&s.found, tid * kEach + x);
+        }
+        __syncthreads();
+        const uint32_t seg = s.found;
+        load(seg);
+        if (wave == 0) {
+            uint32_t n, n_to;
+            double w, m_to;
+            segment(seg, &n, &w, &n_to, &m_to);
+            const double before = s.mass[seg] + (m_to - (double)n * w);
+            const uint64_t may = __ballot(n && w > 0.0 && before <= goal);
+            // the segment's first value where rounding leaves none
+            const uint64_t any = __ballot(n && w > 0.0);
+            const int at = may ? 63 - __clzll(may) : __ffsll((unsigned long long)any) - 1;
+            if ((int)lane == at) {
+                double j = floor((goal - before) / w);
+                j = j < 0.0 ? 0.0 : j > (double)(n - 1) ? (double)(n - 1) : j;
+                s.found = seg * 64 + lane;
+                s.counted = (uint32_t)j;
+                s.rank = s.count[seg] + n_to;
+                s.f64 = w / kept;
+            }
+        }
+        __syncthreads();
+        *want = bits_at(s.found);
+        *nth = s.counted;
+        *rank = s.rank;
+        return s.f64;
+    }
 };
 
-__device__ __forceinline__ double wave_sum(double v)
+// Which of a vector's logits hold the value `want` (either zero for +0).
+__device__ __forceinline__ uint32_t matches(const u32x4& z, uint32_t want)
 {
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = half_of(z, i);
+        m |= (uint32_t)(h == want || (want == 0 && h == 0x8000u)) << i;
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t nth_bit(uint32_t bits, uint32_t nth)
+{
+    for (; nth; --nth) bits &= bits - 1;
+    return (uint32_t)__ffs(bits) - 1u;
 }
 
 template <bool VEC, bool BIAS>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a)
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
 {
     __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    const uint32_t V = a.V, vecs = (V + 7) / 8;
+    // logits of a run: 16 << wide; none where even a wave's vectors are too few
+    uint32_t wide = 0;
+    while ((vecs + (2u << wide) - 1) >> (wide + 1) > kKeys) ++wide;
+    const bool keyed = wide <= 5;
 
-    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const float temp = a.temperature[r];
-        const bool greedy = !(temp > 0.0f);
-        Row<VEC, BIAS> row{s, a.base + (int64_t)r * a.stride_base,
-                           BIAS ? a.bias + (int64_t)r * a.stride_bias : nullptr, a.V, 0, false, 0, 0,
-                           0.0, greedy ? 1.0 : (double)temp};
+    const uint32_t r = blockIdx.x;
+    const float temp = a.temperature[r];
+    const bool greedy = !(temp > 0.0f);
+    const double t = greedy ? 1.0 : (double)temp;
+    const Logits<VEC, BIAS> z{a.base + (int64_t)r * a.stride_base,
+                              BIAS ? a.bias + (int64_t)r * a.stride_bias : nullptr, V};
+    int64_t* dst = a.blk + (r + r / a.bm1 + 1);
 
-        // 1. count, and find the largest value
-        count_row<VEC, BIAS>(s, row.base, row.bias, a.V, 0);
-        uint32_t total = 0, top = 65536u, sum = 0;
-        for (uint32_t w = 0; w < kWaves; ++w) total += s.wave_total[w];
-        for (uint32_t i = tid; i < kWords; i += kThreads) {
-            const uint32_t b = s.bins[i];
-            sum += (b & 0xFFFFu) + (b >> 16);
-            if (i <= kInf) {
-                if (i == 0 ? b != 0 : (b & 0xFFFFu) != 0) top = min(top, order_of(i));
-                if (i != 0 && i != kInf && (b >> 16)) top = min(top, order_of(0x8000u | i));
+    // 1. count.  The cut c is 2^12 .. 2^16, at least 1492 temperatures.
+    uint32_t c = kOne + 12u * 128u;
+    while (c < kOne + 16u * 128u && (double)value_of(c) < 1492.0 * t) c += 128u;
+    const uint32_t cut = 0x8000u | c;
+    for (uint32_t i = tid; i < 2 * kSide; i += kThreads) s.bins[i] = 0;
+    constexpr int kAhead = BIAS ? 4 : 8;     // vectors of a thread in flight
+    u32x4 got[kAhead], add[kAhead];
+    const uint32_t whole = VEC ? V / 8 : 0;  // vectors that are loaded whole
+    // loads are queued always (past the row, its last vector again)
+    auto fetch = [&](int x, uint32_t v) {
+        const uint32_t e = min(v, whole - 1) * 8;
+        got[x] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.base + e));
+        if constexpr (BIAS) add[x] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.bias + e));
+    };
+    u16x2 least = {0xFFFFu, 0xFFFFu};
+    auto take = [&](const u32x4& y, uint32_t v) {
+        int32_t key = tally(s, y, cut, &least);
+        if (keyed) {
+            for (uint32_t d = 1; d < 2u << wide; d <<= 1) key = max(key, __shfl_xor(key, d));
+            if ((v & ((2u << wide) - 1)) == 0 && v < vecs) s.keys[v >> (wide + 1)] = (uint16_t)key;
+        }
+    };
+    if (VEC && whole > 0) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) fetch(x, tid + x * kThreads);
+    }
+    __syncthreads();
+    // Every lane takes part in every vector (as NaN past the row), for the runs.
+    const uint32_t round = (vecs + kThreads - 1) / kThreads * kThreads;
+    auto arrived = [&](int x) {
+        u32x4 y = got[x];
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) y[w] = add_round2(y[w], add[x][w]);
+        }
+        return y;
+    };
+    uint32_t done = 0;  // vectors of all threads
+    if (VEC) {
+        for (; done + kAhead * kThreads <= whole; done += kAhead * kThreads) {
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const u32x4 y = arrived(x);
+                const uint32_t v = done + x * kThreads + tid;
+                fetch(x, v + kAhead * kThreads);
+                take(y, v);
             }
         }
-        for (int m = 32; m; m >>= 1) {
-            sum += __shfl_xor(sum, m);
-            top = min(top, __shfl_xor(top, m));
-        }
-        if (lane == 0) {
-            s.wave_count[wave] = sum;
-            s.count[wave] = top;
-        }
-        __syncthreads();
-        sum = 0;
-        top = 65536u;
-        for (uint32_t w = 0; w < kWaves; ++w) {
-            sum += s.wave_count[w];
-            top = min(top, s.count[w]);
-        }
-        __syncthreads();
-        const bool again = sum != total || top >= order_of(kTopLow) || !(row.t < 0x1p90);
-        if (again) {
-            row.halves = true;
-            uint32_t best = 65536u;
-            for (int half = 1; half <= 2; ++half) {
-                count_row<VEC, BIAS>(s, row.base, row.bias, a.V, half);
-                row.zeros += s.bins[0];
-                for (uint32_t i = tid; i < kWords; i += kThreads) {
-                    if (s.bins[i] == 0) continue;
-                    const uint32_t h = half == 1 ? i : 0x8000u | i;
-                    if (i == 0) best = min(best, order_of(0));
-                    else if (i < kInf || (i == kInf && half == 1)) best = min(best, order_of(h));
-                }
-                __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            if (whole > 0 && done < whole) {
+                const uint32_t v = done + tid;
+                take(v < whole ? arrived(x) : z.at(min(v * 8, V)), v);
+                done += kThreads;
             }
-            row.state = 2;
-            for (int m = 32; m; m >>= 1) best = min(best, __shfl_xor(best, m));
-            if (lane == 0) s.count[wave] = best;
-            __syncthreads();
-            top = 65536u;
-            for (uint32_t w = 0; w < kWaves; ++w) top = min(top, s.count[w]);
-            __syncthreads();
         }
-        const uint32_t n_blk = r / a.bm1;
-        int64_t* dst = a.blk + (r + n_blk + 1);
-        if (top >= 65536u) {  // nothing but NaN and -inf
+    }
+    for (; done < round; done += kThreads) take(z.at(min((done + tid) * 8, V)), done + tid);
+    const uint32_t low = min((uint32_t)least.x, (uint32_t)least.y);
+    {
+        uint32_t l = low;
+        for (int m = 32; m; m >>= 1) l = min(l, __shfl_xor(l, m));
+        if (lane == 0) s.wave_low[wave] = l;
+    }
+    __syncthreads();
+    uint32_t tiny = 0xFFFFu;
+    for (uint32_t w = 0; w < kWaves; ++w) tiny = min(tiny, s.wave_low[w]);
+
+    // 2. choose a value
+    uint32_t want = 0, nth = 0, rank = 0;
+    double p = 0.0;
+    bool usual = tiny >= kLeast - 1 && s.bins[kHuge] == 0 && 1492.0 * t <= (double)value_of(c);
+    if (usual) {
+        Row<VEC, BIAS, false> row{s, z, 0, 0, 0.0, t};
+        const uint32_t top = row.find_top();
+        const uint32_t h = row.bits_at(top);
+        usual = top < row.kOrder && (h < 0x8000u || (h & 0x7FFFu) < c - 128u);
+        if (usual) {
+            row.top = top;
+            row.zmax = (double)value_of(h);
+            p = row.choose(a, r, greedy, &want, &nth, &rank);
+        }
+    }
+    if (!usual) {
+        Row<VEC, BIAS, true> row{s, z, 0xFFFFu, 0, 0.0, t};
+        const uint32_t top = row.find_top();
+        if (top >= row.kOrder) {  // nothing but NaN and -inf
             if (tid == 0) {
                 *dst = 0;
                 if (a.prob) a.prob[r] = 0.0f;
             }
-            __syncthreads();
-            continue;
+            return;
         }
         row.top = top;
-        row.zmax = (double)value_of(bits_at(top));
+        row.zmax = (double)value_of(all_bits_at(top));
+        p = row.choose(a, r, greedy, &want, &nth, &rank);
+    }
+    __syncthreads();
 
-        uint32_t key = top, nth = 0;  // the drawn value, and which of its ids
-        double p_drawn = 1.0;
-        if (!greedy) {
-            // 2. counts and masses of the segments, and the mass that min-p keeps
-            const float min_p = a.min_p[r], top_p = a.top_p[r];
-            const bool by_min = min_p > 0.0f;
-            double kept_min = 0.0;
-            for (uint32_t seg0 = 0; seg0 < kSegs; seg0 += kWaves) {
-                if (row.halves && (seg0 == 0 || seg0 == kSegs / 2)) row.load_half(seg0 * 64);
-                const uint32_t seg = seg0 + wave, i = seg * 64 + lane;
-                const uint32_t n = row.real(i) ? row.count_at(i) : 0;
-                uint32_t c = 0;
-                double m = 0.0;
-                if (__any(n != 0)) {
-                    const double w = n ? row.weight_at(i) : 0.0;
-                    m = (double)n * w;
-                    if (w >= (double)min_p) kept_min += m;
-                    m = wave_sum(m);
-                    c = n;
-                    for (int d = 32; d; d >>= 1) c += __shfl_xor(c, d);
-                }
-                if (lane == 0) {
-                    s.count[seg] = c;
-                    s.mass[seg] = m;
-                }
-            }
-            kept_min = wave_sum(kept_min);
-            if (lane == 0) s.mass_min[wave] = kept_min;
-            __syncthreads();
-            // 3. exclusive prefix over the segments, one per thread
-            const uint32_t c_own = s.count[tid];
-            const double m_own = s.mass[tid];
-            uint32_t c = c_own;
-            double m = m_own;
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t c2 = __shfl_up(c, d);
-                const double m2 = __shfl_up(m, d);
-                if ((int)lane >= d) {
-                    c += c2;
-                    m += m2;
-                }
-            }
-            if (lane == 63) {
-                s.wave_count[wave] = c;
-                s.wave_mass[wave] = m;
-            }
-            __syncthreads();
-            uint32_t c_before = 0, c_all = 0;
-            double m_before = 0.0, m_all = 0.0, m_min = 0.0;
-            for (uint32_t w = 0; w < kWaves; ++w) {
-                if (w == wave) {
-                    c_before = c_all;
-                    m_before = m_all;
-                }
-                c_all += s.wave_count[w];
-                m_all += s.wave_mass[w];
-                m_min += s.mass_min[w];
-            }
-            c_before += c - c_own;
-            m_before += m - m_own;
-            s.count[tid] = c_before;
-            s.mass[tid] = m_before;
-            __syncthreads();
-            // 4. the kept mass: the least of the rules' (each keeps a prefix)
-            const int32_t k = a.top_k[r];
-            double z_mass = m_all;
-            if (k > 0 && (uint32_t)k < c_all) {
-                // the segment in which the k-th id lies
-                if (c_own && c_before < (uint32_t)k && (uint32_t)k <= c_before + c_own) s.found = tid;
-                __syncthreads();
-                const uint32_t seg = s.found;
-                row.load_half(seg * 64);
-                if (wave == 0) {
-                    uint32_t n, n_to;
-                    double w, m_to;
-                    row.segment(seg, &n, &w, &n_to, &m_to);
-                    const uint32_t need = (uint32_t)k - s.count[seg];  // ids of this segment kept
-                    if (n && n_to - n < need && need <= n_to) {
-                        s.f64 = s.mass[seg] + (m_to - (double)n * w) + (double)(need - (n_to - n)) * w;
-                    }
-                }
-                __syncthreads();
-                z_mass = s.f64;
-                __syncthreads();
-            }
-            double kept = z_mass;
-            if (top_p < 1.0f) {
-                const double goal = (double)top_p * z_mass;
-                // the segment holding the last id before which less than goal has gathered
-                if (tid == 0) s.found = top / 64;
-                __syncthreads();
-                if (c_own && m_before < goal) atomicMax(&s.found, tid);
-                __syncthreads();
-                const uint32_t seg = s.found;
-                row.load_half(seg * 64);
-                if (wave == 0) {
-                    uint32_t n, n_to;
-                    double w, m_to;
-                    row.segment(seg, &n, &w, &n_to, &m_to);
-                    const double before = s.mass[seg] + (m_to - (double)n * w);
-                    double got = 0.0;
-                    if (n && before < goal) {
-                        double j = w > 0.0 ? ceil((goal - before) / w) : (double)n;
-                        j = j < 1.0 ? 1.0 : j > (double)n ? (double)n : j;
-                        got = before + j * w;
-                    }
-                    for (int d = 32; d; d >>= 1) got = fmax(got, __shfl_xor(got, d));
-                    if (lane == 0) s.f64 = got;
-                }
-                __syncthreads();
-                kept = fmin(kept, s.f64);
-                __syncthreads();
-            }
-            if (by_min) kept = fmin(kept, m_min);
-            kept = fmax(kept, 1.0);  // the first id's weight
-            // 5. the first id at which the mass passes u * kept
-            float u = a.u[r];
-            u = u > 0.0f ? u : 0.0f;
-            u = u < 1.0f ? u : 0x1.fffffep-1f;
-            const double goal = (double)u * kept;
-            if (tid == 0) s.found = top / 64;
-            __syncthreads();
-            if (c_own && m_own > 0.0 && m_before <= goal) atomicMax(&s.found, tid);
-            __syncthreads();
-            const uint32_t seg = s.found;
-            row.load_half(seg * 64);
-            if (wave == 0) {
-                uint32_t n, n_to;
-                double w, m_to;
-                row.segment(seg, &n, &w, &n_to, &m_to);
-                const double before = s.mass[seg] + (m_to - (double)n * w);
-                const uint64_t may = __ballot(n && w > 0.0 && before <= goal);
-                // the segment's first value where rounding leaves none
-                const uint64_t any = __ballot(n && w > 0.0);
-                const int at = may ? 63 - __clzll(may) : __ffsll((unsigned long long)any) - 1;
-                if ((int)lane == at) {
-                    double j = floor((goal - before) / w);
-                    j = j < 0.0 ? 0.0 : j > (double)(n - 1) ? (double)(n - 1) : j;
-                    s.found = seg * 64 + lane;
-                    s.counted = (uint32_t)j;
-                    s.f64 = w / kept;
-                }
-            }
-            __syncthreads();
-            key = s.found;
-            nth = s.counted;
-            p_drawn = s.f64;
-            __syncthreads();
-        }
-
-        // 6. the nth id (in id order) that holds the drawn value: each wave
-        //    counts its share of the row, then the share with the id is walked
-        const uint32_t want = bits_at(key);
-        const bool zero = want == 0;
-        const uint32_t steps = (a.V + kWaves * 512 - 1) / (kWaves * 512);  // of 512 logits per wave
-        auto matches = [&](u32x4 z) {
-            uint32_t m = 0;
-            for (int w = 0; w < 8; ++w) {
-                const uint32_t h = w & 1 ? z[w / 2] >> 16 : z[w / 2] & 0xFFFFu;
-                m |= (uint32_t)(h == want || (zero && h == 0x8000u)) << w;
-            }
-            return m;
-        };
+    // 3. the nth id (in id order) that holds the value.  Few logits reach it:
+    // a thread looks at consecutive runs, and loads those that do.
+    if (keyed && want > 0 && want < 0x8000u && rank <= V / 64) {
+        const uint32_t runs = (vecs + (2u << wide) - 1) >> (wide + 1);
+        const uint32_t each = (runs + kThreads - 1) / kThreads, first = tid * each;
+        const uint32_t end = min(first + each, runs);
         uint32_t mine = 0;
-        for (uint32_t i = 0; i < steps; ++i) {
-            const uint32_t e = (wave * steps + i) * 512 + lane * 8;
-            if (e < a.V) mine += __popc(matches(logits8<VEC, BIAS>(row.base, row.bias, e, a.V)));
+        for (uint32_t g = first; g < end; ++g) {
+            if ((int32_t)(int16_t)s.keys[g] < (int32_t)want) continue;
+            for (uint32_t x = g << (wide + 1); x < (g + 1) << (wide + 1) && x < vecs; ++x) {
+                mine += __popc(matches(z.at(x * 8), want));
+            }
         }
-        for (int m = 32; m; m >>= 1) mine += __shfl_xor(mine, m);
-        if (lane == 0) s.wave_count[wave] = mine;
+        uint32_t to = mine;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = __shfl_up(to, d);
+            if ((int)lane >= d) to += o;
+        }
+        if (lane == 63) s.wave_count[wave] = to;
         __syncthreads();
-        uint32_t before = 0;
-        for (uint32_t w = 0; w < wave; ++w) before += s.wave_count[w];
-        if (before <= nth && nth < before + mine) {
-            uint32_t left = nth - before;
-            for (uint32_t i = 0; i < steps; ++i) {
-                const uint32_t e = (wave * steps + i) * 512 + lane * 8;
-                const uint32_t m = e < a.V ? matches(logits8<VEC, BIAS>(row.base, row.bias, e, a.V)) : 0;
-                const uint32_t n = __popc(m);
-                uint32_t to = n;
-                for (int d = 1; d < 64; d <<= 1) {
-                    const uint32_t o = __shfl_up(to, d);
-                    if ((int)lane >= d) to += o;
-                }
-                const uint32_t all = __shfl(to, 63);
-                if (left < all) {
-                    if (to - n <= left && left < to) {
-                        uint32_t bits = m;
-                        for (uint32_t k = left - (to - n); k; --k) bits &= bits - 1;
-                        *dst = (int64_t)(e + (uint32_t)__ffs(bits) - 1u);
-                        if (a.prob) a.prob[r] = (float)p_drawn;
-                    }
+        for (uint32_t w = 0; w < wave; ++w) to += s.wave_count[w];
+        if (to - mine <= nth && nth < to) {
+            uint32_t left = nth - (to - mine);
+            for (uint32_t x = first << (wide + 1); x < end << (wide + 1) && x < vecs; ++x) {
+                if ((int32_t)(int16_t)s.keys[x >> (wide + 1)] < (int32_t)want) continue;
+                const uint32_t m = matches(z.at(x * 8), want), n = __popc(m);
+                if (left < n) {
+                    *dst = (int64_t)(x * 8 + nth_bit(m, left));
+                    if (a.prob) a.prob[r] = (float)p;
                     break;
                 }
-                left -= all;
+                left -= n;
             }
         }
-        __syncthreads();
+        return;
+    }
+    // Else each wave counts its share of the row, then the share with the id
+    // is walked.
+    const uint32_t steps = (V + kWaves * 512 - 1) / (kWaves * 512);  // of 512 logits per wave
+    uint32_t mine = 0;
+    for (uint32_t i = 0; i < steps; ++i) {
+        const uint32_t e = (wave * steps + i) * 512 + lane * 8;
+        if (e < V) mine += __popc(matches(z.at(e), want));
+    }
+    for (int m = 32; m; m >>= 1) mine += __shfl_xor(mine, m);
+    if (lane == 0) s.wave_count[wave] = mine;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < wave; ++w) before += s.wave_count[w];
+    if (before <= nth && nth < before + mine) {
+        uint32_t left = nth - before;
+        for (uint32_t i = 0; i < steps; ++i) {
+            const uint32_t e = (wave * steps + i) * 512 + lane * 8;
+            const uint32_t m = e < V ? matches(z.at(e), want) : 0, n = __popc(m);
+            uint32_t to = n;
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t o = __shfl_up(to, d);
+                if ((int)lane >= d) to += o;
+            }
+            const uint32_t all = __shfl(to, 63);
+            if (left < all) {
+                if (to - n <= left && left < to) {
+                    *dst = (int64_t)(e + nth_bit(m, left - (to - n)));
+                    if (a.prob) a.prob[r] = (float)p;
+                }
+                break;
+            }
+            left -= all;
+        }
     }
 }
 
 template <bool VEC, bool BIAS>
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream)
 {
-    const uint32_t grid = a.rows < 65536u ? a.rows : 65536u;
-    hipLaunchKernelGGL((sample_kernel<VEC, BIAS>), dim3(grid), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((sample_kernel<VEC, BIAS>), dim3(a.rows), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 
