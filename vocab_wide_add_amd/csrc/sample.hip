@@ -71,7 +71,7 @@ struct SampleArgs {
 };
 
 struct Shared {
-    uint32_t bins[2 * kSide];
+    __align__(16) uint32_t bins[2 * kSide + 64];   // then a word a lane for what is not counted
     uint16_t keys[kKeys];    // largest logit of a run, as int16 bits
     double mass[kSegs];      // mass of a segment; then: of all segments before it
     uint32_t count[kSegs];   // the same for logits
@@ -79,8 +79,10 @@ struct Shared {
     double wave_min[kWaves];
     uint32_t wave_count[kWaves];
     uint32_t wave_low[kWaves];
+    int32_t wave_high[kWaves];
+    uint16_t turns[kWaves][kKeys / 64 / kWaves + 1];
     double f64;
-    uint32_t found, counted, rank;
+    uint32_t found, counted;
 };
 
 __device__ __forceinline__ float value_of(uint32_t h) { return __uint_as_float(h << 16); }
@@ -139,34 +141,96 @@ __device__ __forceinline__ bool all_alike(const u32x4& z)
     return z[0] == z[1] && z[0] == z[2] && z[0] == z[3] && z[0] >> 16 == (z[0] & 0xFFFFu);
 }
 
-// Counts one vector into the bins; logits with bits from cut on are left out.
-// Returns its largest logit as an int16 (right where it is not negative);
+// Counts one vector into the bins; logits with bits from cut on go to a word of
+// the lane's own instead.  No branch a logit, the arithmetic on pairs: the LDS
+// takes an add of a wave in 15 cycles or so, and this keeps up with it.  Returns
+// the vector's largest logit as an int16 (right where it is not negative);
 // *least: the smallest magnitude less 1 (so that zero does not count).
 __device__ __forceinline__ int32_t tally(Shared& s, const u32x4& z, uint32_t cut, u16x2* least)
 {
-    u32x4 rel;
+    const u16x2 dump = (u16x2)(uint16_t)((2 * kSide + (threadIdx.x & 63)) * 4);
+    u32x4 at;   // byte offsets
     i16x2 top = {INT16_MIN, INT16_MIN};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const uint32_t two = z[w];
         const u16x2 mag = __builtin_bit_cast(u16x2, two & 0x7FFF7FFFu);
         *least = __builtin_elementwise_min(*least, (u16x2)(mag - (u16x2)1));
+        const i16x2 h = __builtin_bit_cast(i16x2, two);
+        top = __builtin_elementwise_max(top, h);
         u16x2 r = __builtin_elementwise_sub_sat(mag, (u16x2)(uint16_t)(kLeast - 1));
         r = __builtin_elementwise_min(r, (u16x2)(uint16_t)kHuge);
-        rel[w] = __builtin_bit_cast(uint32_t, r);
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(i16x2, two));
+        const u16x2 side = __builtin_bit_cast(u16x2, (i16x2)(h >> (i16x2)15)) & (u16x2)(uint16_t)kSide;
+        r = (r + side) << (u16x2)2;
+        u16x2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, two), (u16x2)(uint16_t)(cut - 1));
+        over = (u16x2)0 - __builtin_elementwise_min(over, (u16x2)1);
+        at[w] = __builtin_bit_cast(uint32_t, (u16x2)((r & ~over) | (dump & over)));
     }
+    char* bins = reinterpret_cast<char*>(s.bins);
     if (all_alike(z)) {
-        const uint32_t h = z[0] & 0xFFFFu;
-        if (h < cut) atomicAdd(&s.bins[(rel[0] & 0xFFFFu) + (h >> 15) * kSide], 8u);
+        atomicAdd(reinterpret_cast<uint32_t*>(bins + (at[0] & 0xFFFFu)), 8u);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t h = half_of(z, i);
-            if (h < cut) atomicAdd(&s.bins[half_of(rel, i) + (h >> 15) * kSide], 1u);
-        }
+        for (int i = 0; i < 8; ++i) atomicAdd(reinterpret_cast<uint32_t*>(bins + half_of(at, i)), 1u);
     }
     return max((int32_t)top.x, (int32_t)top.y);
+}
+
+// Sums over the wave, the same in every lane.
+__device__ __forceinline__ uint32_t wave_add(uint32_t v)
+{
+    v += dpp_u32<0xB1>(v);   // lane ^ 1, ^ 2, the other quad of 8, the other 8 of 16
+    v += dpp_u32<0x4E>(v);
+    v += dpp_u32<0x141>(v);
+    v += dpp_u32<0x140>(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)dpp_u32<CTRL>((uint32_t)(b >> 32)) << 32 |
+                                          dpp_u32<CTRL>((uint32_t)b));
+}
+
+__device__ __forceinline__ double wave_add(double v)
+{
+    v += dpp_f64<0xB1>(v);
+    v += dpp_f64<0x4E>(v);
+    v += dpp_f64<0x141>(v);
+    v += dpp_f64<0x140>(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// exp((z - max) / t) in 64 bits, for d = z - max <= 0 and inv = 1 / t.  The
+// quotient with one correction step; then x = k ln 2 + f, |f| <= ln(2) / 2, and
+// the Taylor series of e^f to f^13 (its rest is below 2^-57).
+__device__ __forceinline__ double weight_of(double d, double t, double inv)
+{
+    double x = d * inv;
+    if (t < INFINITY) x = fma(fma(-x, t, d), inv, x);
+    x = d > -INFINITY ? fmax(x, -800.0) : -800.0;   // 0 from exp(-746) on
+    const double k = rint(x * 1.4426950408889634);
+    double f = fma(-k, 0x1.62e42fefa39efp-1, x);    // ln 2 in two parts
+    f = fma(-k, 0x1.abc9e3b39803fp-56, f);
+    double y = 1.0 / 6227020800.0;
+    y = fma(y, f, 1.0 / 479001600.0);
+    y = fma(y, f, 1.0 / 39916800.0);
+    y = fma(y, f, 1.0 / 3628800.0);
+    y = fma(y, f, 1.0 / 362880.0);
+    y = fma(y, f, 1.0 / 40320.0);
+    y = fma(y, f, 1.0 / 5040.0);
+    y = fma(y, f, 1.0 / 720.0);
+    y = fma(y, f, 1.0 / 120.0);
+    y = fma(y, f, 1.0 / 24.0);
+    y = fma(y, f, 1.0 / 6.0);
+    y = fma(y, f, 0.5);
+    y = fma(y, f, 1.0);
+    y = fma(y, f, 1.0);
+    return ldexp(y, (int)k);
 }
 
 // The draw of one row.  FULL: over all values, a window of whose counts the bins
@@ -177,7 +241,7 @@ struct Row {
     const Logits<VEC, BIAS>& z;
     uint32_t window;    // FULL: whose counts the bins hold
     uint32_t top;       // order position of the largest value
-    double zmax, t;
+    double zmax, t, inv;
 
     static constexpr uint32_t kOrder = FULL ? 65536u : 2 * kSide;   // positions
 
@@ -260,7 +324,7 @@ struct Row {
     __device__ __forceinline__ double weight_at(uint32_t i) const
     {
         if (i == top) return 1.0;
-        return exp(((double)value_of(bits_at(i)) - zmax) / t);
+        return weight_of((double)value_of(bits_at(i)) - zmax, t, inv);
     }
 
     // The wave's lanes look at one segment: its counts and masses, in order,
@@ -284,17 +348,14 @@ struct Row {
         *m_to = m;
     }
 
-    // Chooses the value: its bits in *want, which of its ids in *nth, the number
-    // of logits not below it in *rank; returns the probability.
-    __device__ double choose(const SampleArgs& a, uint32_t r, bool greedy, uint32_t* want, uint32_t* nth,
-                             uint32_t* rank)
+    // Chooses the value: its bits in *want, which of its ids in *nth; returns the
+    // probability.
+    __device__ double choose(const SampleArgs& a, uint32_t r, bool greedy, uint32_t* want, uint32_t* nth)
     {
         const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
         if (greedy) {
-            load(top / 64);
             *want = bits_at(top);
             *nth = 0;
-            *rank = count_at(top);
             return 1.0;
         }
         // counts and masses of the segments, and the mass that min-p keeps
@@ -302,30 +363,54 @@ struct Row {
         const float min_p = a.min_p[r], top_p = a.top_p[r];
         const bool by_min = min_p > 0.0f;
         double kept_min = 0.0;
-        for (uint32_t seg0 = 0; seg0 < kUsed; seg0 += kWaves) {
+        // three segments of a wave at a time, for their latencies to overlap
+        constexpr uint32_t kTurn = FULL ? 1 : 3;
+        for (uint32_t seg0 = 0; seg0 < kUsed; seg0 += kTurn * kWaves) {
             if (FULL && seg0 % (kWindow / 64) == 0) load(seg0);
-            const uint32_t seg = seg0 + wave, i = seg * 64 + lane;
-            if (seg >= kUsed) continue;
-            const uint32_t n = real(i) ? count_at(i) : 0;
-            uint32_t c = 0;
-            double m = 0.0;
-            if (__any(n != 0)) {
-                const double w = n ? weight_at(i) : 0.0;
-                m = (double)n * w;
-                if (w >= (double)min_p) kept_min += m;
-                c = n;
-                for (int d = 32; d; d >>= 1) {
-                    m += __shfl_xor(m, d);
-                    c += __shfl_xor(c, d);
-                }
+            uint32_t n[kTurn];
+            bool some = false;
+#pragma unroll
+            for (uint32_t x = 0; x < kTurn; ++x) {
+                const uint32_t seg = seg0 + x * kWaves + wave, i = seg * 64 + lane;
+                n[x] = seg < kUsed && real(i) ? count_at(i) : 0;
+                some |= n[x] != 0;
             }
-            if (lane == 0) {
-                s.count[seg] = c;
-                s.mass[seg] = m;
+            if (!__any(some)) {
+#pragma unroll
+                for (uint32_t x = 0; x < kTurn; ++x) {
+                    const uint32_t seg = seg0 + x * kWaves + wave;
+                    if (lane == 0 && seg < kUsed) {
+                        s.count[seg] = 0;
+                        s.mass[seg] = 0.0;
+                    }
+                }
+                continue;
+            }
+            uint32_t c[kTurn];
+            double m[kTurn];
+#pragma unroll
+            for (uint32_t x = 0; x < kTurn; ++x) {
+                const uint32_t i = (seg0 + x * kWaves + wave) * 64 + lane;
+                const double w = n[x] ? weight_at(i) : 0.0;
+                m[x] = (double)n[x] * w;
+                if (w >= (double)min_p) kept_min += m[x];
+            }
+#pragma unroll
+            for (uint32_t x = 0; x < kTurn; ++x) {
+                m[x] = wave_add(m[x]);
+                c[x] = wave_add(n[x]);
+            }
+#pragma unroll
+            for (uint32_t x = 0; x < kTurn; ++x) {
+                const uint32_t seg = seg0 + x * kWaves + wave;
+                if (lane == 0 && seg < kUsed) {
+                    s.count[seg] = c[x];
+                    s.mass[seg] = m[x];
+                }
             }
         }
         if (by_min) {
-            for (int d = 32; d; d >>= 1) kept_min += __shfl_xor(kept_min, d);
+            kept_min = wave_add(kept_min);
             if (lane == 0) s.wave_min[wave] = kept_min;
         }
         __syncthreads();
@@ -471,14 +556,12 @@ struct Row {
                 j = j < 0.0 ? 0.0 : j > (double)(n - 1) ? (double)(n - 1) : j;
                 s.found = seg * 64 + lane;
                 s.counted = (uint32_t)j;
-                s.rank = s.count[seg] + n_to;
                 s.f64 = w / kept;
             }
         }
         __syncthreads();
         *want = bits_at(s.found);
         *nth = s.counted;
-        *rank = s.rank;
         return s.f64;
     }
 };
@@ -515,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     const uint32_t r = blockIdx.x;
     const float temp = a.temperature[r];
     const bool greedy = !(temp > 0.0f);
-    const double t = greedy ? 1.0 : (double)temp;
+    const double t = greedy ? 1.0 : (double)temp, inv = 1.0 / t;
     const Logits<VEC, BIAS> z{a.base + (int64_t)r * a.stride_base,
                               BIAS ? a.bias + (int64_t)r * a.stride_bias : nullptr, V};
     int64_t* dst = a.blk + (r + r / a.bm1 + 1);
@@ -524,7 +607,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     uint32_t c = kOne + 12u * 128u;
     while (c < kOne + 16u * 128u && (double)value_of(c) < 1492.0 * t) c += 128u;
     const uint32_t cut = 0x8000u | c;
-    for (uint32_t i = tid; i < 2 * kSide; i += kThreads) s.bins[i] = 0;
+    for (uint32_t i = tid * 4; i < 2 * kSide; i += kThreads * 4) {
+        *reinterpret_cast<u32x4*>(&s.bins[i]) = u32x4{0, 0, 0, 0};
+    }
     constexpr int kAhead = BIAS ? 4 : 8;     // vectors of a thread in flight
     u32x4 got[kAhead], add[kAhead];
     const uint32_t whole = VEC ? V / 8 : 0;  // vectors that are loaded whole
@@ -535,10 +620,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         if constexpr (BIAS) add[x] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.bias + e));
     };
     u16x2 least = {0xFFFFu, 0xFFFFu};
+    int32_t high = INT16_MIN;
     auto take = [&](const u32x4& y, uint32_t v) {
         int32_t key = tally(s, y, cut, &least);
+        high = max(high, key);
         if (keyed) {
-            for (uint32_t d = 1; d < 2u << wide; d <<= 1) key = max(key, __shfl_xor(key, d));
+            key = max(key, (int32_t)dpp_u32<0xB1>((uint32_t)key));   // lane ^ 1
+            for (uint32_t d = 2; d < 2u << wide; d <<= 1) key = max(key, __shfl_xor(key, d));
             if ((v & ((2u << wide) - 1)) == 0 && v < vecs) s.keys[v >> (wide + 1)] = (uint16_t)key;
         }
     };
@@ -581,30 +669,41 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     const uint32_t low = min((uint32_t)least.x, (uint32_t)least.y);
     {
         uint32_t l = low;
-        for (int m = 32; m; m >>= 1) l = min(l, __shfl_xor(l, m));
-        if (lane == 0) s.wave_low[wave] = l;
+        int32_t h = high;
+        for (int m = 32; m; m >>= 1) {
+            l = min(l, __shfl_xor(l, m));
+            h = max(h, __shfl_xor(h, m));
+        }
+        if (lane == 0) {
+            s.wave_low[wave] = l;
+            s.wave_high[wave] = h;
+        }
     }
     __syncthreads();
     uint32_t tiny = 0xFFFFu;
-    for (uint32_t w = 0; w < kWaves; ++w) tiny = min(tiny, s.wave_low[w]);
+    for (uint32_t w = 0; w < kWaves; ++w) {
+        tiny = min(tiny, s.wave_low[w]);
+        high = max(high, s.wave_high[w]);
+    }
 
     // 2. choose a value
-    uint32_t want = 0, nth = 0, rank = 0;
+    uint32_t want = 0, nth = 0;
     double p = 0.0;
     bool usual = tiny >= kLeast - 1 && s.bins[kHuge] == 0 && 1492.0 * t <= (double)value_of(c);
     if (usual) {
-        Row<VEC, BIAS, false> row{s, z, 0, 0, 0.0, t};
-        const uint32_t top = row.find_top();
+        Row<VEC, BIAS, false> row{s, z, 0, 0, 0.0, t, inv};
+        // a positive maximum is known already
+        const uint32_t top = high > 0 ? kSide - 1 - ((uint32_t)high - (kLeast - 1)) : row.find_top();
         const uint32_t h = row.bits_at(top);
         usual = top < row.kOrder && (h < 0x8000u || (h & 0x7FFFu) < c - 128u);
         if (usual) {
             row.top = top;
             row.zmax = (double)value_of(h);
-            p = row.choose(a, r, greedy, &want, &nth, &rank);
+            p = row.choose(a, r, greedy, &want, &nth);
         }
     }
     if (!usual) {
-        Row<VEC, BIAS, true> row{s, z, 0xFFFFu, 0, 0.0, t};
+        Row<VEC, BIAS, true> row{s, z, 0xFFFFu, 0, 0.0, t, inv};
         const uint32_t top = row.find_top();
         if (top >= row.kOrder) {  // nothing but NaN and -inf
             if (tid == 0) {
@@ -615,42 +714,71 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         }
         row.top = top;
         row.zmax = (double)value_of(all_bits_at(top));
-        p = row.choose(a, r, greedy, &want, &nth, &rank);
+        p = row.choose(a, r, greedy, &want, &nth);
     }
     __syncthreads();
 
-    // 3. the nth id (in id order) that holds the value.  Few logits reach it:
-    // a thread looks at consecutive runs, and loads those that do.
-    if (keyed && want > 0 && want < 0x8000u && rank <= V / 64) {
+    // 3. the nth id (in id order) that holds the value, among the runs that reach
+    // it: a wave lists those of its share in order, counts their matches 64 runs
+    // at a time, and the one with the id looks at its 64 again.
+    if (usual && keyed && want > 0 && want < 0x8000u) {
         const uint32_t runs = (vecs + (2u << wide) - 1) >> (wide + 1);
-        const uint32_t each = (runs + kThreads - 1) / kThreads, first = tid * each;
-        const uint32_t end = min(first + each, runs);
-        uint32_t mine = 0;
-        for (uint32_t g = first; g < end; ++g) {
-            if ((int32_t)(int16_t)s.keys[g] < (int32_t)want) continue;
-            for (uint32_t x = g << (wide + 1); x < (g + 1) << (wide + 1) && x < vecs; ++x) {
-                mine += __popc(matches(z.at(x * 8), want));
-            }
+        const uint32_t share = (runs + kWaves * 64 - 1) / (kWaves * 64) * 64, first = wave * share;
+        uint32_t* list = s.bins + first;   // the bins are not needed any more
+        uint32_t n = 0;
+        for (uint32_t g0 = first; g0 < min(first + share, runs); g0 += 64) {
+            const uint32_t g = g0 + lane;
+            const bool on = g < runs && (int32_t)(int16_t)s.keys[g] >= (int32_t)want;
+            const uint64_t all = __ballot(on);
+            if (on) list[n + __popcll(all & ((1ull << lane) - 1))] = g;
+            n += (uint32_t)__popcll(all);
         }
-        uint32_t to = mine;
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t o = __shfl_up(to, d);
-            if ((int)lane >= d) to += o;
-        }
-        if (lane == 63) s.wave_count[wave] = to;
-        __syncthreads();
-        for (uint32_t w = 0; w < wave; ++w) to += s.wave_count[w];
-        if (to - mine <= nth && nth < to) {
-            uint32_t left = nth - (to - mine);
-            for (uint32_t x = first << (wide + 1); x < end << (wide + 1) && x < vecs; ++x) {
-                if ((int32_t)(int16_t)s.keys[x >> (wide + 1)] < (int32_t)want) continue;
-                const uint32_t m = matches(z.at(x * 8), want), n = __popc(m);
-                if (left < n) {
-                    *dst = (int64_t)(x * 8 + nth_bit(m, left));
-                    if (a.prob) a.prob[r] = (float)p;
-                    break;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        auto held = [&](uint32_t at) {
+            uint32_t count = 0;
+            if (at < n) {
+                const uint32_t x0 = list[at] << (wide + 1);
+                for (uint32_t x = x0; x < x0 + (2u << wide) && x < vecs; x += 2) {
+                    const u32x4 p0 = z.at(x * 8), p1 = z.at(min(x * 8 + 8, V));
+                    count += __popc(matches(p0, want)) + __popc(matches(p1, want));
                 }
-                left -= n;
+            }
+            return count;
+        };
+        uint32_t sum = 0;
+        for (uint32_t at = 0; at < n; at += 128) {
+            const uint32_t c0 = wave_add(held(at + lane)), c1 = wave_add(held(at + 64 + lane));
+            if (lane == 0) {
+                s.turns[wave][at / 64] = (uint16_t)min(c0, 65535u);
+                s.turns[wave][at / 64 + 1] = (uint16_t)min(c1, 65535u);
+            }
+            sum += c0 + c1;
+        }
+        if (lane == 0) s.wave_count[wave] = sum;
+        __syncthreads();
+        uint32_t before = 0;
+        for (uint32_t w = 0; w < wave; ++w) before += s.wave_count[w];
+        if (before <= nth && nth < before + sum) {
+            uint32_t left = nth - before, at = 0;
+            while (left >= s.turns[wave][at]) left -= s.turns[wave][at++];
+            const uint32_t in = held(at * 64 + lane);
+            uint32_t to = in;
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t o = __shfl_up(to, d);
+                if ((int)lane >= d) to += o;
+            }
+            if (to - in <= left && left < to) {
+                left -= to - in;
+                for (uint32_t x = list[at * 64 + lane] << (wide + 1);; ++x) {
+                    const uint32_t m = matches(z.at(x * 8), want), k = __popc(m);
+                    if (left < k) {
+                        *dst = (int64_t)(x * 8 + nth_bit(m, left));
+                        if (a.prob) a.prob[r] = (float)p;
+                        break;
+                    }
+                    left -= k;
+                }
             }
         }
         return;
@@ -659,9 +787,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     // is walked.
     const uint32_t steps = (V + kWaves * 512 - 1) / (kWaves * 512);  // of 512 logits per wave
     uint32_t mine = 0;
-    for (uint32_t i = 0; i < steps; ++i) {
-        const uint32_t e = (wave * steps + i) * 512 + lane * 8;
-        if (e < V) mine += __popc(matches(z.at(e), want));
+    for (uint32_t i = 0; i < steps; i += 4) {
+        u32x4 y[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const uint32_t e = (wave * steps + i + x) * 512 + lane * 8;
+            y[x] = z.at(i + x < steps ? min(e, V) : V);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mine += __popc(matches(y[x], want));
     }
     for (int m = 32; m; m >>= 1) mine += __shfl_xor(mine, m);
     if (lane == 0) s.wave_count[wave] = mine;
