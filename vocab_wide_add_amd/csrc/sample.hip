@@ -726,12 +726,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         const uint32_t share = (runs + kWaves * 64 - 1) / (kWaves * 64) * 64, first = wave * share;
         uint32_t* list = s.bins + first;   // the bins are not needed any more
         uint32_t n = 0;
-        for (uint32_t g0 = first; g0 < min(first + share, runs); g0 += 64) {
-            const uint32_t g = g0 + lane;
-            const bool on = g < runs && (int32_t)(int16_t)s.keys[g] >= (int32_t)want;
-            const uint64_t all = __ballot(on);
-            if (on) list[n + __popcll(all & ((1ull << lane) - 1))] = g;
-            n += (uint32_t)__popcll(all);
+        for (uint32_t g0 = first; g0 < min(first + share, runs); g0 += 256) {
+            int32_t key[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t g = g0 + x * 64 + lane;
+                key[x] = g < min(first + share, runs) ? (int32_t)(int16_t)s.keys[g] : -1;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const bool on = key[x] >= (int32_t)want;
+                const uint64_t all = __ballot(on);
+                if (on) list[n + __popcll(all & ((1ull << lane) - 1))] = g0 + x * 64 + lane;
+                n += (uint32_t)__popcll(all);
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -746,9 +754,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
             }
             return count;
         };
-        uint32_t sum = 0;
+        uint32_t sum = 0, first64 = 0;
         for (uint32_t at = 0; at < n; at += 128) {
-            const uint32_t c0 = wave_add(held(at + lane)), c1 = wave_add(held(at + 64 + lane));
+            const uint32_t h0 = held(at + lane), h1 = n > at + 64 ? held(at + 64 + lane) : 0;
+            const uint32_t c0 = wave_add(h0), c1 = wave_add(h1);
+            if (at == 0) first64 = h0;
             if (lane == 0) {
                 s.turns[wave][at / 64] = (uint16_t)min(c0, 65535u);
                 s.turns[wave][at / 64 + 1] = (uint16_t)min(c1, 65535u);
@@ -762,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         if (before <= nth && nth < before + sum) {
             uint32_t left = nth - before, at = 0;
             while (left >= s.turns[wave][at]) left -= s.turns[wave][at++];
-            const uint32_t in = held(at * 64 + lane);
+            const uint32_t in = at == 0 ? first64 : held(at * 64 + lane);
             uint32_t to = in;
             for (int d = 1; d < 64; d <<= 1) {
                 const uint32_t o = __shfl_up(to, d);
