@@ -72,6 +72,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 32;        // keys of one tile
 constexpr int kRound = kTile * kWaves;
+constexpr int kUnits = 256;       // compute units of the chip
 constexpr int kMaxChunk = 2048;  // keys of one part
 constexpr int kMaxChunkStaged = 1024;  // the same where LDS also holds the keys
 constexpr float kNone = -INFINITY;
@@ -206,27 +207,36 @@ struct Stage : Lines<E4M3, DP> {
     static constexpr uint32_t kBytes = kKeys * L::kRow;                  // keys or values
     static constexpr uint32_t kCopies = kKeys * L::kPieces / kThreads;   // of a thread, keys or values
 
-    // Queues the copies of keys [t, t + kKeys).
-    // ONCE: no other workgroup reads them, so they pass the caches by.
-    template <bool ONCE>
-    static __device__ __forceinline__ void copy(const AttnArgs& a, const int64_t* place, uint32_t t,
-                                                const char* kbase, const char* vbase, const char* lds)
+    // Where a thread's pieces of keys [t, t + kKeys) are.  Rows that do not exist
+    // and pieces past the head's end: any bytes of the pool, masked or dropped
+    // after.
+    struct From {
+        const char *k[kCopies], *v[kCopies];
+    };
+    static __device__ __forceinline__ From find(const AttnArgs& a, const int64_t* place, uint32_t t,
+                                                const char* kbase, const char* vbase)
     {
-        const uint32_t wave = threadIdx.x / 64, used = a.D * (E4M3 ? 1 : 2);
+        const uint32_t used = a.D * (E4M3 ? 1 : 2);
+        From f;
 #pragma unroll
         for (uint32_t x = 0; x < kCopies; ++x) {
             const uint32_t at = x * kThreads + threadIdx.x, row = at / L::kPieces, piece = at % L::kPieces;
             const uint32_t kd = (piece ^ L::turn(row)) * 16, vd = piece * 16;
-            const int64_t kp = place[t + row], vp = place[t + L::slot(row)];
-            // rows that are not there and pieces past the head's end: any bytes
-            // of the pool, masked or dropped after
-            const char* ks = kbase + kp + (kd < used ? kd : 0);
-            const char* vs = vbase + vp + (vd < used ? vd : 0);
-            const char* to = lds + (x * kThreads + wave * 64) * 16;
-            const uint32_t at_k = lds_addr(reinterpret_cast<const uint16_t*>(to));
-            const uint32_t at_v = lds_addr(reinterpret_cast<const uint16_t*>(to + kBytes));
-            dma16<ONCE>(reinterpret_cast<const uint16_t*>(ks), at_k);
-            dma16<ONCE>(reinterpret_cast<const uint16_t*>(vs), at_v);
+            f.k[x] = kbase + place[t + row] + (kd < used ? kd : 0);
+            f.v[x] = vbase + place[t + L::slot(row)] + (vd < used ? vd : 0);
+        }
+        return f;
+    }
+
+    // Queues their copies to LDS byte address `to`, the wave's part of a stage.
+    // ONCE: no other workgroup reads them, so they pass the caches by.
+    template <bool ONCE>
+    static __device__ __forceinline__ void copy(const From& f, uint32_t to)
+    {
+#pragma unroll
+        for (uint32_t x = 0; x < kCopies; ++x) {
+            dma16<ONCE>(reinterpret_cast<const uint16_t*>(f.k[x]), to + x * kThreads * 16);
+            dma16<ONCE>(reinterpret_cast<const uint16_t*>(f.v[x]), to + kBytes + x * kThreads * 16);
         }
     }
 };
@@ -751,10 +761,14 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
         through:;
         }
     } else {
-        auto copy = [&](uint32_t at, uint32_t half) {
-            S::template copy<ONCE>(a, place, at, t.kbase, t.vbase, pool + half * (2 * S::kBytes));
-        };
-        if (padded > 0) copy(0, 0);
+        const uint32_t to = lds_addr(reinterpret_cast<const uint16_t*>(pool)) +
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave * 64 * 16));
+        // addresses are looked up before the wait, so that the copies follow it at once
+        typename S::From from = {};
+        if (padded > 0) {
+            S::template copy<ONCE>(S::find(a, place, 0, t.kbase, t.vbase), to);
+            if (S::kKeys < padded) from = S::find(a, place, S::kKeys, t.kbase, t.vbase);
+        }
         for (uint32_t at = 0; at < padded; at += S::kKeys) {
             // this stage's copies have landed, and every wave is through with
             // the stage before, whose half the next copies fill
@@ -762,7 +776,10 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
             wait_vmcnt<0>();
             __syncthreads();
             const char* here = pool + half * (2 * S::kBytes);
-            if (at + S::kKeys < padded) copy(at + S::kKeys, 1 - half);
+            if (at + S::kKeys < padded) {
+                S::template copy<ONCE>(from, to + (1 - half) * (2 * S::kBytes));
+                if (at + 2 * S::kKeys < padded) from = S::find(a, place, at + 2 * S::kKeys, t.kbase, t.vbase);
+            }
             if (!some) continue;
 #pragma unroll
             for (uint32_t x = 0; x < S::kKeys / kTile / KW; ++x) {
@@ -932,10 +949,15 @@ struct Plan {
 
 // Rows: as many waves of 16 as hold them, up to the workgroup's 4, so that a
 // block of queries reads the cache once; more go to further workgroups, which
-// find the keys in their XCD's L2.  Parts: enough workgroups to fill the chip
-// several times over (kTarget), each with whole rounds of its four waves;
-// never more than kMaxChunk keys.
-constexpr int64_t kTarget = 768;
+// find the keys in their XCD's L2.
+//
+// Parts: whole rounds of a workgroup's four waves, never more than kMaxChunk
+// keys.  The chip holds two workgroups a compute unit (one at 256 dims).  Where
+// all sequences have the same number of keys to read (one sequence, or a
+// window), as many parts as fit at once (24 windows of 1777, 120 owners: 26 us
+// with 4 parts, 33 with 5); where lengths may differ, a quarter more, so that
+// long ones do not run alone (32 sequences up to 4096: 61 us with 2 parts, 56
+// with 3).
 
 Plan plan_of(const Shape& s)
 {
@@ -946,8 +968,11 @@ Plan plan_of(const Shape& s)
     p.groups = (tiles + p.rw - 1) / p.rw;
     int64_t span = s.max_len;
     if (s.window > 0 && s.window + s.Q - 1 < span) span = s.window + s.Q - 1;
-    const int64_t owners = s.N * s.heads;
-    const int64_t want = (kTarget + owners * p.groups - 1) / (owners * p.groups);
+    const int64_t owners = s.N * s.heads, wide = owners * p.groups;
+    const int64_t slots = (s.dim > 128 ? 1 : 2) * (int64_t)kUnits;
+    const bool even = s.N == 1 || s.window > 0 || s.dim > 128;
+    int64_t want = even ? slots / wide : (slots * 5 / 4 + wide - 1) / wide;
+    if (want < 1) want = 1;
     const int64_t most = p.rw > 1 ? kMaxChunkStaged : kMaxChunk;
     int64_t chunk = (span + want - 1) / want;
     chunk = (chunk + kRound - 1) / kRound * kRound;
