@@ -496,13 +496,24 @@ int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads,
  *   top_k          device pointer, int32 [N*(B-1)].
  *   N, B, V, strides, stream   as for xpress_add_argmax_to_blk.
  *
- * Asynchronous; one launch; no workspace.  Errors as for
- * xpress_add_argmax_to_blk (stride_bias_r is not looked at without bias).
+ * Asynchronous.  Up to 32 rows of 98304 to about 2 million logits are counted in
+ * parts by several workgroups each, in two launches, whose lists meet in the
+ * (device, stream) workspace (xpress_sample_reserve grows it before a capture);
+ * where it cannot be had, and else, one launch and no workspace, with the same
+ * results.  Errors as for xpress_add_argmax_to_blk (stride_bias_r is not looked
+ * at without bias).
  */
 int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, int64_t* blk, float* prob,
                          const float* temperature, const int32_t* top_k, const float* top_p,
                          const float* min_p, const float* u, int64_t N, int64_t B, int64_t V,
                          int64_t stride_base_r, int64_t stride_bias_r, hipStream_t stream);
+
+/*
+ * xpress_sample_reserve -- grow the (device, stream) workspace to what
+ * xpress_sample_to_blk uses for N*(B-1) rows of V logits.  Synchronous.  Returns
+ * XPRESS_OK, XPRESS_EINVAL, XPRESS_ENOMEM or XPRESS_EHIP.
+ */
+int xpress_sample_reserve(int64_t N, int64_t B, int64_t V, hipStream_t stream);
 
 /*
  * xpress_release -- free every workspace the library holds on the current

@@ -239,3 +239,70 @@ def test_without_probabilities_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("filters", ["open", "greedy", "k_p_min", "hot", "cold"])
+@pytest.mark.parametrize("rows,V", [(33, 152064), (32, 98304), (31, 98303), (2, 1000003), (1, 3000001)])
+def test_either_side_of_the_split_into_parts(filters, rows, V):
+    """Up to 32 rows of 98304 to 2 million logits go in parts, others do not."""
+    say("sample sides %s %d %d" % (filters, rows, V))
+    rng = np.random.default_rng([rows, V])
+    base = normal(rng, rows, V)
+    verify(base, None, rows, 2, V, settings(rows, rng, **FILTERS[filters]))
+
+
+@pytest.mark.gpu
+def test_whole_rows_and_parts_draw_the_same():
+    """The same rows among more than 32, and alone; also where the workspace is not to be had."""
+    rng = np.random.default_rng(22)
+    rows, V = 40, 100000
+    base = normal(rng, rows, V)
+    base[3, ::2] = float("-inf")
+    base[4, ::3] = torch.finfo(torch.bfloat16).min
+    base[5] = (base[5].float() * 4).round().to(torch.bfloat16)        # ties
+    base[6, 7] = float("inf")
+    s = settings(rows, rng)
+    s["temperature"] = rng.choice([0.0, 0.5, 1.0, 3.0, 20.0, 100.0], rows).astype(np.float32)
+    s["top_p"] = rng.choice([0.5, 0.9, 1.0], rows).astype(np.float32)
+    s["min_p"] = rng.choice([0.0, 0.01], rows).astype(np.float32)
+    s["top_k"] = rng.choice([0, 5, 700], rows).astype(np.int32)
+    dev = base.cuda()
+    ids, p = draw(dev, None, rows, 2, V, s)
+    few = {k: v[:20].copy() for k, v in s.items()}
+    native.xpress_release()
+    got, q = draw(dev[:20], None, 20, 2, V, few)
+    assert np.array_equal(got, ids[:20]) and np.array_equal(q, p[:20])
+    native.xpress_release()
+    native.xpress_set_workspace_limit(1 << 10)
+    try:
+        got, q = draw(dev[:20], None, 20, 2, V, few)
+    finally:
+        native.xpress_set_workspace_limit(0)
+    assert np.array_equal(got, ids[:20]) and np.array_equal(q, p[:20])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("reserve", [False, True])
+def test_parts_in_a_graph(reserve):
+    rng = np.random.default_rng(23)
+    N, B, V = 1, 4, 100000
+    base, bias = normal(rng, 3, V).cuda(), normal(rng, 3, V, 0.5).cuda()
+    s = settings(3, rng, **FILTERS["p"])
+    want, _ = draw(base, bias, N, B, V, s)
+    dev = {k: torch.from_numpy(v).cuda() for k, v in s.items()}
+    blk = torch.zeros(N, B, dtype=torch.int64, device="cuda")
+    stream = torch.cuda.Stream()
+    if reserve:
+        native.xpress_sample_reserve(N, B, V, stream=stream)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        native.xpress_sample_to_blk(base, bias, blk, dev["temperature"], dev["top_k"], dev["top_p"],
+                                    dev["min_p"], dev["u"], N, B, V, V, V)
+    for _ in range(3):
+        blk.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)
+        draw(base, bias, N, B, V, s)

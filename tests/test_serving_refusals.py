@@ -207,3 +207,12 @@ def test_binding_checks_shapes_on_the_gpu():
         native.xpress_paged_attention(q4, kc, vc, table, lens, torch.empty_like(q4), 65)
     with pytest.raises(native.XpressError):      # out on q
         native.xpress_paged_attention(q4, kc, vc, table, lens, q4, 16)
+
+
+def test_sample_reserve_checks_its_sizes():
+    for bad in ((-1, 2, 1000), (1, 0, 1000), (1, 2, 0), (1, 2, 2 ** 31), (2 ** 31, 3, 1000), (2 ** 62, 2, 10)):
+        with pytest.raises(native.XpressError):
+            native.xpress_sample_reserve(*bad, stream=0)
+    # nothing is needed: no HIP call either
+    for none in ((0, 2, 152064), (5, 1, 152064), (100, 2, 152064), (1, 2, 20000)):
+        native.xpress_sample_reserve(*none, stream=0)

@@ -9,7 +9,8 @@
 // the row counts the values in LDS (exact, whatever the order of the atomics);
 // the exponentials are then taken once per distinct value, in 64 bits; and
 // the drawn token is the j-th id holding one known value.  No sort, no prefix
-// sum over the vocabulary.  A workgroup of 512 threads takes a row.
+// sum over the vocabulary.  A workgroup of 512 threads takes a row; few long rows
+// are counted in parts.
 //
 // Bins.  Magnitudes of 2^-26 to 2^16 have a 32-bit count each, for either sign:
 // 43 KB, so that two workgroups share a compute unit and one streams its row
@@ -28,8 +29,11 @@
 // The order's walk goes by segments of 64 values, largest first.  A wave takes
 // a segment at a time, one value per lane.
 //
-// Measured (V = 152064): 480 rows with bias 88 us, 3.3 TB/s; 15 rows 57 us; one row
-// without bias 37 us, the time of one workgroup from load to draw.
+// Bound: the rows' bytes where they are many; at the same time each compute
+// unit's LDS, which takes an add of a wave in some 15 cycles (2376 a row of
+// 152064, 16 us).  Measured at V = 152064: 480 rows with bias 74 us, 3.9 TB/s; 15
+// rows with bias 29 us, one row without 26 us, of which the counting takes 8 and
+// the exponentials and searches of one workgroup the rest.
 
 #include <hip/hip_runtime.h>
 
@@ -49,6 +53,8 @@ typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
+constexpr int kDrawThreads = 1024;               // where a row comes in parts
+constexpr int kMostWaves = kDrawThreads / 64;
 constexpr uint32_t kInf = 0x7F80u;               // magnitude bits of infinity
 constexpr uint32_t kOne = 0x3F80u;               // of 1
 constexpr uint32_t kLeast = kOne - 26u * 128u;   // of 2^-26
@@ -57,6 +63,8 @@ constexpr uint32_t kHuge = kRels + 1;            // all from 2^16 on
 constexpr uint32_t kSide = 5440;                 // bins of a sign, whole segments
 constexpr uint32_t kWindow = 10240;              // of the 65536 values, whole segments
 constexpr uint32_t kKeys = 10240;
+constexpr uint32_t kWidest = 5;                  // runs are of a wave's vectors at most
+constexpr uint32_t kMaxParts = 8;
 constexpr uint32_t kSegs = 1024;
 static_assert(kSide % 64 == 0 && kSide > kHuge && kWindow <= 2 * kSide && kWindow % 64 == 0, "bins");
 
@@ -68,6 +76,10 @@ struct SampleArgs {
     const int32_t* top_k;
     int64_t stride_base, stride_bias;
     uint32_t rows, bm1, V;
+    // a row in parts
+    uint32_t parts, part_vecs, list_room;
+    uint32_t* lists;   // [rows, parts, list_room]
+    uint4* infos;      // [rows, parts]: entries of the list, and what the counting saw
 };
 
 struct Shared {
@@ -75,11 +87,11 @@ struct Shared {
     uint16_t keys[kKeys];    // largest logit of a run, as int16 bits
     double mass[kSegs];      // mass of a segment; then: of all segments before it
     uint32_t count[kSegs];   // the same for logits
-    double wave_mass[kWaves];
-    double wave_min[kWaves];
-    uint32_t wave_count[kWaves];
-    uint32_t wave_low[kWaves];
-    int32_t wave_high[kWaves];
+    double wave_mass[kMostWaves];
+    double wave_min[kMostWaves];
+    uint32_t wave_count[kMostWaves];
+    uint32_t wave_low[kMostWaves];
+    int32_t wave_high[kMostWaves];
     uint16_t turns[kWaves][kKeys / 64 / kWaves + 1];
     double f64;
     uint32_t found, counted;
@@ -235,8 +247,10 @@ __device__ __forceinline__ double weight_of(double d, double t, double inv)
 
 // The draw of one row.  FULL: over all values, a window of whose counts the bins
 // hold; else the bins hold the counts of all values that can be drawn.
-template <bool VEC, bool BIAS, bool FULL>
+template <bool VEC, bool BIAS, bool FULL, int THREADS>
 struct Row {
+    static constexpr uint32_t kThreads = THREADS, kWaves = THREADS / 64;
+
     Shared& s;
     const Logits<VEC, BIAS>& z;
     uint32_t window;    // FULL: whose counts the bins hold
@@ -584,59 +598,52 @@ __device__ __forceinline__ uint32_t nth_bit(uint32_t bits, uint32_t nth)
     return (uint32_t)__ffs(bits) - 1u;
 }
 
-template <bool VEC, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
+// What the counting learns beside the counts: the largest logit (right where it is
+// not negative) and the smallest magnitude less 1.
+struct Seen {
+    int32_t high;
+    uint32_t tiny;
+};
+
+// Counts the vectors [v0, v1) of a row into the bins, which it clears.  KEYS: also
+// keeps the runs' largest logits, of 16 << wide each.
+template <bool VEC, bool BIAS, bool KEYS>
+__device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& z, uint32_t v0, uint32_t v1,
+                                            uint32_t cut, uint32_t wide)
 {
-    __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
-    const uint32_t V = a.V, vecs = (V + 7) / 8;
-    // logits of a run: 16 << wide; none where even a wave's vectors are too few
-    uint32_t wide = 0;
-    while ((vecs + (2u << wide) - 1) >> (wide + 1) > kKeys) ++wide;
-    const bool keyed = wide <= 5;
-
-    const uint32_t r = blockIdx.x;
-    const float temp = a.temperature[r];
-    const bool greedy = !(temp > 0.0f);
-    const double t = greedy ? 1.0 : (double)temp, inv = 1.0 / t;
-    const Logits<VEC, BIAS> z{a.base + (int64_t)r * a.stride_base,
-                              BIAS ? a.bias + (int64_t)r * a.stride_bias : nullptr, V};
-    int64_t* dst = a.blk + (r + r / a.bm1 + 1);
-
-    // 1. count.  The cut c is 2^12 .. 2^16, at least 1492 temperatures.
-    uint32_t c = kOne + 12u * 128u;
-    while (c < kOne + 16u * 128u && (double)value_of(c) < 1492.0 * t) c += 128u;
-    const uint32_t cut = 0x8000u | c;
-    for (uint32_t i = tid * 4; i < 2 * kSide; i += kThreads * 4) {
-        *reinterpret_cast<u32x4*>(&s.bins[i]) = u32x4{0, 0, 0, 0};
-    }
-    constexpr int kAhead = BIAS ? 4 : 8;     // vectors of a thread in flight
+    constexpr int kAhead = BIAS || !KEYS ? 4 : 8;  // vectors of a thread in flight
     u32x4 got[kAhead], add[kAhead];
-    const uint32_t whole = VEC ? V / 8 : 0;  // vectors that are loaded whole
-    // loads are queued always (past the row, its last vector again)
+    const uint32_t whole = VEC ? min(v1, z.V / 8) : 0;  // the vectors below it are loaded whole
+    // loads are queued always (past the range, its last vector again)
     auto fetch = [&](int x, uint32_t v) {
         const uint32_t e = min(v, whole - 1) * 8;
         got[x] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.base + e));
         if constexpr (BIAS) add[x] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.bias + e));
     };
+    Seen seen = {INT16_MIN, 0};
     u16x2 least = {0xFFFFu, 0xFFFFu};
-    int32_t high = INT16_MIN;
     auto take = [&](const u32x4& y, uint32_t v) {
         int32_t key = tally(s, y, cut, &least);
-        high = max(high, key);
-        if (keyed) {
-            key = max(key, (int32_t)dpp_u32<0xB1>((uint32_t)key));   // lane ^ 1
-            for (uint32_t d = 2; d < 2u << wide; d <<= 1) key = max(key, __shfl_xor(key, d));
-            if ((v & ((2u << wide) - 1)) == 0 && v < vecs) s.keys[v >> (wide + 1)] = (uint16_t)key;
+        seen.high = max(seen.high, key);
+        if constexpr (KEYS) {
+            if (wide <= kWidest) {
+                key = max(key, (int32_t)dpp_u32<0xB1>((uint32_t)key));   // lane ^ 1
+                for (uint32_t d = 2; d < 2u << wide; d <<= 1) key = max(key, __shfl_xor(key, d));
+                if ((v & ((2u << wide) - 1)) == 0 && v < v1) s.keys[v >> (wide + 1)] = (uint16_t)key;
+            }
         }
     };
-    if (VEC && whole > 0) {
+    const bool some = VEC && whole > v0;
+    if (some) {
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) fetch(x, tid + x * kThreads);
+        for (int x = 0; x < kAhead; ++x) fetch(x, v0 + tid + x * kThreads);
+    }
+    for (uint32_t i = tid * 4; i < 2 * kSide; i += kThreads * 4) {
+        *reinterpret_cast<u32x4*>(&s.bins[i]) = u32x4{0, 0, 0, 0};
     }
     __syncthreads();
-    // Every lane takes part in every vector (as NaN past the row), for the runs.
-    const uint32_t round = (vecs + kThreads - 1) / kThreads * kThreads;
+    // Every lane takes part in every vector (as NaN past the range), for the runs.
     auto arrived = [&](int x) {
         u32x4 y = got[x];
         if constexpr (BIAS) {
@@ -645,83 +652,175 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         }
         return y;
     };
-    uint32_t done = 0;  // vectors of all threads
+    auto slow = [&](uint32_t v) { return z.at(v < v1 ? v * 8 : z.V); };
+    uint32_t at = v0;  // of all threads
     if (VEC) {
-        for (; done + kAhead * kThreads <= whole; done += kAhead * kThreads) {
+        for (; at + kAhead * kThreads <= whole; at += kAhead * kThreads) {
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
                 const u32x4 y = arrived(x);
-                const uint32_t v = done + x * kThreads + tid;
+                const uint32_t v = at + x * kThreads + tid;
                 fetch(x, v + kAhead * kThreads);
                 take(y, v);
             }
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-            if (whole > 0 && done < whole) {
-                const uint32_t v = done + tid;
-                take(v < whole ? arrived(x) : z.at(min(v * 8, V)), v);
-                done += kThreads;
+            if (some && at < whole) {
+                const uint32_t v = at + tid;
+                take(v < whole ? arrived(x) : slow(v), v);
+                at += kThreads;
             }
         }
     }
-    for (; done < round; done += kThreads) take(z.at(min((done + tid) * 8, V)), done + tid);
-    const uint32_t low = min((uint32_t)least.x, (uint32_t)least.y);
-    {
-        uint32_t l = low;
-        int32_t h = high;
-        for (int m = 32; m; m >>= 1) {
-            l = min(l, __shfl_xor(l, m));
-            h = max(h, __shfl_xor(h, m));
-        }
-        if (lane == 0) {
-            s.wave_low[wave] = l;
-            s.wave_high[wave] = h;
-        }
+    for (; at < v1; at += kThreads) take(slow(at + tid), at + tid);
+    seen.tiny = min((uint32_t)least.x, (uint32_t)least.y);
+    for (int m = 32; m; m >>= 1) {
+        seen.tiny = min(seen.tiny, __shfl_xor(seen.tiny, m));
+        seen.high = max(seen.high, __shfl_xor(seen.high, m));
+    }
+    if (lane == 0) {
+        s.wave_low[wave] = seen.tiny;
+        s.wave_high[wave] = seen.high;
     }
     __syncthreads();
-    uint32_t tiny = 0xFFFFu;
     for (uint32_t w = 0; w < kWaves; ++w) {
-        tiny = min(tiny, s.wave_low[w]);
-        high = max(high, s.wave_high[w]);
+        seen.tiny = min(seen.tiny, s.wave_low[w]);
+        seen.high = max(seen.high, s.wave_high[w]);
     }
+    return seen;
+}
 
-    // 2. choose a value
-    uint32_t want = 0, nth = 0;
-    double p = 0.0;
-    bool usual = tiny >= kLeast - 1 && s.bins[kHuge] == 0 && 1492.0 * t <= (double)value_of(c);
-    if (usual) {
-        Row<VEC, BIAS, false> row{s, z, 0, 0, 0.0, t, inv};
+// The cut of a temperature: bits of c = 2^12 .. 2^16, at least 1492 temperatures
+// if that is in the range.
+__device__ __forceinline__ uint32_t cut_of(double t)
+{
+    uint32_t c = kOne + 12u * 128u;
+    while (c < kOne + 16u * 128u && (double)value_of(c) < 1492.0 * t) c += 128u;
+    return c;
+}
+
+struct Drawn {
+    uint32_t want, nth;   // value bits, and which of its ids
+    double p;
+    bool usual, none;     // from the bins of all drawable values; nothing to draw
+};
+
+// Draws a value from the counts in the bins, or from the row counted again.
+template <int THREADS, bool VEC, bool BIAS>
+__device__ __forceinline__ Drawn draw(Shared& s, const SampleArgs& a, const Logits<VEC, BIAS>& z, uint32_t r,
+                                      const Seen& seen, uint32_t c, bool greedy, double t)
+{
+    const double inv = 1.0 / t;
+    Drawn d = {0, 0, 0.0, false, false};
+    d.usual = seen.tiny >= kLeast - 1 && s.bins[kHuge] == 0 && 1492.0 * t <= (double)value_of(c);
+    if (d.usual) {
+        Row<VEC, BIAS, false, THREADS> row{s, z, 0, 0, 0.0, t, inv};
         // a positive maximum is known already
-        const uint32_t top = high > 0 ? kSide - 1 - ((uint32_t)high - (kLeast - 1)) : row.find_top();
+        const uint32_t top = seen.high > 0 ? kSide - 1 - ((uint32_t)seen.high - (kLeast - 1)) : row.find_top();
         const uint32_t h = row.bits_at(top);
-        usual = top < row.kOrder && (h < 0x8000u || (h & 0x7FFFu) < c - 128u);
-        if (usual) {
+        d.usual = top < row.kOrder && (h < 0x8000u || (h & 0x7FFFu) < c - 128u);
+        if (d.usual) {
             row.top = top;
             row.zmax = (double)value_of(h);
-            p = row.choose(a, r, greedy, &want, &nth);
+            d.p = row.choose(a, r, greedy, &d.want, &d.nth);
         }
     }
-    if (!usual) {
-        Row<VEC, BIAS, true> row{s, z, 0xFFFFu, 0, 0.0, t, inv};
+    if (!d.usual) {
+        Row<VEC, BIAS, true, THREADS> row{s, z, 0xFFFFu, 0, 0.0, t, inv};
         const uint32_t top = row.find_top();
-        if (top >= row.kOrder) {  // nothing but NaN and -inf
-            if (tid == 0) {
-                *dst = 0;
-                if (a.prob) a.prob[r] = 0.0f;
-            }
-            return;
+        d.none = top >= row.kOrder;  // nothing but NaN and -inf
+        if (!d.none) {
+            row.top = top;
+            row.zmax = (double)value_of(all_bits_at(top));
+            d.p = row.choose(a, r, greedy, &d.want, &d.nth);
         }
-        row.top = top;
-        row.zmax = (double)value_of(all_bits_at(top));
-        p = row.choose(a, r, greedy, &want, &nth);
     }
     __syncthreads();
+    return d;
+}
 
-    // 3. the nth id (in id order) that holds the value, among the runs that reach
+// The nth id (in id order) of vectors [v0, v1) that holds the value: each wave
+// counts its share, then the share with the id is walked.
+template <int THREADS, bool VEC, bool BIAS>
+__device__ __forceinline__ void walk(Shared& s, const Logits<VEC, BIAS>& z, uint32_t v0, uint32_t v1, uint32_t want,
+                                     uint32_t nth, int64_t* dst)
+{
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const uint32_t steps = (v1 - v0 + THREADS - 1) / THREADS;  // of 64 vectors per wave
+    auto look = [&](uint32_t i) {
+        const uint32_t v = v0 + (wave * steps + i) * 64 + lane;
+        return z.at(i < steps && v < v1 ? v * 8 : z.V);
+    };
+    uint32_t mine = 0;
+    for (uint32_t i = 0; i < steps; i += 4) {
+        u32x4 y[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) y[x] = look(i + x);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mine += __popc(matches(y[x], want));
+    }
+    mine = wave_add(mine);
+    if (lane == 0) s.wave_count[wave] = mine;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < wave; ++w) before += s.wave_count[w];
+    if (before <= nth && nth < before + mine) {
+        uint32_t left = nth - before;
+        for (uint32_t i = 0; i < steps; ++i) {
+            const uint32_t m = matches(look(i), want), n = __popc(m);
+            uint32_t to = n;
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t o = __shfl_up(to, d);
+                if ((int)lane >= d) to += o;
+            }
+            const uint32_t all = __shfl(to, 63);
+            if (left < all) {
+                if (to - n <= left && left < to) {
+                    const uint32_t v = v0 + (wave * steps + i) * 64 + lane;
+                    *dst = (int64_t)(v * 8 + nth_bit(m, left - (to - n)));
+                }
+                break;
+            }
+            left -= all;
+        }
+    }
+}
+
+template <bool VEC, bool BIAS>
+__device__ __forceinline__ Logits<VEC, BIAS> logits_of(const SampleArgs& a, uint32_t r)
+{
+    return {a.base + (int64_t)r * a.stride_base, BIAS ? a.bias + (int64_t)r * a.stride_bias : nullptr, a.V};
+}
+
+// A workgroup a row.
+template <bool VEC, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
+{
+    __shared__ Shared s;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64, r = blockIdx.x;
+    const uint32_t V = a.V, vecs = (V + 7) / 8;
+    uint32_t wide = 0;
+    while ((vecs + (2u << wide) - 1) >> (wide + 1) > kKeys) ++wide;
+    const float temp = a.temperature[r];
+    const bool greedy = !(temp > 0.0f);
+    const double t = greedy ? 1.0 : (double)temp;
+    const Logits<VEC, BIAS> z = logits_of<VEC, BIAS>(a, r);
+    int64_t* dst = a.blk + (r + r / a.bm1 + 1);
+
+    const uint32_t c = cut_of(t);
+    const Seen seen = count_range<VEC, BIAS, true>(s, z, 0, vecs, 0x8000u | c, wide);
+    const Drawn d = draw<kThreads>(s, a, z, r, seen, c, greedy, t);
+    if (tid == 0 && a.prob) a.prob[r] = (float)d.p;
+    if (d.none) {
+        if (tid == 0) *dst = 0;
+        return;
+    }
+    const uint32_t want = d.want, nth = d.nth;
+    // The nth id (in id order) that holds the value, among the runs that reach
     // it: a wave lists those of its share in order, counts their matches 64 runs
     // at a time, and the one with the id looks at its 64 again.
-    if (usual && keyed && want > 0 && want < 0x8000u) {
+    if (d.usual && wide <= kWidest && want > 0 && want < 0x8000u) {
         const uint32_t runs = (vecs + (2u << wide) - 1) >> (wide + 1);
         const uint32_t share = (runs + kWaves * 64 - 1) / (kWaves * 64) * 64, first = wave * share;
         uint32_t* list = s.bins + first;   // the bins are not needed any more
@@ -784,7 +883,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
                     const uint32_t m = matches(z.at(x * 8), want), k = __popc(m);
                     if (left < k) {
                         *dst = (int64_t)(x * 8 + nth_bit(m, left));
-                        if (a.prob) a.prob[r] = (float)p;
                         break;
                     }
                     left -= k;
@@ -793,52 +891,136 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         }
         return;
     }
-    // Else each wave counts its share of the row, then the share with the id
-    // is walked.
-    const uint32_t steps = (V + kWaves * 512 - 1) / (kWaves * 512);  // of 512 logits per wave
-    uint32_t mine = 0;
-    for (uint32_t i = 0; i < steps; i += 4) {
-        u32x4 y[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint32_t e = (wave * steps + i + x) * 512 + lane * 8;
-            y[x] = z.at(i + x < steps ? min(e, V) : V);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) mine += __popc(matches(y[x], want));
-    }
-    for (int m = 32; m; m >>= 1) mine += __shfl_xor(mine, m);
-    if (lane == 0) s.wave_count[wave] = mine;
+    walk<kThreads>(s, z, 0, vecs, want, nth, dst);
+}
+
+// Few rows: a.parts workgroups count a row's parts, and list the bins that are
+// not 0, as bin << 18 | count; one workgroup a row then adds the lists up and
+// draws, and looks for the id in the one part that has it.
+template <bool VEC, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 4) count_kernel(SampleArgs a)
+{
+    __shared__ Shared s;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, r = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    const uint32_t vecs = (a.V + 7) / 8, v0 = min(part * a.part_vecs, vecs), v1 = min(v0 + a.part_vecs, vecs);
+    const float temp = a.temperature[r];
+    const uint32_t c = cut_of(temp > 0.0f ? (double)temp : 1.0);
+    const Seen seen = count_range<VEC, BIAS, false>(s, logits_of<VEC, BIAS>(a, r), v0, v1, 0x8000u | c, 0);
+    if (tid == 0) s.found = 0;
     __syncthreads();
-    uint32_t before = 0;
-    for (uint32_t w = 0; w < wave; ++w) before += s.wave_count[w];
-    if (before <= nth && nth < before + mine) {
-        uint32_t left = nth - before;
-        for (uint32_t i = 0; i < steps; ++i) {
-            const uint32_t e = (wave * steps + i) * 512 + lane * 8;
-            const uint32_t m = e < V ? matches(z.at(e), want) : 0, n = __popc(m);
-            uint32_t to = n;
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t o = __shfl_up(to, d);
-                if ((int)lane >= d) to += o;
-            }
-            const uint32_t all = __shfl(to, 63);
-            if (left < all) {
-                if (to - n <= left && left < to) {
-                    *dst = (int64_t)(e + nth_bit(m, left - (to - n)));
-                    if (a.prob) a.prob[r] = (float)p;
-                }
-                break;
-            }
-            left -= all;
-        }
+    uint32_t* list = a.lists + (int64_t)blockIdx.x * a.list_room;
+    for (uint32_t i0 = 0; i0 < 2 * kSide; i0 += kThreads) {
+        const uint32_t i = i0 + tid, n = i < 2 * kSide ? s.bins[i] : 0;
+        const uint64_t on = __ballot(n != 0);
+        uint32_t at = 0;
+        if (lane == 0 && on) at = atomicAdd(&s.found, (uint32_t)__popcll(on));
+        at = __shfl(at, 0) + (uint32_t)__popcll(on & ((1ull << lane) - 1));
+        if (n != 0) list[at] = i << 18 | n;
     }
+    __syncthreads();
+    // whole quadruples
+    if (tid < 4 && (s.found + tid) / 4 == s.found / 4 && s.found % 4 != 0) list[s.found + tid] = 0;
+    if (tid == 0) {
+        a.infos[blockIdx.x] = uint4{s.found, seen.tiny, (uint32_t)seen.high, 0};
+    }
+}
+
+template <bool VEC, bool BIAS>
+__global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a)
+{
+    __shared__ Shared s;
+    __shared__ uint32_t held[kMaxParts];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, r = blockIdx.x;
+    const uint32_t vecs = (a.V + 7) / 8;
+    const float temp = a.temperature[r];
+    const bool greedy = !(temp > 0.0f);
+    const double t = greedy ? 1.0 : (double)temp;
+    const Logits<VEC, BIAS> z = logits_of<VEC, BIAS>(a, r);
+    int64_t* dst = a.blk + (r + r / a.bm1 + 1);
+    for (uint32_t i = tid * 4; i < 2 * kSide; i += kDrawThreads * 4) {
+        *reinterpret_cast<u32x4*>(&s.bins[i]) = u32x4{0, 0, 0, 0};
+    }
+    if (tid < kMaxParts) held[tid] = 0;
+    __syncthreads();
+    // a wave's list: two waves a part, four entries a lane
+    static_assert(kMaxParts * 2 * 64 == kDrawThreads, "waves of a part");
+    const uint32_t part = tid / 128;
+    const u32x4* list = reinterpret_cast<const u32x4*>(a.lists + (int64_t)(r * a.parts + part) * a.list_room);
+    const uint32_t quads = (a.infos[r * a.parts + part].x + 3) / 4;
+    auto each = [&](auto use) {
+        for (uint32_t i = tid % 128; i < quads; i += 4 * 128) {
+            u32x4 e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e[x] = i + x * 128 < quads ? list[i + x * 128] : u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) use(e[x][y] >> 18, e[x][y] & 0x3FFFFu);
+        }
+    };
+    each([&](uint32_t bin, uint32_t n) {
+        if (n) atomicAdd(&s.bins[bin], n);
+    });
+    Seen seen = {INT16_MIN, 0xFFFFu};
+    for (uint32_t p = 0; p < a.parts; ++p) {
+        const uint4 info = a.infos[r * a.parts + p];
+        seen.tiny = min(seen.tiny, info.y);
+        seen.high = max(seen.high, (int32_t)info.z);
+    }
+    __syncthreads();
+    const Drawn d = draw<kDrawThreads>(s, a, z, r, seen, cut_of(t), greedy, t);
+    if (tid == 0 && a.prob) a.prob[r] = (float)d.p;
+    if (d.none) {
+        if (tid == 0) *dst = 0;
+        return;
+    }
+    uint32_t v0 = 0, v1 = vecs, nth = d.nth;
+    if (d.usual) {
+        // the parts' numbers of the value (either zero for +0)
+        const uint32_t mag = d.want & 0x7FFFu, rel = mag ? mag - (kLeast - 1) : 0;
+        const uint32_t bin = rel + (d.want >> 15) * kSide;
+        uint32_t count = 0;
+        each([&](uint32_t at, uint32_t n) {
+            if (at == bin || (rel == 0 && at == kSide)) count += n;
+        });
+        count = wave_add(count);
+        if (lane == 0 && count) atomicAdd(&held[part], count);
+        __syncthreads();
+        uint32_t p = 0;
+        while (p + 1 < a.parts && nth >= held[p]) nth -= held[p++];
+        v0 = min(p * a.part_vecs, vecs);
+        v1 = min(v0 + a.part_vecs, vecs);
+    }
+    walk<kDrawThreads>(s, z, v0, v1, d.want, nth, dst);
+}
+
+// Long rows go in parts while their number leaves most compute units idle: a row
+// of 152064 in 27 us where one workgroup takes 33 (32 rows: 30 and 36, 64 rows: 36
+// both; rows of 100000: 25 and 27, 64 of them 32 and 30; of 50000: 24 and 20).
+void plan_parts(SampleArgs* a)
+{
+    a->part_vecs = ((a->V + 7) / 8 + kMaxParts - 1) / kMaxParts;
+    a->parts = a->V >= 98304u && a->part_vecs < (1u << 15) && a->rows <= 32 ? kMaxParts : 1;  // counts in 18 bits
+    a->list_room = a->part_vecs * 8 < 2 * kSide ? a->part_vecs * 8 : 2 * kSide;   // quadruples
+}
+
+// Workspace words (8 bytes) of rows in parts.
+int64_t part_words(const SampleArgs& a)
+{
+    return a.parts > 1 ? (int64_t)a.rows * a.parts * (2 + (a.list_room + 1) / 2) : 0;
 }
 
 template <bool VEC, bool BIAS>
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((sample_kernel<VEC, BIAS>), dim3(a.rows), dim3(kThreads), 0, stream, a);
+    if (a.parts > 1) {
+        hipLaunchKernelGGL((count_kernel<VEC, BIAS>), dim3(a.rows * a.parts), dim3(kThreads), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((draw_kernel<VEC, BIAS>), dim3(a.rows), dim3(kDrawThreads), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((sample_kernel<VEC, BIAS>), dim3(a.rows), dim3(kThreads), 0, stream, a);
+    }
     return hipGetLastError();
 }
 
@@ -898,6 +1080,19 @@ extern "C" int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, 
     a.rows = (uint32_t)rows;
     a.bm1 = (uint32_t)(B - 1);
     a.V = (uint32_t)V;
+    plan_parts(&a);
+    if (a.parts > 1) {
+        // Without the memory, or in a capture that would have to allocate it, the
+        // rows go in one part each: the same draws, later.
+        uint64_t* table = nullptr;
+        if (xpress::workspace_table(stream, part_words(a), &table) == XPRESS_OK) {
+            a.infos = reinterpret_cast<uint4*>(table);
+            a.lists = reinterpret_cast<uint32_t*>(a.infos + (int64_t)a.rows * a.parts);
+        } else {
+            (void)hipGetLastError();
+            a.parts = 1;
+        }
+    }
     const bool vec = xpress::is_aligned16(base) && (rows == 1 || stride_base_r % 8 == 0) &&
                      (!bias || (xpress::is_aligned16(bias) && (rows == 1 || stride_bias_r % 8 == 0)));
     hipError_t e;
@@ -907,4 +1102,18 @@ extern "C" int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, 
         e = bias ? launch_sample<false, true>(a, stream) : launch_sample<false, false>(a, stream);
     }
     return e == hipSuccess ? XPRESS_OK : xpress::hip_fail(e);
+}
+
+extern "C" int xpress_sample_reserve(int64_t N, int64_t B, int64_t V, hipStream_t stream)
+{
+    if (N < 0 || B < 1 || V < 1 || V > 0x7FFFFFFFll) return XPRESS_EINVAL;
+    if (B - 1 > 0 && N > 0x7FFFFFFFll / (B - 1)) return XPRESS_EINVAL;
+    SampleArgs a = {};
+    a.rows = (uint32_t)(N * (B - 1));
+    a.V = (uint32_t)V;
+    if (a.rows == 0) return XPRESS_OK;
+    plan_parts(&a);
+    if (a.parts == 1) return XPRESS_OK;
+    uint64_t* table = nullptr;
+    return xpress::workspace_table(stream, part_words(a), &table);
 }

@@ -113,6 +113,8 @@ def load():
         lib.xpress_paged_attention_plan.restype = i32
         lib.xpress_sample_to_blk.argtypes = [vp] * 9 + [i64] * 5 + [vp]
         lib.xpress_sample_to_blk.restype = i32
+        lib.xpress_sample_reserve.argtypes = [i64, i64, i64, vp]
+        lib.xpress_sample_reserve.restype = i32
         lib.xpress_last_hip_error.argtypes = []
         lib.xpress_last_hip_error.restype = i32
         lib.xpress_error_string.argtypes = [i32]
@@ -576,6 +578,13 @@ def xpress_sample_to_blk(base, bias, blk, temperature, top_k, top_p, min_p, u, N
                                        _ptr(u), int(N), int(B), int(V), int(stride_base_r),
                                        int(stride_bias_r), _stream(stream)),
            "xpress_sample_to_blk")
+
+
+def xpress_sample_reserve(N: int, B: int, V: int, stream=None) -> None:
+    """Grow the (device, stream) workspace to what xpress_sample_to_blk needs to
+    spread few rows over the chip, as before a capture."""
+    _check(load().xpress_sample_reserve(int(N), int(B), int(V), _stream(stream)),
+           "xpress_sample_reserve")
 
 
 def xpress_last_hip_error() -> int:
