@@ -7,6 +7,11 @@ addresses; for a tensor the binding also checks that its storage covers the
 bytes the call will touch, which a bare pointer cannot tell the library.  A
 nonzero status raises :class:`XpressError`.  If the library has not been
 built, the first call raises -- there is no fallback path.
+
+The serving operators take their arguments from torch tensors in a small host
+module, ``_marshal.so`` (4 us a call; asking the tensors in Python takes 10); the
+Python code here makes the call where an argument is not a regular tensor, and
+says what is wrong with it.
 """
 from __future__ import annotations
 
@@ -115,6 +120,9 @@ def load():
         lib.xpress_sample_to_blk.restype = i32
         lib.xpress_sample_reserve.argtypes = [i64, i64, i64, vp]
         lib.xpress_sample_reserve.restype = i32
+        lib.append_at, lib.attention_at, lib.sample_at = [
+            ctypes.cast(f, vp).value for f in (lib.xpress_kv_append, lib.xpress_paged_attention,
+                                               lib.xpress_sample_to_blk)]
         lib.xpress_last_hip_error.argtypes = []
         lib.xpress_last_hip_error.restype = i32
         lib.xpress_error_string.argtypes = [i32]
@@ -161,6 +169,16 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _stream_of_tensors(stream):
+    """The same for a call with tensors: before the GPU is in use there is none of
+    them on it, and the handle goes nowhere."""
+    if stream is None:
+        if not _torch.cuda.is_initialized():
+            return 0
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+    return _stream(stream)
 
 
 def _check(status: int, where: str):
@@ -384,14 +402,23 @@ _KV_CACHE = "5Q11q"
 _APPEND_ARGS = struct.Struct(_KV_CACHE + "7Q14q")
 _ATTENTION_ARGS = struct.Struct(_KV_CACHE + "4Q5qd6q")
 _torch = None
+_marshal = None
 _types = {}
 
 
 def _use_torch():
-    """torch, imported by the first call that takes tensors only."""
-    global _torch
+    """torch, imported by the first call that takes tensors only, and the host
+    module whose functions make a call from tensors (None: the arguments are not
+    what they should be, and the Python code after it says why)."""
+    global _torch, _marshal
     if _torch is None:
         import torch
+        try:
+            from . import _marshal as marshal
+        except ImportError as e:
+            raise ImportError("_marshal.so is not built for this torch; run `python -m "
+                              "vocab_wide_add_amd.build`") from e
+        _marshal = marshal
         _types.update({torch.bfloat16: XPRESS_BF16, torch.float16: XPRESS_FP16,
                        torch.float8_e4m3fn: XPRESS_E4M3})
         _torch = torch
@@ -480,7 +507,11 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
     tokens of each sequence in order); k_scale, v_scale fp32 [heads].  See the
     header for the definition.
     """
-    torch = _use_torch()
+    torch, lib = _torch or _use_torch(), _lib or load()
+    status = _marshal.kv_append(lib.append_at, _stream_of_tensors(stream), q, k, v, q_out, k_cache, v_cache, page_table,
+                                positions, cos_sin, seq_of, k_scale, v_scale, interleaved)
+    if status is not None:
+        return _check(status, "xpress_kv_append")
     shape, dev = k.shape, k_cache.get_device()
     T, heads, dim = shape
     cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
@@ -505,7 +536,7 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
         *cache, qp, kp, vp, op, _plain(positions, "positions", i32, (T,), dev),
         _plain(seq_of, "seq_of", i32, (T,), dev), cp, T, hq, code, rot, max_pos,
         1 if interleaved else 0, qt, qh, kt, kh, vt, vh, ot, oh)
-    _check((_lib or load()).xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
+    _check(lib.xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
 
 
 def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: int, lse=None,
@@ -520,7 +551,11 @@ def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: 
     keys a query sees back from itself (0: all).  See the header for the
     definition.
     """
-    torch = _use_torch()
+    torch, lib = _torch or _use_torch(), _lib or load()
+    status = _marshal.paged_attention(lib.attention_at, _stream_of_tensors(stream), q, k_cache, v_cache, page_table, lens,
+                                      out, lse, k_scale, v_scale, max_len, window, scale)
+    if status is not None:
+        return _check(status, "xpress_paged_attention")
     shape, dev = q.shape, k_cache.get_device()
     N, Q, hq, dim = shape
     cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
@@ -534,7 +569,7 @@ def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: 
         *cache, qp, op, _plain(lse, "lse", torch.float32, (N, Q, hq), dev),
         _plain(lens, "lens", torch.int32, (N,), dev), Q, hq, code, int(max_len), int(window),
         1.0 / math.sqrt(dim) if scale is None else float(scale), qn, qi, qh, on, oi, oh)
-    _check((_lib or load()).xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
+    _check(lib.xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
 
 
 def xpress_paged_attention_reserve(N: int, Q: int, Hq: int, heads: int, dim: int, max_len: int,
@@ -564,6 +599,13 @@ def xpress_sample_to_blk(base, bias, blk, temperature, top_k, top_p, min_p, u, N
     number u[r]; prob[r], its probability.  bias may be None.  temperature,
     top_p, min_p, u, prob fp32 and top_k int32, one per row.
     """
+    lib = _lib or load()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.sample(lib.sample_at, _stream_of_tensors(stream), base, bias, blk, prob, temperature, top_k, top_p,
+                             min_p, u, N, B, V, stride_base_r, stride_bias_r)
+    if status is not None:
+        return _check(status, "xpress_sample_to_blk")
     rows = int(N) * (int(B) - 1)
     if rows > 0:
         _span(base, ((rows - 1) * int(stride_base_r) + int(V)) * 2, "base")
