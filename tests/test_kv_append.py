@@ -207,3 +207,28 @@ def test_prompts_with_more_work_than_threads(cache, layout):
     made = build(rng, [700, 1, 901], [700, 1, 901], 32, 8, 128, 32, 16, "bf16", cache, layout)
     assert sum((700, 1, 901)) * 48 * 8 > 1 << 19
     check(*made, 32, 8, 128, True)
+
+
+@pytest.mark.gpu
+def test_places_past_32_bits():
+    """A pool of more than 2^32 elements with the sequence on its last pages."""
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of GPU memory")
+    rng = np.random.default_rng(9)
+    rows, kc, vc, table, pos, seq, cs, sc = build(rng, [60], [9], 4, 2, 128, 128, 16, "bf16", "bf16")
+    pages = (2 ** 32) // (2 * 16 * 128) + 64
+    shift = pages - kc.shape[0]
+    dev = rows.cuda()
+    q, k, v = dev[:, :4], dev[:, 4:6], dev[:, 6:]
+    small = [torch.zeros(9, 4, 128, dtype=torch.bfloat16, device="cuda"), kc.cuda(), vc.cuda()]
+    native.xpress_kv_append(q, k, v, *small, table.cuda(), pos.cuda(), cs.cuda())
+    big = [torch.zeros(pages, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for b, x in zip(big, (kc, vc)):
+        b[shift:] = x.cuda()
+    out = torch.zeros_like(small[0])
+    native.xpress_kv_append(q, k, v, out, *big, torch.where(table >= 0, table + shift, table).cuda(), pos.cuda(),
+                            cs.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(out, small[0])
+    for b, x in zip(big, small[1:]):
+        assert torch.equal(b[shift:], x) and not b[:shift].any()

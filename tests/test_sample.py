@@ -306,3 +306,44 @@ def test_parts_in_a_graph(reserve):
         torch.cuda.synchronize()
         assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)
         draw(base, bias, N, B, V, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [3000, 152064])
+def test_rows_past_32_bits(V):
+    """Rows 2^31 elements apart."""
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GiB of GPU memory")
+    rng = np.random.default_rng([24, V])
+    stride = 2 ** 31 + 8
+    rows = normal(rng, 3, V)
+    base = torch.empty(2 * stride + V, dtype=torch.bfloat16, device="cuda")
+    for r in range(3):
+        base[r * stride:r * stride + V] = rows[r].cuda()
+    s = settings(3, rng, **FILTERS["p"])
+    want = draw(rows.cuda(), None, 1, 4, V, s)
+    got = draw(base.as_strided((3, V), (stride, 1)), None, 1, 4, V, s)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Rows in parts on two streams, each with a workspace of its own."""
+    rng = np.random.default_rng(25)
+    V = 120000
+    sets = []
+    for i in range(2):
+        base = normal(rng, 6, V)
+        s = settings(6, rng, **FILTERS["k_p_min"])
+        sets.append((base.cuda(), {k: torch.from_numpy(v).cuda() for k, v in s.items()},
+                     draw(base.cuda(), None, 2, 4, V, s)[0]))
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(4):
+        out = [torch.zeros(2, 4, dtype=torch.int64, device="cuda") for _ in sets]
+        torch.cuda.synchronize()
+        for (base, d, _), blk, stream in zip(sets, out, streams):
+            native.xpress_sample_to_blk(base, None, blk, d["temperature"], d["top_k"], d["top_p"], d["min_p"],
+                                        d["u"], 2, 4, V, V, stream=stream)
+        torch.cuda.synchronize()
+        for (_, _, want), blk in zip(sets, out):
+            assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)
