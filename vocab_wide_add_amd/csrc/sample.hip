@@ -14,12 +14,12 @@
 //
 // Bins.  Magnitudes of 2^-26 to 2^16 have a 32-bit count each, for either sign:
 // 43 KB, so that two workgroups share a compute unit and one streams its row
-// while the other draws.  Values below -c are not counted, c = 2^12 or more by
-// the temperature: next to a maximum above -c / 2 their weight is at most
-// exp(-746), 0 in 64 bits (masks are such values, and counting them would send
-// every lane to one word).  A row with anything else (a tinier value that is
-// not 0, 2^16 or more, a maximum too low, a temperature above 43) is counted
-// again over all 65536 values, in seven windows of the order, a pass for each.
+// while the other draws.  Values of -2^16 and below (masks) go to words that
+// are not looked at, one for each lane: next to a maximum above -2^15, at a
+// temperature of 2^15 / 746 or less, their weight is at most exp(-746), 0 in 64
+// bits.  A row with anything else (a tinier value that is not 0, 2^16 or more, a
+// lower maximum, a higher temperature) is counted again over all 65536 values,
+// in seven windows of the order, a pass for each.
 //
 // The j-th id.  While the row goes by, the largest of each 16 logits is kept
 // (in 16 bits; a run doubles with every doubling of the row past 163840): only
@@ -29,11 +29,12 @@
 // The order's walk goes by segments of 64 values, largest first.  A wave takes
 // a segment at a time, one value per lane.
 //
-// Bound: the rows' bytes where they are many; at the same time each compute
-// unit's LDS, which takes an add of a wave in some 15 cycles (2376 a row of
-// 152064, 16 us).  Measured at V = 152064: 480 rows with bias 74 us, 3.9 TB/s; 15
-// rows with bias 29 us, one row without 26 us, of which the counting takes 8 and
-// the exponentials and searches of one workgroup the rest.
+// Bound: many rows by their bytes, by the vector instructions (some 12 a logit in
+// all, half of the time) and by how little of a row's draw overlaps with the two
+// rows' counting, none of them alone; few rows by the chain of one workgroup.
+// Measured at V = 152064: 480 rows with bias 73 us, 4.0 TB/s; 15 rows with bias
+// 28 us and one without 26 us, 8 of them the counting, the rest the exponentials
+// and searches of one workgroup.
 
 #include <hip/hip_runtime.h>
 
@@ -59,14 +60,16 @@ constexpr uint32_t kInf = 0x7F80u;               // magnitude bits of infinity
 constexpr uint32_t kOne = 0x3F80u;               // of 1
 constexpr uint32_t kLeast = kOne - 26u * 128u;   // of 2^-26
 constexpr uint32_t kRels = 42u * 128u;           // magnitudes up to 2^16: 1 .. kRels; 0 is zero
-constexpr uint32_t kHuge = kRels + 1;            // all from 2^16 on
+constexpr uint32_t kHuge = kRels + 1;            // all from 2^16 on: this and 62 more
+constexpr uint32_t kTwo16 = kOne + 16u * 128u;   // magnitude bits of 2^16
+constexpr double kHottest = 32768.0 / 746.0;
 constexpr uint32_t kSide = 5440;                 // bins of a sign, whole segments
 constexpr uint32_t kWindow = 10240;              // of the 65536 values, whole segments
 constexpr uint32_t kKeys = 10240;
 constexpr uint32_t kWidest = 5;                  // runs are of a wave's vectors at most
 constexpr uint32_t kMaxParts = 8;
 constexpr uint32_t kSegs = 1024;
-static_assert(kSide % 64 == 0 && kSide > kHuge && kWindow <= 2 * kSide && kWindow % 64 == 0, "bins");
+static_assert(kSide % 64 == 0 && kHuge + 63 == kSide && kWindow <= 2 * kSide && kWindow % 64 == 0, "bins");
 
 struct SampleArgs {
     const uint16_t *base, *bias;
@@ -83,7 +86,7 @@ struct SampleArgs {
 };
 
 struct Shared {
-    __align__(16) uint32_t bins[2 * kSide + 64];   // then a word a lane for what is not counted
+    __align__(16) uint32_t bins[2 * kSide];
     uint16_t keys[kKeys];    // largest logit of a run, as int16 bits
     double mass[kSegs];      // mass of a segment; then: of all segments before it
     uint32_t count[kSegs];   // the same for logits
@@ -153,14 +156,12 @@ __device__ __forceinline__ bool all_alike(const u32x4& z)
     return z[0] == z[1] && z[0] == z[2] && z[0] == z[3] && z[0] >> 16 == (z[0] & 0xFFFFu);
 }
 
-// Counts one vector into the bins; logits with bits from cut on go to a word of
-// the lane's own instead.  No branch a logit, the arithmetic on pairs: the LDS
-// takes an add of a wave in 15 cycles or so, and this keeps up with it.  Returns
-// the vector's largest logit as an int16 (right where it is not negative);
-// *least: the smallest magnitude less 1 (so that zero does not count).
-__device__ __forceinline__ int32_t tally(Shared& s, const u32x4& z, uint32_t cut, u16x2* least)
+// Counts one vector into the bins.  No branch a logit, the arithmetic on pairs.
+// Returns the vector's largest logit as an int16 (right where it is not
+// negative); *least: the smallest magnitude less 1 (so that zero does not count).
+__device__ __forceinline__ int32_t tally(Shared& s, const u32x4& z, u16x2* least)
 {
-    const u16x2 dump = (u16x2)(uint16_t)((2 * kSide + (threadIdx.x & 63)) * 4);
+    const u16x2 last = (u16x2)(uint16_t)(kHuge + threadIdx.x % 63);
     u32x4 at;   // byte offsets
     i16x2 top = {INT16_MIN, INT16_MIN};
 #pragma unroll
@@ -171,12 +172,9 @@ __device__ __forceinline__ int32_t tally(Shared& s, const u32x4& z, uint32_t cut
         const i16x2 h = __builtin_bit_cast(i16x2, two);
         top = __builtin_elementwise_max(top, h);
         u16x2 r = __builtin_elementwise_sub_sat(mag, (u16x2)(uint16_t)(kLeast - 1));
-        r = __builtin_elementwise_min(r, (u16x2)(uint16_t)kHuge);
+        r = __builtin_elementwise_min(r, last);
         const u16x2 side = __builtin_bit_cast(u16x2, (i16x2)(h >> (i16x2)15)) & (u16x2)(uint16_t)kSide;
-        r = (r + side) << (u16x2)2;
-        u16x2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, two), (u16x2)(uint16_t)(cut - 1));
-        over = (u16x2)0 - __builtin_elementwise_min(over, (u16x2)1);
-        at[w] = __builtin_bit_cast(uint32_t, (u16x2)((r & ~over) | (dump & over)));
+        at[w] = __builtin_bit_cast(uint32_t, (u16x2)((r + side) << (u16x2)2));
     }
     char* bins = reinterpret_cast<char*>(s.bins);
     if (all_alike(z)) {
@@ -609,7 +607,7 @@ struct Seen {
 // keeps the runs' largest logits, of 16 << wide each.
 template <bool VEC, bool BIAS, bool KEYS>
 __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& z, uint32_t v0, uint32_t v1,
-                                            uint32_t cut, uint32_t wide)
+                                            uint32_t wide)
 {
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
     constexpr int kAhead = BIAS || !KEYS ? 4 : 8;  // vectors of a thread in flight
@@ -624,7 +622,7 @@ __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& 
     Seen seen = {INT16_MIN, 0};
     u16x2 least = {0xFFFFu, 0xFFFFu};
     auto take = [&](const u32x4& y, uint32_t v) {
-        int32_t key = tally(s, y, cut, &least);
+        int32_t key = tally(s, y, &least);
         seen.high = max(seen.high, key);
         if constexpr (KEYS) {
             if (wide <= kWidest) {
@@ -691,15 +689,6 @@ __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& 
     return seen;
 }
 
-// The cut of a temperature: bits of c = 2^12 .. 2^16, at least 1492 temperatures
-// if that is in the range.
-__device__ __forceinline__ uint32_t cut_of(double t)
-{
-    uint32_t c = kOne + 12u * 128u;
-    while (c < kOne + 16u * 128u && (double)value_of(c) < 1492.0 * t) c += 128u;
-    return c;
-}
-
 struct Drawn {
     uint32_t want, nth;   // value bits, and which of its ids
     double p;
@@ -709,17 +698,17 @@ struct Drawn {
 // Draws a value from the counts in the bins, or from the row counted again.
 template <int THREADS, bool VEC, bool BIAS>
 __device__ __forceinline__ Drawn draw(Shared& s, const SampleArgs& a, const Logits<VEC, BIAS>& z, uint32_t r,
-                                      const Seen& seen, uint32_t c, bool greedy, double t)
+                                      const Seen& seen, bool greedy, double t)
 {
     const double inv = 1.0 / t;
     Drawn d = {0, 0, 0.0, false, false};
-    d.usual = seen.tiny >= kLeast - 1 && s.bins[kHuge] == 0 && 1492.0 * t <= (double)value_of(c);
+    d.usual = seen.tiny >= kLeast - 1 && seen.high < (int32_t)kTwo16 && t <= kHottest;
     if (d.usual) {
         Row<VEC, BIAS, false, THREADS> row{s, z, 0, 0, 0.0, t, inv};
         // a positive maximum is known already
         const uint32_t top = seen.high > 0 ? kSide - 1 - ((uint32_t)seen.high - (kLeast - 1)) : row.find_top();
         const uint32_t h = row.bits_at(top);
-        d.usual = top < row.kOrder && (h < 0x8000u || (h & 0x7FFFu) < c - 128u);
+        d.usual = top < row.kOrder && (h < 0x8000u || (h & 0x7FFFu) < kTwo16 - 128u);
         if (d.usual) {
             row.top = top;
             row.zmax = (double)value_of(h);
@@ -808,9 +797,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     const Logits<VEC, BIAS> z = logits_of<VEC, BIAS>(a, r);
     int64_t* dst = a.blk + (r + r / a.bm1 + 1);
 
-    const uint32_t c = cut_of(t);
-    const Seen seen = count_range<VEC, BIAS, true>(s, z, 0, vecs, 0x8000u | c, wide);
-    const Drawn d = draw<kThreads>(s, a, z, r, seen, c, greedy, t);
+    const Seen seen = count_range<VEC, BIAS, true>(s, z, 0, vecs, wide);
+    const Drawn d = draw<kThreads>(s, a, z, r, seen, greedy, t);
     if (tid == 0 && a.prob) a.prob[r] = (float)d.p;
     if (d.none) {
         if (tid == 0) *dst = 0;
@@ -903,9 +891,7 @@ __global__ void __launch_bounds__(kThreads, 4) count_kernel(SampleArgs a)
     __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid & 63, r = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
     const uint32_t vecs = (a.V + 7) / 8, v0 = min(part * a.part_vecs, vecs), v1 = min(v0 + a.part_vecs, vecs);
-    const float temp = a.temperature[r];
-    const uint32_t c = cut_of(temp > 0.0f ? (double)temp : 1.0);
-    const Seen seen = count_range<VEC, BIAS, false>(s, logits_of<VEC, BIAS>(a, r), v0, v1, 0x8000u | c, 0);
+    const Seen seen = count_range<VEC, BIAS, false>(s, logits_of<VEC, BIAS>(a, r), v0, v1, 0);
     if (tid == 0) s.found = 0;
     __syncthreads();
     uint32_t* list = a.lists + (int64_t)blockIdx.x * a.list_room;
@@ -968,7 +954,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a)
         seen.high = max(seen.high, (int32_t)info.z);
     }
     __syncthreads();
-    const Drawn d = draw<kDrawThreads>(s, a, z, r, seen, cut_of(t), greedy, t);
+    const Drawn d = draw<kDrawThreads>(s, a, z, r, seen, greedy, t);
     if (tid == 0 && a.prob) a.prob[r] = (float)d.p;
     if (d.none) {
         if (tid == 0) *dst = 0;
