@@ -496,11 +496,11 @@ int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads,
  *   top_k          device pointer, int32 [N*(B-1)].
  *   N, B, V, strides, stream   as for xpress_add_argmax_to_blk.
  *
- * Asynchronous.  Up to 32 rows of 98304 to about 2 million logits are counted in
- * parts by several workgroups each, in two launches, whose lists meet in the
- * (device, stream) workspace (xpress_sample_reserve grows it before a capture);
- * where it cannot be had, and else, one launch and no workspace, with the same
- * results.  Errors as for xpress_add_argmax_to_blk (stride_bias_r is not looked
+ * Asynchronous.  With a bias, up to 32 rows of 98304 to about 2 million logits
+ * are counted in parts by several workgroups each, in two launches, whose lists
+ * meet in the (device, stream) workspace (xpress_sample_reserve grows it before
+ * a capture); where it cannot be had, and else, one launch and no workspace,
+ * with the same results.  Errors as for xpress_add_argmax_to_blk (stride_bias_r is not looked
  * at without bias).
  */
 int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, int64_t* blk, float* prob,

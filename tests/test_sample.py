@@ -245,11 +245,13 @@ def test_without_probabilities_and_in_a_graph():
 @pytest.mark.parametrize("filters", ["open", "greedy", "k_p_min", "hot", "cold"])
 @pytest.mark.parametrize("rows,V", [(33, 152064), (32, 98304), (31, 98303), (2, 1000003), (1, 3000001)])
 def test_either_side_of_the_split_into_parts(filters, rows, V):
-    """Up to 32 rows of 98304 to 2 million logits go in parts, others do not."""
+    """With a bias, up to 32 rows of 98304 to 2 million logits go in parts, others do not."""
     say("sample sides %s %d %d" % (filters, rows, V))
     rng = np.random.default_rng([rows, V])
-    base = normal(rng, rows, V)
-    verify(base, None, rows, 2, V, settings(rows, rng, **FILTERS[filters]))
+    base, bias = normal(rng, rows, V), normal(rng, rows, V, 0.5)
+    s = settings(rows, rng, **FILTERS[filters])
+    verify(base, bias, rows, 2, V, s)
+    verify(base, None, rows, 2, V, s)
 
 
 @pytest.mark.gpu
@@ -257,7 +259,7 @@ def test_whole_rows_and_parts_draw_the_same():
     """The same rows among more than 32, and alone; also where the workspace is not to be had."""
     rng = np.random.default_rng(22)
     rows, V = 40, 100000
-    base = normal(rng, rows, V)
+    base, bias = normal(rng, rows, V), normal(rng, rows, V, 0.5).cuda()
     base[3, ::2] = float("-inf")
     base[4, ::3] = torch.finfo(torch.bfloat16).min
     base[5] = (base[5].float() * 4).round().to(torch.bfloat16)        # ties
@@ -267,16 +269,17 @@ def test_whole_rows_and_parts_draw_the_same():
     s["top_p"] = rng.choice([0.5, 0.9, 1.0], rows).astype(np.float32)
     s["min_p"] = rng.choice([0.0, 0.01], rows).astype(np.float32)
     s["top_k"] = rng.choice([0, 5, 700], rows).astype(np.int32)
+    bias[5] = 0
     dev = base.cuda()
-    ids, p = draw(dev, None, rows, 2, V, s)
+    ids, p = draw(dev, bias, rows, 2, V, s)
     few = {k: v[:20].copy() for k, v in s.items()}
     native.xpress_release()
-    got, q = draw(dev[:20], None, 20, 2, V, few)
+    got, q = draw(dev[:20], bias[:20], 20, 2, V, few)
     assert np.array_equal(got, ids[:20]) and np.array_equal(q, p[:20])
     native.xpress_release()
     native.xpress_set_workspace_limit(1 << 10)
     try:
-        got, q = draw(dev[:20], None, 20, 2, V, few)
+        got, q = draw(dev[:20], bias[:20], 20, 2, V, few)
     finally:
         native.xpress_set_workspace_limit(0)
     assert np.array_equal(got, ids[:20]) and np.array_equal(q, p[:20])
@@ -331,19 +334,20 @@ def test_two_streams_at_once():
     """Rows in parts on two streams, each with a workspace of its own."""
     rng = np.random.default_rng(25)
     V = 120000
+    bias = normal(rng, 6, V, 0.5).cuda()
     sets = []
     for i in range(2):
         base = normal(rng, 6, V)
         s = settings(6, rng, **FILTERS["k_p_min"])
         sets.append((base.cuda(), {k: torch.from_numpy(v).cuda() for k, v in s.items()},
-                     draw(base.cuda(), None, 2, 4, V, s)[0]))
+                     draw(base.cuda(), bias, 2, 4, V, s)[0]))
     streams = [torch.cuda.Stream() for _ in sets]
     for _ in range(4):
         out = [torch.zeros(2, 4, dtype=torch.int64, device="cuda") for _ in sets]
         torch.cuda.synchronize()
         for (base, d, _), blk, stream in zip(sets, out, streams):
-            native.xpress_sample_to_blk(base, None, blk, d["temperature"], d["top_k"], d["top_p"], d["min_p"],
-                                        d["u"], 2, 4, V, V, stream=stream)
+            native.xpress_sample_to_blk(base, bias, blk, d["temperature"], d["top_k"], d["top_p"], d["min_p"],
+                                        d["u"], 2, 4, V, V, V, stream=stream)
         torch.cuda.synchronize()
         for (_, _, want), blk in zip(sets, out):
             assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)

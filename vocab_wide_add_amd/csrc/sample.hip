@@ -9,8 +9,8 @@
 // the row counts the values in LDS (exact, whatever the order of the atomics);
 // the exponentials are then taken once per distinct value, in 64 bits; and
 // the drawn token is the j-th id holding one known value.  No sort, no prefix
-// sum over the vocabulary.  A workgroup of 512 threads takes a row; few long rows
-// are counted in parts.
+// sum over the vocabulary.  A workgroup of 512 threads, or 1024 where it has a
+// compute unit for itself, takes a row; few long rows are counted in parts.
 //
 // Bins.  Magnitudes of 2^-26 to 2^16 have a 32-bit count each, for either sign:
 // 43 KB, so that two workgroups share a compute unit and one streams its row
@@ -33,8 +33,8 @@
 // all, half of the time) and by how little of a row's draw overlaps with the two
 // rows' counting, none of them alone; few rows by the chain of one workgroup.
 // Measured at V = 152064: 480 rows with bias 73 us, 4.0 TB/s; 15 rows with bias
-// 28 us and one without 26 us, 8 of them the counting, the rest the exponentials
-// and searches of one workgroup.
+// 28 us, 9 of them the counting in parts, the rest the exponentials and searches of
+// one workgroup; one row without bias 25 us.
 
 #include <hip/hip_runtime.h>
 
@@ -54,7 +54,8 @@ typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr int kDrawThreads = 1024;               // where a row comes in parts
+constexpr int kDrawThreads = 1024;               // where a row has a compute unit for itself
+constexpr uint32_t kUnits = 256;                 // compute units of the chip
 constexpr int kMostWaves = kDrawThreads / 64;
 constexpr uint32_t kInf = 0x7F80u;               // magnitude bits of infinity
 constexpr uint32_t kOne = 0x3F80u;               // of 1
@@ -95,7 +96,7 @@ struct Shared {
     uint32_t wave_count[kMostWaves];
     uint32_t wave_low[kMostWaves];
     int32_t wave_high[kMostWaves];
-    uint16_t turns[kWaves][kKeys / 64 / kWaves + 1];
+    uint16_t turns[kMostWaves][kKeys / 64 / kWaves + 1];
     double f64;
     uint32_t found, counted;
 };
@@ -605,7 +606,7 @@ struct Seen {
 
 // Counts the vectors [v0, v1) of a row into the bins, which it clears.  KEYS: also
 // keeps the runs' largest logits, of 16 << wide each.
-template <bool VEC, bool BIAS, bool KEYS>
+template <int THREADS, bool VEC, bool BIAS, bool KEYS>
 __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& z, uint32_t v0, uint32_t v1,
                                             uint32_t wide)
 {
@@ -635,9 +636,9 @@ __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& 
     const bool some = VEC && whole > v0;
     if (some) {
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) fetch(x, v0 + tid + x * kThreads);
+        for (int x = 0; x < kAhead; ++x) fetch(x, v0 + tid + x * THREADS);
     }
-    for (uint32_t i = tid * 4; i < 2 * kSide; i += kThreads * 4) {
+    for (uint32_t i = tid * 4; i < 2 * kSide; i += THREADS * 4) {
         *reinterpret_cast<u32x4*>(&s.bins[i]) = u32x4{0, 0, 0, 0};
     }
     __syncthreads();
@@ -653,12 +654,12 @@ __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& 
     auto slow = [&](uint32_t v) { return z.at(v < v1 ? v * 8 : z.V); };
     uint32_t at = v0;  // of all threads
     if (VEC) {
-        for (; at + kAhead * kThreads <= whole; at += kAhead * kThreads) {
+        for (; at + kAhead * THREADS <= whole; at += kAhead * THREADS) {
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
                 const u32x4 y = arrived(x);
-                const uint32_t v = at + x * kThreads + tid;
-                fetch(x, v + kAhead * kThreads);
+                const uint32_t v = at + x * THREADS + tid;
+                fetch(x, v + kAhead * THREADS);
                 take(y, v);
             }
         }
@@ -667,11 +668,11 @@ __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& 
             if (some && at < whole) {
                 const uint32_t v = at + tid;
                 take(v < whole ? arrived(x) : slow(v), v);
-                at += kThreads;
+                at += THREADS;
             }
         }
     }
-    for (; at < v1; at += kThreads) take(slow(at + tid), at + tid);
+    for (; at < v1; at += THREADS) take(slow(at + tid), at + tid);
     seen.tiny = min((uint32_t)least.x, (uint32_t)least.y);
     for (int m = 32; m; m >>= 1) {
         seen.tiny = min(seen.tiny, __shfl_xor(seen.tiny, m));
@@ -682,7 +683,7 @@ __device__ __forceinline__ Seen count_range(Shared& s, const Logits<VEC, BIAS>& 
         s.wave_high[wave] = seen.high;
     }
     __syncthreads();
-    for (uint32_t w = 0; w < kWaves; ++w) {
+    for (uint32_t w = 0; w < THREADS / 64; ++w) {
         seen.tiny = min(seen.tiny, s.wave_low[w]);
         seen.high = max(seen.high, s.wave_high[w]);
     }
@@ -783,8 +784,8 @@ __device__ __forceinline__ Logits<VEC, BIAS> logits_of(const SampleArgs& a, uint
 }
 
 // A workgroup a row.
-template <bool VEC, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
+template <int THREADS, bool VEC, bool BIAS>
+__global__ void __launch_bounds__(THREADS, 4) sample_kernel(SampleArgs a)
 {
     __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64, r = blockIdx.x;
@@ -797,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     const Logits<VEC, BIAS> z = logits_of<VEC, BIAS>(a, r);
     int64_t* dst = a.blk + (r + r / a.bm1 + 1);
 
-    const Seen seen = count_range<VEC, BIAS, true>(s, z, 0, vecs, wide);
-    const Drawn d = draw<kThreads>(s, a, z, r, seen, greedy, t);
+    const Seen seen = count_range<THREADS, VEC, BIAS, true>(s, z, 0, vecs, wide);
+    const Drawn d = draw<THREADS>(s, a, z, r, seen, greedy, t);
     if (tid == 0 && a.prob) a.prob[r] = (float)d.p;
     if (d.none) {
         if (tid == 0) *dst = 0;
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
     // at a time, and the one with the id looks at its 64 again.
     if (d.usual && wide <= kWidest && want > 0 && want < 0x8000u) {
         const uint32_t runs = (vecs + (2u << wide) - 1) >> (wide + 1);
-        const uint32_t share = (runs + kWaves * 64 - 1) / (kWaves * 64) * 64, first = wave * share;
+        const uint32_t share = (runs + (THREADS / 64) * 64 - 1) / ((THREADS / 64) * 64) * 64, first = wave * share;
         uint32_t* list = s.bins + first;   // the bins are not needed any more
         uint32_t n = 0;
         for (uint32_t g0 = first; g0 < min(first + share, runs); g0 += 256) {
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a)
         }
         return;
     }
-    walk<kThreads>(s, z, 0, vecs, want, nth, dst);
+    walk<THREADS>(s, z, 0, vecs, want, nth, dst);
 }
 
 // Few rows: a.parts workgroups count a row's parts, and list the bins that are
@@ -891,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 4) count_kernel(SampleArgs a)
     __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid & 63, r = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
     const uint32_t vecs = (a.V + 7) / 8, v0 = min(part * a.part_vecs, vecs), v1 = min(v0 + a.part_vecs, vecs);
-    const Seen seen = count_range<VEC, BIAS, false>(s, logits_of<VEC, BIAS>(a, r), v0, v1, 0);
+    const Seen seen = count_range<kThreads, VEC, BIAS, false>(s, logits_of<VEC, BIAS>(a, r), v0, v1, 0);
     if (tid == 0) s.found = 0;
     __syncthreads();
     uint32_t* list = a.lists + (int64_t)blockIdx.x * a.list_room;
@@ -980,13 +981,14 @@ __global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(SampleArgs a)
     walk<kDrawThreads>(s, z, v0, v1, d.want, nth, dst);
 }
 
-// Long rows go in parts while their number leaves most compute units idle: a row
-// of 152064 in 27 us where one workgroup takes 33 (32 rows: 30 and 36, 64 rows: 36
-// both; rows of 100000: 25 and 27, 64 of them 32 and 30; of 50000: 24 and 20).
-void plan_parts(SampleArgs* a)
+// Long rows with a bias go in parts while their number leaves most compute units
+// idle: a row of 152064 in 26 us where one workgroup takes 28, 16 rows 28 and 30;
+// at 64 rows one workgroup each is faster (33 and 31), at 50000 logits too (24
+// and 19), and without a bias, which is half the bytes (26 and 25).
+void plan_parts(SampleArgs* a, bool bias)
 {
     a->part_vecs = ((a->V + 7) / 8 + kMaxParts - 1) / kMaxParts;
-    a->parts = a->V >= 98304u && a->part_vecs < (1u << 15) && a->rows <= 32 ? kMaxParts : 1;  // counts in 18 bits
+    a->parts = bias && a->V >= 98304u && a->part_vecs < (1u << 15) && a->rows <= 32 ? kMaxParts : 1;  // counts in 18 bits
     a->list_room = a->part_vecs * 8 < 2 * kSide ? a->part_vecs * 8 : 2 * kSide;   // quadruples
 }
 
@@ -1004,8 +1006,13 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t stream)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((draw_kernel<VEC, BIAS>), dim3(a.rows), dim3(kDrawThreads), 0, stream, a);
+    } else if (a.rows > kUnits || a.V <= 32768u) {
+        // 512 threads: two rows to a compute unit (480 rows of 152064: 73 us, 112 with
+        // 1024), or short ones (2000 logits: 12 us and 14).  1024 else (200 rows of
+        // 152064: 41 us, 50 with 512).
+        hipLaunchKernelGGL((sample_kernel<kThreads, VEC, BIAS>), dim3(a.rows), dim3(kThreads), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((sample_kernel<VEC, BIAS>), dim3(a.rows), dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((sample_kernel<kDrawThreads, VEC, BIAS>), dim3(a.rows), dim3(kDrawThreads), 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -1066,7 +1073,7 @@ extern "C" int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, 
     a.rows = (uint32_t)rows;
     a.bm1 = (uint32_t)(B - 1);
     a.V = (uint32_t)V;
-    plan_parts(&a);
+    plan_parts(&a, bias != nullptr);
     if (a.parts > 1) {
         // Without the memory, or in a capture that would have to allocate it, the
         // rows go in one part each: the same draws, later.
@@ -1098,7 +1105,7 @@ extern "C" int xpress_sample_reserve(int64_t N, int64_t B, int64_t V, hipStream_
     a.rows = (uint32_t)(N * (B - 1));
     a.V = (uint32_t)V;
     if (a.rows == 0) return XPRESS_OK;
-    plan_parts(&a);
+    plan_parts(&a, true);
     if (a.parts == 1) return XPRESS_OK;
     uint64_t* table = nullptr;
     return xpress::workspace_table(stream, part_words(a), &table);
