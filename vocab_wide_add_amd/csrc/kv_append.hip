@@ -199,9 +199,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a)
     }
 }
 
-// A thread per piece while that leaves the chip's thread slots unfilled;
-// beyond, one workgroup a token, each thread taking items / kThreads pieces.
-constexpr uint64_t kSlots = 1u << 19;  // 256 compute units of 2048 threads
+// A thread per piece while that fills at most half of the chip's thread slots
+// (512 tokens of 384 pieces into e4m3: 5.0 us, 5.8 with a workgroup a token);
+// beyond, one workgroup a token, each thread taking items / kThreads pieces (1000
+// such tokens: 7.5 us, 8.0 with a thread per piece; 8000: 44 and 52).
+constexpr uint64_t kSlots = 1u << 18;  // of 256 compute units of 2048 threads
 
 template <bool FP16, bool E4M3, bool INTER, int W>
 hipError_t launch_pieces(const AppendArgs& a, hipStream_t stream)
