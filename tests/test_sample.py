@@ -351,3 +351,23 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for (_, _, want), blk in zip(sets, out):
             assert np.array_equal(blk[:, 1:].reshape(-1).cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+def test_every_wave_agrees_on_the_segment_of_the_draw():
+    """Rows counted again over all values (a tiny logit, a high temperature, one of 2^16) whose
+    searches end in the window that the bins hold already, so that no barrier but the searches' own
+    stands between the last one's answer and its use."""
+    rng = np.random.default_rng(26)
+    rows, V = 96, 4099
+    base = normal(rng, rows, V)
+    base[0::3, 3] = 2.0 ** -40
+    base[1::3, 5] = -2.0 ** 17
+    s = settings(rows, rng)
+    s["temperature"] = np.where(np.arange(rows) % 3 == 0, 1.0, 50.0).astype(np.float32)
+    s["top_k"] = rng.choice([0, 9, 1000], rows).astype(np.int32)
+    s["top_p"] = rng.choice([0.3, 0.95, 1.0], rows).astype(np.float32)
+    s["min_p"] = rng.choice([0.0, 0.05], rows).astype(np.float32)
+    want = verify(base, None, 32, 4, V, s)[0]
+    for _ in range(8):
+        assert np.array_equal(draw(base.cuda(), None, 32, 4, V, s)[0], want)

@@ -99,6 +99,7 @@ struct Shared {
     uint16_t turns[kMostWaves][kKeys / 64 / kWaves + 1];
     double f64;
     uint32_t found, counted;
+    uint32_t chosen;         // apart from `found`, which waves still read when it is set
 };
 
 __device__ __forceinline__ float value_of(uint32_t h) { return __uint_as_float(h << 16); }
@@ -567,13 +568,13 @@ struct Row {
             if ((int)lane == at) {
                 double j = floor((goal - before) / w);
                 j = j < 0.0 ? 0.0 : j > (double)(n - 1) ? (double)(n - 1) : j;
-                s.found = seg * 64 + lane;
+                s.chosen = seg * 64 + lane;
                 s.counted = (uint32_t)j;
                 s.f64 = w / kept;
             }
         }
         __syncthreads();
-        *want = bits_at(s.found);
+        *want = bits_at(s.chosen);
         *nth = s.counted;
         return s.f64;
     }
