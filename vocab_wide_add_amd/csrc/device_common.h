@@ -162,7 +162,9 @@ __device__ __forceinline__ void wait_vmcnt()
 // wait-count pass does not add a wait for every pending load before each LDS
 // read; the contraction loop waits for exactly the chunk it is about to read
 // (wait_vmcnt), and extra loads the compiler places after these only make
-// its own waits stricter.  ONCE: the bytes are read once and pass the caches by.
+// its own waits stricter.  A load to LDS must not follow a write of M0 at once:
+// the compiler keeps a wait state between the two, and so does the s_nop here.
+// ONCE: the bytes are read once and pass the caches by.
 template <bool ONCE = false>
 __device__ __forceinline__ void dma16(const uint16_t* gsrc, uint32_t lds_base)
 {
@@ -173,6 +175,7 @@ __device__ __forceinline__ void dma16(const uint16_t* gsrc, uint32_t lds_base)
         asm volatile(
             "s_mov_b32 %0, m0\n\t"
             "s_mov_b32 m0, %2\n\t"
+            "s_nop 0\n\t"
             "global_load_lds_dwordx4 %1, off nt\n\t"
             "s_mov_b32 m0, %0"
             : "=&s"(saved)
@@ -183,6 +186,7 @@ __device__ __forceinline__ void dma16(const uint16_t* gsrc, uint32_t lds_base)
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, off\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
