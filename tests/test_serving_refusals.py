@@ -216,3 +216,78 @@ def test_sample_reserve_checks_its_sizes():
     # nothing is needed: no HIP call either
     for none in ((0, 2, 152064), (5, 1, 152064), (100, 2, 152064), (1, 2, 20000)):
         native.xpress_sample_reserve(*none, stream=0)
+
+
+def sample_inputs(device):
+    f = dict(device=device)
+    return dict(base=torch.zeros(3, 100, dtype=torch.bfloat16, **f), bias=torch.zeros(3, 100, dtype=torch.bfloat16, **f),
+                blk=torch.zeros(1, 4, dtype=torch.int64, **f), temperature=torch.ones(3, **f),
+                top_k=torch.zeros(3, dtype=torch.int32, **f), top_p=torch.ones(3, **f), min_p=torch.zeros(3, **f),
+                u=torch.full((3,), 0.5, **f), prob=torch.zeros(3, **f))
+
+
+def sample_wrong(name, device):
+    """Tensors for this argument whose storage is long enough, but that are not what it takes."""
+    f = dict(device=device)
+    if name in ("base", "bias"):
+        yield torch.zeros(3, 100, dtype=torch.float16, **f)
+        yield torch.zeros(3, 100, **f)
+        yield torch.zeros(100, 3, dtype=torch.bfloat16, **f).t()
+        yield torch.zeros(3, 200, dtype=torch.bfloat16, **f)[:, ::2]
+    elif name == "blk":
+        yield torch.zeros(1, 8, dtype=torch.int32, **f)
+        yield torch.zeros(1, 4, dtype=torch.float64, **f)
+        yield torch.zeros(1, 8, dtype=torch.int64, **f)[:, ::2]
+        yield torch.zeros(1, 8, dtype=torch.int64, **f)[:, :3]
+    else:
+        real = torch.int32 if name == "top_k" else torch.float32
+        for other in (torch.int64, torch.float64, torch.int32, torch.float32):
+            if other is not real:
+                yield torch.zeros(6, dtype=other, **f)
+        yield torch.zeros(3, 4, dtype=real, **f)[:, 0]      # a column of a table of settings
+        yield torch.zeros(1, dtype=real, **f).expand(3)
+        yield torch.zeros(8, dtype=real, **f)[:2]           # too few, in a longer storage
+
+
+def refuses_sample(device):
+    good = sample_inputs(device)
+    for name in good:
+        for bad in sample_wrong(name, device):
+            args = dict(good, **{name: bad})
+            with pytest.raises(ValueError, match="^%s:" % name):
+                native.xpress_sample_to_blk(*[args[x] for x in ("base", "bias", "blk", "temperature", "top_k", "top_p",
+                                                                "min_p", "u")], 1, 4, 100, 100, 100, prob=args["prob"])
+
+
+def test_sample_refuses_other_types_and_strides():
+    refuses_sample("cpu")
+
+
+@pytest.mark.gpu
+def test_sample_refuses_other_types_and_strides_on_the_gpu():
+    refuses_sample("cuda")
+    good = sample_inputs("cuda")
+    for name in good:
+        if name == "base":
+            continue
+        args = dict(good, **{name: good[name].cpu()})
+        with pytest.raises(ValueError, match="^%s: expected a tensor on cuda:0" % name):
+            native.xpress_sample_to_blk(*[args[x] for x in ("base", "bias", "blk", "temperature", "top_k", "top_p",
+                                                            "min_p", "u")], 1, 4, 100, 100, 100, prob=args["prob"])
+    assert (good["blk"] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [torch.int16, torch.uint16])
+def test_sample_takes_bits_and_addresses(bits):
+    good = sample_inputs("cuda")
+    good["base"].copy_(torch.randn(3, 100))
+    names = ("base", "bias", "blk", "temperature", "top_k", "top_p", "min_p", "u")
+    native.xpress_sample_to_blk(*[good[x] for x in names], 1, 4, 100, 100, 100)
+    want = good["blk"].clone()
+    assert want[0, 1:].any()
+    for other in (dict(good, base=good["base"].view(bits), bias=good["bias"].view(bits)),
+                  {k: v.data_ptr() for k, v in good.items()}):
+        good["blk"].zero_()
+        native.xpress_sample_to_blk(*[other[x] for x in names], 1, 4, 100, 100, 100)
+        assert torch.equal(good["blk"], want)

@@ -227,11 +227,22 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     }
 }
 
-// Whether the tensor's storage holds `bytes` from its first element on.
-bool holds(const Tensor* t, int64_t bytes)
+// Logits: bf16, or their bits in 16-bit integers, with unit stride along the last
+// dimension, in a storage that holds `bytes` from the first element on.  The rows'
+// places come from the call's strides.
+bool logits(const Tensor* t, int64_t bytes, int64_t dev)
 {
-    return !t || (t->is_cuda() && t->has_storage() &&
-                  (int64_t)t->storage().nbytes() - t->storage_offset() * (int64_t)t->element_size() >= bytes);
+    if (!t) return true;
+    const at::ScalarType type = t->scalar_type();
+    return (type == at::kBFloat16 || type == at::kShort || type == at::kUInt16) && on(*t, dev) &&
+           (t->dim() == 0 || t->size(-1) <= 1 || t->stride(-1) == 1) && t->has_storage() &&
+           (int64_t)t->storage().nbytes() - t->storage_offset() * 2 >= bytes;
+}
+
+// At least n numbers of this type, one after the other.
+bool numbers(const Tensor* t, at::ScalarType type, int64_t n, int64_t dev)
+{
+    return t->scalar_type() == type && on(*t, dev) && t->is_contiguous() && t->numel() >= n;
 }
 
 // entry, stream, base, bias, blk, prob, temperature, top_k, top_p, min_p, u, N, B,
@@ -260,12 +271,15 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n)
         const unsigned __int128 base = ((unsigned __int128)(rows - (rows > 0)) * d[3] + V) * 2u,
                                 bias = ((unsigned __int128)(rows - (rows > 0)) * d[4] + V) * 2u,
                                 far = (unsigned __int128)1 << 62;
-        if (rows == 0 || base > far || bias > far || !holds(t[0], (int64_t)base) || !holds(t[1], (int64_t)bias) ||
-            !holds(t[2], N * B * 8)) {
+        if (rows == 0 || base > far || bias > far || !t[0]->is_cuda()) Py_RETURN_NONE;
+        const int64_t dev = t[0]->get_device();
+        if (!logits(t[0], (int64_t)base, dev) || !logits(t[1], (int64_t)bias, dev) ||
+            !numbers(t[2], at::kLong, N * B, dev)) {
             Py_RETURN_NONE;
         }
         for (int i = 3; i < 9; ++i) {
-            if ((i != 3 && !t[i]) || !holds(t[i], rows * 4)) Py_RETURN_NONE;
+            const at::ScalarType type = i == 5 ? at::kInt : at::kFloat;   // top_k; the others
+            if (t[i] ? !numbers(t[i], type, rows, dev) : i != 3) Py_RETURN_NONE;
         }
         void* fn = PyLong_AsVoidPtr(a[0]);
         if (!fn && PyErr_Occurred()) return nullptr;

@@ -591,13 +591,44 @@ def xpress_paged_attention_plan(N: int, Q: int, Hq: int, heads: int, dim: int, m
     return dict(zip(("chunk", "splits", "rows", "launches"), [o.value for o in out]))
 
 
+def _one_device(t, what: str, dev):
+    if dev is not None and t.device != dev:
+        raise ValueError("%s: expected a tensor on %s, as base is, got one on %s" % (what, dev, t.device))
+
+
+def _logits(t, what: str, nbytes: int, dev):
+    """Refuse a tensor that is not bf16 (or its bits in 16-bit integers) with unit
+    stride along its last dimension, or that ends before nbytes (addresses are the
+    caller's responsibility)."""
+    if t is None or not hasattr(t, "data_ptr"):
+        return
+    if t.dtype not in (_torch.bfloat16, _torch.int16, _torch.uint16) \
+            or (t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s: bf16 with unit stride along its last dimension expected, got %s of strides %s"
+                         % (what, t.dtype, t.stride()))
+    _span(t, nbytes, what)
+    _one_device(t, what, dev)
+
+
+def _numbers(t, what: str, dtype, n: int, dev):
+    """Refuse a tensor that is not n or more contiguous numbers of this type."""
+    if t is None or not hasattr(t, "data_ptr"):
+        return
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError("%s: a contiguous %s tensor of %d numbers expected, got %s of shape %s and strides %s"
+                         % (what, dtype, n, t.dtype, tuple(t.shape), t.stride()))
+    _one_device(t, what, dev)
+
+
 def xpress_sample_to_blk(base, bias, blk, temperature, top_k, top_p, min_p, u, N: int, B: int,
                          V: int, stride_base_r: int, stride_bias_r: int = 0, prob=None,
                          stream=None) -> None:
     """blk[n, 1+b] = a token drawn from softmax(bf16(base + bias) / temperature)
     of row r = n*(B-1) + b, cut by top_k, top_p and min_p, with the uniform
-    number u[r]; prob[r], its probability.  bias may be None.  temperature,
-    top_p, min_p, u, prob fp32 and top_k int32, one per row.
+    number u[r]; prob[r], its probability.  bias may be None.  base and bias
+    bf16 (or its bits as 16-bit integers) with unit stride along a row, blk
+    int64, top_k int32, temperature, top_p, min_p, u and prob fp32, one per row
+    and contiguous, all on one device.  Integer addresses are taken as they are.
     """
     lib = _lib or load()
     if _marshal is None:
@@ -608,13 +639,15 @@ def xpress_sample_to_blk(base, bias, blk, temperature, top_k, top_p, min_p, u, N
         return _check(status, "xpress_sample_to_blk")
     rows = int(N) * (int(B) - 1)
     if rows > 0:
-        _span(base, ((rows - 1) * int(stride_base_r) + int(V)) * 2, "base")
+        t, dev = _torch, base.device if hasattr(base, "data_ptr") else None
+        _logits(base, "base", ((rows - 1) * int(stride_base_r) + int(V)) * 2, dev)
         if bias is not None:
-            _span(bias, ((rows - 1) * int(stride_bias_r) + int(V)) * 2, "bias")
-        _span(blk, int(N) * int(B) * 8, "blk")
-        for t, what in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"),
-                        (min_p, "min_p"), (u, "u"), (prob, "prob")):
-            _span(t, rows * 4, what)
+            _logits(bias, "bias", ((rows - 1) * int(stride_bias_r) + int(V)) * 2, dev)
+        _numbers(blk, "blk", t.int64, int(N) * int(B), dev)
+        _numbers(top_k, "top_k", t.int32, rows, dev)
+        for x, what in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (u, "u"),
+                        (prob, "prob")):
+            _numbers(x, what, t.float32, rows, dev)
     _check(load().xpress_sample_to_blk(_ptr(base), _ptr(bias), _ptr(blk), _ptr(prob),
                                        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
                                        _ptr(u), int(N), int(B), int(V), int(stride_base_r),
