@@ -1,5 +1,8 @@
 """The host module that fills the serving operators' argument structs: the same calls as
 the binding's Python code makes, and None for whatever that code refuses."""
+import inspect
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -92,3 +95,56 @@ def test_irregular_arguments_are_left_alone():
     for f, n in ((m.kv_append, 15), (m.paged_attention, 14), (m.sample, 16)):
         with pytest.raises(TypeError):
             f(*[None] * (n - 1))
+
+
+def test_the_other_entry_points_do_without_it(monkeypatch):
+    """A stream is looked up where the module is not built; a serving operator says so."""
+    monkeypatch.setitem(sys.modules, "vocab_wide_add_amd._marshal", None)
+    monkeypatch.delattr("vocab_wide_add_amd._marshal", raising=False)
+    monkeypatch.setattr(native, "_marshal", None)
+    monkeypatch.setattr(native, "_torch", None)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1234, raising=False)
+    assert native._stream(None) == 1234
+    d = inputs("cpu")
+    q, k, v = d["rows"][:, :4], d["rows"][:, 4:6], d["rows"][:, 6:]
+    with pytest.raises(ImportError, match="_marshal.so"):
+        native.xpress_kv_append(q, k, v, q, d["kc"], d["vc"], d["table"], d["pos"], None)
+
+
+@pytest.mark.parametrize("op", ["append", "attention", "sample"])
+def test_first_calls_of_two_threads(monkeypatch, op):
+    """Whatever another thread's first call has set so far, a call finds all that it needs."""
+    native._use_torch()
+    d = inputs("cpu")
+    q, k, v = d["rows"][:, :4], d["rows"][:, 4:6], d["rows"][:, 6:]
+    n = torch.zeros(3)
+
+    def call():
+        if op == "append":
+            native.xpress_kv_append(q, k, v, q, d["kc"], d["vc"], d["table"], d["pos"], None)
+        elif op == "attention":
+            native.xpress_paged_attention(q.reshape(2, 3, 4, 64), d["kc"], d["vc"], d["table"], d["lens"],
+                                          q.reshape(2, 3, 4, 64), 40)
+        else:
+            native.xpress_sample_to_blk(torch.zeros(3, 8, dtype=torch.bfloat16), None,
+                                        torch.zeros(1, 4, dtype=torch.int64), n, n.int(), n, n, n, 1, 4, 8, 8)
+
+    # what the names hold after each assignment of a first call, in its order
+    states, names = [], ("_torch", "_marshal")
+    real = {x: getattr(native, x) for x in names}
+
+    order = [x.split(" = ")[0].strip() for x in inspect.getsource(native).splitlines()
+             if x.startswith(("        _torch = ", "        _marshal = "))]
+    assert sorted(order) == sorted(names)
+    held = dict.fromkeys(names)
+    states.append(dict(held))
+    for x in order:
+        held[x] = real[x]
+        states.append(dict(held))
+    for s in states:
+        for x, y in s.items():
+            monkeypatch.setattr(native, x, y)
+        with pytest.raises(ValueError, match="GPU"):
+            call()

@@ -161,7 +161,7 @@ def _span(t, nbytes: int, what: str):
 def _stream(stream):
     """HIP stream handle: None means torch's current stream on the current device."""
     if stream is None:
-        torch = _torch or _use_torch()
+        torch = _torch or _import_torch()
         if not torch.cuda.is_initialized():
             return torch.cuda.current_stream().cuda_stream
         # the same handle, without building the Stream object around it
@@ -406,23 +406,33 @@ _marshal = None
 _types = {}
 
 
-def _use_torch():
-    """torch, imported by the first call that takes tensors only, and the host
-    module whose functions make a call from tensors (None: the arguments are not
-    what they should be, and the Python code after it says why)."""
-    global _torch, _marshal
+def _import_torch():
+    """torch, imported by the first call that takes tensors or a stream from it.
+    (_torch is set last: another thread that sees it sees the rest.)"""
+    global _torch
     if _torch is None:
         import torch
+        _types.update({torch.bfloat16: XPRESS_BF16, torch.float16: XPRESS_FP16,
+                       torch.float8_e4m3fn: XPRESS_E4M3})
+        _torch = torch
+    return _torch
+
+
+def _use_torch():
+    """torch, and the host module whose functions make a serving operator's call from
+    tensors (None: the arguments are not what they should be, and the Python code
+    after it says why).  The other entry points do without the module.  (_marshal is
+    set after _torch, for other threads.)"""
+    global _marshal
+    torch = _import_torch()
+    if _marshal is None:
         try:
             from . import _marshal as marshal
         except ImportError as e:
             raise ImportError("_marshal.so is not built for this torch; run `python -m "
                               "vocab_wide_add_amd.build`") from e
         _marshal = marshal
-        _types.update({torch.bfloat16: XPRESS_BF16, torch.float16: XPRESS_FP16,
-                       torch.float8_e4m3fn: XPRESS_E4M3})
-        _torch = torch
-    return _torch
+    return torch
 
 
 def _dtype(t, what: str) -> int:
@@ -507,7 +517,10 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
     tokens of each sequence in order); k_scale, v_scale fp32 [heads].  See the
     header for the definition.
     """
-    torch, lib = _torch or _use_torch(), _lib or load()
+    lib = _lib or load()
+    if _marshal is None:
+        _use_torch()
+    torch = _torch
     status = _marshal.kv_append(lib.append_at, _stream_of_tensors(stream), q, k, v, q_out, k_cache, v_cache, page_table,
                                 positions, cos_sin, seq_of, k_scale, v_scale, interleaved)
     if status is not None:
@@ -551,7 +564,10 @@ def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: 
     keys a query sees back from itself (0: all).  See the header for the
     definition.
     """
-    torch, lib = _torch or _use_torch(), _lib or load()
+    lib = _lib or load()
+    if _marshal is None:
+        _use_torch()
+    torch = _torch
     status = _marshal.paged_attention(lib.attention_at, _stream_of_tensors(stream), q, k_cache, v_cache, page_table, lens,
                                       out, lse, k_scale, v_scale, max_len, window, scale)
     if status is not None:
