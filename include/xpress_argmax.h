@@ -499,9 +499,10 @@ int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads,
  * Asynchronous.  With a bias, up to 32 rows of 98304 to about 2 million logits
  * are counted in parts by several workgroups each, in two launches, whose lists
  * meet in the (device, stream) workspace (xpress_sample_reserve grows it before
- * a capture); where it cannot be had, and else, one launch and no workspace,
- * with the same results.  Errors as for xpress_add_argmax_to_blk (stride_bias_r is not looked
- * at without bias).
+ * a capture); where the memory cannot be had, and else, one launch and no
+ * workspace, with the same results.  Errors as for xpress_add_argmax_to_blk, but
+ * for XPRESS_ENOMEM and XPRESS_ECAPTURE, which are not returned (stride_bias_r is
+ * not looked at without bias).
  */
 int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, int64_t* blk, float* prob,
                          const float* temperature, const int32_t* top_k, const float* top_p,

@@ -371,3 +371,40 @@ def test_every_wave_agrees_on_the_segment_of_the_draw():
     want = verify(base, None, 32, 4, V, s)[0]
     for _ in range(8):
         assert np.array_equal(draw(base.cuda(), None, 32, 4, V, s)[0], want)
+
+
+@pytest.mark.gpu
+def test_errors_of_others_are_not_cleared():
+    """A HIP error that the caller has pending is reported by the launch, whether the rows would
+    have gone in parts or not; an allocation that failed in the library leaves none behind."""
+    import ctypes
+    rng = np.random.default_rng(27)
+    V = 100000
+    base, bias = normal(rng, 1, V).cuda(), normal(rng, 1, V, 0.5).cuda()
+    s = settings(1, rng)
+    lib = native.load()
+    lib.hipMalloc.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t]
+    none = ctypes.c_void_p()
+    native.xpress_release()
+    native.xpress_set_workspace_limit(1 << 10)
+    try:
+        want = draw(base, bias, 1, 2, V, s)
+        dev = {k: torch.from_numpy(v).cuda() for k, v in s.items()}
+        blk = torch.zeros(1, 2, dtype=torch.int64, device="cuda")
+        for b in (bias, None):
+            assert lib.hipMalloc(ctypes.byref(none), 1 << 60) != 0
+            assert lib.hipPeekAtLastError() != 0
+            with pytest.raises(native.XpressError) as e:
+                native.xpress_sample_to_blk(base, b, blk, dev["temperature"], dev["top_k"], dev["top_p"],
+                                            dev["min_p"], dev["u"], 1, 2, V, V, V)
+            assert e.value.status == native.XPRESS_EHIP
+            assert lib.hipPeekAtLastError() == 0
+        got = draw(base, bias, 1, 2, V, s)
+    finally:
+        native.xpress_set_workspace_limit(0)
+    assert np.array_equal(got[0], want[0])
+    with pytest.raises(native.XpressError) as e:
+        native.xpress_latent_reserve(1 << 22, 16, 64, 8192)      # 1 TB
+    assert e.value.status == native.XPRESS_ENOMEM
+    assert lib.hipPeekAtLastError() == 0
+    assert np.array_equal(draw(base, bias, 1, 2, V, s)[0], want[0])

@@ -1079,12 +1079,14 @@ extern "C" int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, 
         // Without the memory, or in a capture that would have to allocate it, the
         // rows go in one part each: the same draws, later.
         uint64_t* table = nullptr;
-        if (xpress::workspace_table(stream, part_words(a), &table) == XPRESS_OK) {
+        const int rc = xpress::workspace_table(stream, part_words(a), &table);
+        if (rc == XPRESS_OK) {
             a.infos = reinterpret_cast<uint4*>(table);
             a.lists = reinterpret_cast<uint32_t*>(a.infos + (int64_t)a.rows * a.parts);
-        } else {
-            (void)hipGetLastError();
+        } else if (rc == XPRESS_ENOMEM || rc == XPRESS_ECAPTURE) {
             a.parts = 1;
+        } else {
+            return rc;
         }
     }
     const bool vec = xpress::is_aligned16(base) && (rows == 1 || stride_base_r % 8 == 0) &&

@@ -604,6 +604,15 @@ int64_t grown_cap(int64_t need, int64_t old_cap, int64_t floor_cap)
     return cap;
 }
 
+// An allocation that failed is told by the status alone: it does not stay behind
+// as HIP's last error, which the next launch would report as its own.
+int no_memory(hipError_t e)
+{
+    note_hip_error(e);
+    (void)hipGetLastError();
+    return XPRESS_ENOMEM;
+}
+
 // Make sure the (device, stream) workspace holds `rows` atomic slots and a
 // `table` entry table; grows (synchronously) when needed.  Called with
 // g_ws_mu held.
@@ -625,10 +634,7 @@ int ensure_workspace_locked(int dev, hipStream_t stream, int64_t rows, int64_t t
         if (g_ws_limit > 0 && g_ws_bytes[dev] + cap * 8 > g_ws_limit) return XPRESS_ENOMEM;
         void* p = nullptr;
         e = hipMalloc(&p, (size_t)cap * 8u);
-        if (e != hipSuccess) {
-            note_hip_error(e);
-            return XPRESS_ENOMEM;
-        }
+        if (e != hipSuccess) return no_memory(e);
         // zeroed before any kernel can see it (synchronous)
         e = hipMemset(p, 0, (size_t)cap * 8u);
         if (e == hipSuccess) e = hipDeviceSynchronize();
@@ -646,10 +652,7 @@ int ensure_workspace_locked(int dev, hipStream_t stream, int64_t rows, int64_t t
         if (g_ws_limit > 0 && g_ws_bytes[dev] + cap * 8 > g_ws_limit) return XPRESS_ENOMEM;
         void* p = nullptr;
         e = hipMalloc(&p, (size_t)cap * 8u);
-        if (e != hipSuccess) {
-            note_hip_error(e);
-            return XPRESS_ENOMEM;
-        }
+        if (e != hipSuccess) return no_memory(e);
         if (w.table) g_retired[dev].push_back(w.table);
         w.table = static_cast<uint64_t*>(p);
         w.table_cap = cap;
