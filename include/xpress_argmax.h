@@ -420,8 +420,8 @@ int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t stream);
  *
  * Scores, softmax statistics and sums are fp32.  Asynchronous; one launch,
  * or two when the length is split (partial results meet in the (device,
- * stream) workspace; xpress_paged_attention_reserve grows it before a
- * capture).  The result does not depend on the order in which workgroups
+ * stream) workspace, in at most 1 GiB of it up to max_len 2^30;
+ * xpress_paged_attention_reserve grows it before a capture).  The result does not depend on the order in which workgroups
  * run.  N == 0 or Q == 0 queues nothing.  Errors: XPRESS_EINVAL (sizes,
  * types, strides, null or misaligned pointers, out or lse overlapping an
  * input or the caches; nothing queued), XPRESS_ENOMEM / XPRESS_ECAPTURE

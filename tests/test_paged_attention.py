@@ -318,3 +318,91 @@ def test_append_then_attend_gives_the_same_as_a_fresh_cache():
     e = 71 * 2.0 ** -24 * R + 46 * 2.0 ** -24 + 2.0 ** -16
     for got in (one, whole.double().cpu().numpy()):
         assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2 * e[..., None] * A * 1.01).all()
+
+
+def near64(out, lse, q, kc, vc, table, lens, max_len, at, n, window=0, k_scale=None, v_scale=None):
+    """Query `at` of sequence n of a call against 64 bits, with the tolerances above."""
+    Q, D = q.shape[1], q.shape[-1]
+    want, want_lse, A, R = ref.attention64(
+        q[n:n + 1, at:at + 1], kc, vc, table[n:n + 1], [int(lens[n]) - (Q - 1 - at)], max_len,
+        float(np.float32(1 / math.sqrt(D))), window, k_scale, v_scale)
+    u = 2.0 ** -24
+    e = (D + 4) * u * R + 4 * u + 3 * R * u + (int(lens[n]) / 32 + 40) * u
+    tol = ref.half_step(q.dtype) * np.abs(want) + 2 * (e + 2.0 ** -16)[..., None] * A
+    if q.dtype == torch.float16:
+        tol = tol + 2.0 ** -25
+    got, got_lse = out[n:n + 1, at:at + 1].double().cpu().numpy(), lse[n:n + 1, at:at + 1].double().cpu().numpy()
+    assert (np.abs(got - want) <= tol * (1 + 2.0 ** -8)).all(), np.abs(got - want).max()
+    empty = np.isinf(want_lse)
+    assert np.array_equal(np.isneginf(got_lse), empty) and (got[empty] == 0).all()
+    off = np.abs(np.where(empty, 0, got_lse) - np.where(empty, 0, want_lse))
+    assert (off <= 2 * e + 4 * u * np.abs(np.where(empty, 0, want_lse))).all(), off.max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [0, 3001])
+def test_a_prompt_in_one_part(window):
+    """Hundreds of queries over several thousand keys: one part, several tables of places."""
+    say("attention prompt %d" % window)
+    Hq, Hk, D, Q, L = 256, 8, 64, 512, 5000
+    assert native.xpress_paged_attention_plan(1, Q, Hq, Hk, D, L, window)["splits"] == 1
+    args, _ = made(90, [L], Q, Hq, Hk, D, 16)
+    q, kc, vc, table, lens = args
+    table = table.clone()
+    table[0, 100], table[0, 200] = -1, kc.shape[0]            # pages that are not there, in later tables
+    out, lse = call(up(q), up(kc), up(vc), up(table), up(lens), L, window)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all()
+    for at in (0, 1, 255, Q - 1):
+        near64(out, lse, q, kc, vc, table, lens, L, at, 0, window)
+
+
+@pytest.mark.gpu
+def test_a_prompt_with_values_that_some_do_not_see():
+    """A NaN value that only the last queries see: the others' sums are taken again, table by table."""
+    Hq, Hk, D, Q, L = 256, 8, 64, 512, 5000
+    args, _ = made(91, [L], Q, Hq, Hk, D, 16)
+    q, kc, vc, table, lens = args
+    vc = vc.clone()
+    vc[int(table[0, (L - 3) // 16]), :, (L - 3) % 16] = float("nan")
+    out, lse = call(up(q), up(kc), up(vc), up(table), up(lens), L)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0, Q - 3:]).all() and torch.isfinite(out[0, :Q - 3]).all()
+    for at in (0, 300, Q - 4):
+        near64(out, lse, q, kc, vc, table, lens, L, at, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,Q,Hq,Hk,D,dtype,cache", [
+    (4000, 1, 8, 8, 64, "bf16", "bf16"), (4000, 1, 8, 8, 128, "fp16", "fp16"), (1000, 2, 32, 2, 64, "fp16", "e4m3"),
+    (1000, 8, 8, 1, 128, "bf16", "bf16"), (4000, 1, 4, 2, 256, "bf16", "e4m3"), (1000, 3, 14, 2, 80, "bf16", "e4m3")])
+def test_many_rows_under_a_high_bound(N, Q, Hq, Hk, D, dtype, cache):
+    """Parts longer than a table of places, as the workspace's limit asks for."""
+    say("attention bound %d %d %d %d %d %s %s" % (N, Q, Hq, Hk, D, dtype, cache))
+    bound, page = 2 ** 20, 256
+    plan = native.xpress_paged_attention_plan(N, Q, Hq, Hk, D, bound)
+    assert plan["chunk"] > 2048 and plan["splits"] > 1
+    rng = np.random.default_rng([92, D])
+    lens = rng.integers(0, 60, N)
+    far = [0, N // 2, N - 1]
+    lens[far] = 20011, 4097, 9000
+    args, scales = made(92, [600], 1, Hq, Hk, D, page, dtype, cache, fill=0.0)
+    _, kc, vc, _, _ = args
+    q = torch.from_numpy((rng.standard_normal((N, Q, Hq, D)) * 1.5).astype(np.float32)).to(ref.TYPES[dtype])
+    # every sequence on pages of the one small pool, in an order of its own
+    table = torch.full((N, bound // page), -1, dtype=torch.int32)
+    for n in range(N):
+        need = -(-int(lens[n]) // page)
+        table[n, :need] = torch.from_numpy(rng.integers(0, kc.shape[0], need).astype(np.int32))
+    table[0, 30] = -1
+    lens_t = torch.from_numpy(lens.astype(np.int32))
+    try:
+        out, lse = call(up(q), up(kc), up(vc), up(table), up(lens_t), bound, **{k: up(v) for k, v in scales.items()})
+        torch.cuda.synchronize()
+        assert native.xpress_workspace_bytes() <= 3 << 30       # with what earlier calls left
+    finally:
+        native.xpress_release()
+    assert torch.isfinite(out).all()
+    for n in far + [1, 2, 3, 4]:
+        for at in {0, Q - 1}:
+            near64(out, lse, q, kc, vc, table, lens, bound, at, n, **scales)

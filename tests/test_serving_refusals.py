@@ -291,3 +291,23 @@ def test_sample_takes_bits_and_addresses(bits):
         good["blk"].zero_()
         native.xpress_sample_to_blk(*[other[x] for x in names], 1, 4, 100, 100, 100)
         assert torch.equal(good["blk"], want)
+
+
+@pytest.mark.parametrize("shape", [
+    (1, 4096, 32, 8, 128, 131072), (1, 32768, 32, 8, 128, 32768), (4, 8192, 32, 8, 128, 8192),
+    (128, 16, 32, 8, 128, 131072), (4096, 1, 32, 8, 128, 131072), (1000, 2, 32, 2, 64, 2 ** 20),
+    (1, 2 ** 20, 32, 8, 256, 2 ** 20), (2 ** 20, 1, 16, 16, 256, 2 ** 30), (64, 1, 8, 8, 64, 2 ** 31 - 1, 2 ** 31 - 1)])
+def test_parts_take_a_gib_at_most(shape):
+    """Whatever the lengths' bound and the number of queries, the parts' sums stay within 1 GiB."""
+    N, Q, Hq, heads, dim, max_len = shape[:6]
+    p = native.xpress_paged_attention_plan(*shape)
+    assert p["splits"] * p["chunk"] >= max_len and (p["splits"] - 1) * p["chunk"] < max_len
+    assert p["chunk"] % 128 == 0 and p["chunk"] <= 2 ** 30
+    if p["splits"] > 1 and max_len <= 2 ** 30:
+        assert p["splits"] * N * Q * Hq * (dim + 2) * 4 <= 1 << 30
+
+
+def test_groups_of_rows_that_fill_the_chip_are_not_split():
+    for shape in ((1, 4096, 32, 8, 128, 131072), (1, 512, 256, 8, 64, 5000), (1, 32768, 32, 8, 128, 32768, 4096)):
+        p = native.xpress_paged_attention_plan(*shape)
+        assert p["splits"] == 1 and p["launches"] == 1

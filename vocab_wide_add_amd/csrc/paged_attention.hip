@@ -80,8 +80,8 @@ constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 32;        // keys of one tile
 constexpr int kRound = kTile * kWaves;
 constexpr int kUnits = 256;       // compute units of the chip
-constexpr int kMaxChunk = 2048;  // keys of one part
-constexpr int kMaxChunkStaged = 1024;  // the same where LDS also holds the keys
+constexpr int kTable = 2048;     // keys whose places LDS holds at once
+constexpr int kTableStaged = 1024;  // the same where LDS also holds the keys
 constexpr float kNone = -INFINITY;
 
 struct AttnArgs {
@@ -116,7 +116,7 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, uint32_t n)
     const int64_t lo = (int64_t)k.len - a.Q - a.window + 1;
     k.lo = a.window > 0 && lo > 0 ? (int32_t)lo : 0;
     k.hi = k.len;
-    k.parts = (uint32_t)(k.hi - k.lo + (int32_t)a.chunk - 1) / a.chunk;
+    k.parts = ((uint32_t)(k.hi - k.lo) + a.chunk - 1) / a.chunk;
     return k;
 }
 
@@ -650,8 +650,9 @@ constexpr int tiles_ahead()
 
 // RW waves of the workgroup hold 16 rows each, KW = kWaves / RW waves share a
 // row's keys.  RW = 1: each wave loads its own tiles to registers, one tile
-// ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.
-template <bool FP16, bool E4M3, int DP, int RW, bool ONCE>
+// ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.  MANY: the
+// part may have more keys than the table of places, which is then filled again.
+template <bool FP16, bool E4M3, int DP, int RW, bool ONCE, bool MANY>
 __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a)
 {
     constexpr int kDeep = RW > 1 ? 1 : tiles_ahead<E4M3, DP>();
@@ -661,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     constexpr int KW = kWaves / RW;
     constexpr int kRow = row_stride<DP>();
     constexpr int kSums = kWaves * 16 * kRow * 4, kStages = RW > 1 ? 4 * S::kBytes : kWaves * kTile * S::kRow;
-    constexpr int kPlaces = RW > 1 ? kMaxChunkStaged : kMaxChunk + kDeep * kRound;
+    constexpr int kKeysAtOnce = RW > 1 ? kTableStaged : kTable;
+    constexpr int kPlaces = RW > 1 ? kTableStaged : kTable + kDeep * kRound;
     __shared__ __align__(16) int64_t place[kPlaces];
     __shared__ uint32_t there[kPlaces / kTile];
     // the stages, then the waves' sums
@@ -681,32 +683,47 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     const uint32_t rw = wave % RW, kw = wave / RW;
     const Keys keys = keys_of(a, n);
     if (split > 0 && split >= keys.parts) return;
-    const int32_t key0 = keys.lo + (int32_t)(split * a.chunk);
-    const uint32_t count = (uint32_t)min(keys.hi - key0, (int32_t)a.chunk);  // 0: an empty sequence
+    const int32_t part0 = keys.lo + (int32_t)(split * a.chunk);
+    const uint32_t part_count = (uint32_t)min(keys.hi - part0, (int32_t)a.chunk);  // 0: an empty sequence
     const uint32_t row0 = group * (16 * RW);
 
-    // places of the part's keys
+    // the keys of the table: the whole part, or a piece of it
+    int32_t key0 = part0;
+    uint32_t count = MANY ? min(part_count, (uint32_t)kKeysAtOnce) : part_count;
     if (tid == 0) holes = 0;
     __syncthreads();
     constexpr uint32_t kPad = RW > 1 ? S::kKeys : kTile;
-    const uint32_t padded = (count + kPad - 1) / kPad * kPad;
-    const uint32_t filled = RW > 1 ? padded : padded + kDeep * kRound;
-    for (uint32_t j0 = wave * 64; j0 < filled; j0 += kThreads) {
-        const uint32_t j = j0 + lane;
-        int64_t at = -1;
-        if (j < count) {
-            const uint32_t key = (uint32_t)key0 + j, slot = key / a.page_size;
-            const uint32_t page = (uint32_t)a.page_table[(int64_t)n * a.table + slot];
-            if (page < a.pages) {
-                at = (int64_t)page * a.page + (int64_t)(key - slot * a.page_size) * a.token;
-            } else {
-                holes = 1;
+    uint32_t padded = (count + kPad - 1) / kPad * kPad;
+    auto find_places = [&]() {
+        const uint32_t filled = RW > 1 ? padded : padded + kDeep * kRound;
+        for (uint32_t j0 = wave * 64; j0 < filled; j0 += kThreads) {
+            const uint32_t j = j0 + lane;
+            int64_t at = -1;
+            if (j < count) {
+                const uint32_t key = (uint32_t)key0 + j, slot = key / a.page_size;
+                const uint32_t page = (uint32_t)a.page_table[(int64_t)n * a.table + slot];
+                if (page < a.pages) {
+                    at = (int64_t)page * a.page + (int64_t)(key - slot * a.page_size) * a.token;
+                } else {
+                    holes = 1;
+                }
             }
+            const uint64_t on = __ballot(at >= 0);
+            if (j < filled) place[j] = at < 0 ? 0 : at;
+            if (lane < 2 && j0 + lane * kTile < filled) there[j0 / kTile + lane] = (uint32_t)(on >> (lane * kTile));
         }
-        const uint64_t on = __ballot(at >= 0);
-        if (j < filled) place[j] = at < 0 ? 0 : at;
-        if (lane < 2 && j0 + lane * kTile < filled) there[j0 / kTile + lane] = (uint32_t)(on >> (lane * kTile));
-    }
+    };
+    find_places();
+    // MANY: the table of the keys from part0 + from on, once every wave is through
+    // with the one before
+    auto turn_to = [&](uint32_t from) {
+        key0 = part0 + (int32_t)from;
+        count = min(part_count - from, (uint32_t)kKeysAtOnce);
+        padded = (count + kPad - 1) / kPad * kPad;
+        __syncthreads();
+        find_places();
+        __syncthreads();
+    };
 
     T t{a, place, there, a.kc + hk * a.head, a.vc + hk * a.head, lane & 15, lane / 16};
     t.scale = a.scale * (a.k_scale ? a.k_scale[hk] : 1.0f);
@@ -739,66 +756,82 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     const bool some = first_row < a.rows;
     const int32_t first = keys.len - (int32_t)a.Q + (int32_t)(first_row / a.G);
     const int32_t last = keys.len - (int32_t)a.Q + (int32_t)(last_row / a.G);
-    const bool whole = holes == 0;
+    bool whole = holes == 0;
     // every row sees every key of the tile at t
     auto all_seen = [&](uint32_t at) {
         const int32_t k0 = key0 + (int32_t)at;
         return whole && at + kTile <= count && k0 + kTile - 1 <= first &&
                (a.window == 0 || (int64_t)k0 > (int64_t)last - a.window);
     };
-    if constexpr (RW == 1) {
-        const uint32_t begin = kw * kTile;
-        char* own = pool + kw * (kTile * S::kRow);
-        if (begin < padded) {
-#pragma unroll
-            for (int x = 0; x < kDeep; ++x) {
-                t.fetch_keys(x, begin + x * kRound);
-                t.template load_values<ONCE>(x, begin + x * kRound);
-            }
-            for (uint32_t at = begin;;) {
+    for (uint32_t from = 0;;) {
+        if constexpr (RW == 1) {
+            const uint32_t begin = kw * kTile;
+            char* own = pool + kw * (kTile * S::kRow);
+            if (begin < padded) {
 #pragma unroll
                 for (int x = 0; x < kDeep; ++x) {
-                    const uint32_t next = at + kDeep * kRound;
-                    if (all_seen(at)) t.template tile_own<false>(x, own, at, next, key0);
-                    else t.template tile_own<true>(x, own, at, next, key0);
-                    at += kRound;
-                    if (at >= padded) goto through;
+                    t.fetch_keys(x, begin + x * kRound);
+                    t.template load_values<ONCE>(x, begin + x * kRound);
+                }
+                for (uint32_t at = begin;;) {
+#pragma unroll
+                    for (int x = 0; x < kDeep; ++x) {
+                        const uint32_t next = at + kDeep * kRound;
+                        if (all_seen(at)) t.template tile_own<false>(x, own, at, next, key0);
+                        else t.template tile_own<true>(x, own, at, next, key0);
+                        at += kRound;
+                        if (at >= padded) goto through;
+                    }
+                }
+            through:;
+            }
+        } else {
+            const uint32_t to = lds_addr(reinterpret_cast<const uint16_t*>(pool)) +
+                                (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave * 64 * 16));
+            // addresses are looked up before the wait, so that the copies follow it at once
+            typename S::From from = {};
+            if (padded > 0) {
+                S::template copy<ONCE>(S::find(a, place, 0, t.kbase, t.vbase), to);
+                if (S::kKeys < padded) from = S::find(a, place, S::kKeys, t.kbase, t.vbase);
+            }
+            for (uint32_t at = 0; at < padded; at += S::kKeys) {
+                // this stage's copies have landed, and every wave is through with
+                // the stage before, whose half the next copies fill
+                const uint32_t half = at / S::kKeys % 2;
+                wait_vmcnt<0>();
+                __syncthreads();
+                const char* here = pool + half * (2 * S::kBytes);
+                if (at + S::kKeys < padded) {
+                    S::template copy<ONCE>(from, to + (1 - half) * (2 * S::kBytes));
+                    if (at + 2 * S::kKeys < padded) from = S::find(a, place, at + 2 * S::kKeys, t.kbase, t.vbase);
+                }
+                if (!some) continue;
+#pragma unroll
+                for (uint32_t x = 0; x < S::kKeys / kTile / KW; ++x) {
+                    const uint32_t off = (x * KW + kw) * kTile;
+                    const char *ks = here + off * S::kRow, *vs = ks + S::kBytes;
+                    if (all_seen(at + off)) t.template tile<false>(ks, vs, at + off, key0);
+                    else t.template tile<true>(ks, vs, at + off, key0);
                 }
             }
-        through:;
         }
-    } else {
-        const uint32_t to = lds_addr(reinterpret_cast<const uint16_t*>(pool)) +
-                            (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave * 64 * 16));
-        // addresses are looked up before the wait, so that the copies follow it at once
-        typename S::From from = {};
-        if (padded > 0) {
-            S::template copy<ONCE>(S::find(a, place, 0, t.kbase, t.vbase), to);
-            if (S::kKeys < padded) from = S::find(a, place, S::kKeys, t.kbase, t.vbase);
-        }
-        for (uint32_t at = 0; at < padded; at += S::kKeys) {
-            // this stage's copies have landed, and every wave is through with
-            // the stage before, whose half the next copies fill
-            const uint32_t half = at / S::kKeys % 2;
-            wait_vmcnt<0>();
-            __syncthreads();
-            const char* here = pool + half * (2 * S::kBytes);
-            if (at + S::kKeys < padded) {
-                S::template copy<ONCE>(from, to + (1 - half) * (2 * S::kBytes));
-                if (at + 2 * S::kKeys < padded) from = S::find(a, place, at + 2 * S::kKeys, t.kbase, t.vbase);
-            }
-            if (!some) continue;
-#pragma unroll
-            for (uint32_t x = 0; x < S::kKeys / kTile / KW; ++x) {
-                const uint32_t off = (x * KW + kw) * kTile;
-                const char *ks = here + off * S::kRow, *vs = ks + S::kBytes;
-                if (all_seen(at + off)) t.template tile<false>(ks, vs, at + off, key0);
-                else t.template tile<true>(ks, vs, at + off, key0);
-            }
-        }
+        if constexpr (!MANY) break;
+        from += kKeysAtOnce;
+        if (from >= part_count) break;
+        turn_to(from);
+        whole = holes == 0;
     }
-    if (some && __any(!t.finite())) {
-        t.reset();
+    const bool again = some && __any(!t.finite());
+    if (again) t.reset();
+    if constexpr (MANY) {
+        if (__syncthreads_or(again)) {
+            for (uint32_t from = 0; from < part_count; from += kKeysAtOnce) {
+                turn_to(from);
+                if (!again) continue;
+                for (uint32_t at = kw * kTile; at < padded; at += KW * kTile) t.tile_careful(at, key0, first, last);
+            }
+        }
+    } else if (again) {
         for (uint32_t at = kw * kTile; at < padded; at += KW * kTile) t.tile_careful(at, key0, first, last);
     }
 
@@ -958,13 +991,22 @@ struct Plan {
 // block of queries reads the cache once; more go to further workgroups, which
 // find the keys in their XCD's L2.
 //
-// Parts: whole rounds of a workgroup's four waves, never more than kMaxChunk
-// keys.  The chip holds two workgroups a compute unit (one at 256 dims).  Where
-// all sequences have the same number of keys to read (one sequence, or a
-// window), as many parts as fit at once (24 windows of 1777, 120 owners: 26 us
-// with 4 parts, 33 with 5); where lengths may differ, a quarter more, so that
-// long ones do not run alone (32 sequences up to 4096: 61 us with 2 parts, 56
-// with 3).
+// Parts: whole rounds of a workgroup's four waves.  The chip holds two workgroups
+// a compute unit (one at 256 dims).  Where all sequences have the same number of
+// keys to read (one sequence, or a window), as many parts as fit at once (24
+// windows of 1777, 120 owners: 26 us with 4 parts, 33 with 5); where lengths may
+// differ, a quarter more, so that long ones do not run alone (32 sequences up to
+// 4096: 61 us with 2 parts, 56 with 3).  A part has no more keys than the table of
+// places, but for two cases in which its workgroup goes through several tables:
+// the parts' sums would take more than kMostWords (2048 sequences of 1009 under a
+// bound of 131072: 2.1 ms with 31 parts, 2.8 with 64), or one sequence's groups of
+// rows alone fill the chip four times over, and parts would only add their sums
+// (4096 queries over 32768 keys, 32 heads on 8: 4.3 ms, 7.1 in 32 parts; over 8192
+// keys 1.30 and 1.50 in 8).
+constexpr int64_t kMostWords = (int64_t)1 << 27;   // 1 GiB
+
+// Workspace words (8 bytes) of one part of every row: sums and (m, l).
+int64_t words_a_part(const Shape& s) { return s.N * s.Q * s.Hq * (s.dim + 2) / 2; }
 
 Plan plan_of(const Shape& s)
 {
@@ -980,11 +1022,19 @@ Plan plan_of(const Shape& s)
     const bool even = s.N == 1 || s.window > 0 || s.dim > 128;
     int64_t want = even ? slots / wide : (slots * 5 / 4 + wide - 1) / wide;
     if (want < 1) want = 1;
-    const int64_t most = p.rw > 1 ? kMaxChunkStaged : kMaxChunk;
-    int64_t chunk = (span + want - 1) / want;
-    chunk = (chunk + kRound - 1) / kRound * kRound;
-    p.chunk = chunk > most ? most : chunk;
+    const int64_t table = p.rw > 1 ? kTableStaged : kTable;
+    auto rounds = [](int64_t keys) {   // at most 2^30, so that a part's end is in 32 bits
+        const int64_t up = (keys + kRound - 1) / kRound * kRound;
+        return up < (1 << 30) ? up : (int64_t)1 << 30;
+    };
+    p.chunk = rounds((span + want - 1) / want);
+    if (p.chunk > table && !(s.N == 1 && wide >= 4 * slots)) p.chunk = table;
     p.splits = (span + p.chunk - 1) / p.chunk;
+    if (p.splits > 1 && p.splits * words_a_part(s) > kMostWords) {
+        const int64_t fit = kMostWords / words_a_part(s);
+        p.chunk = rounds(fit > 1 ? (span + fit - 1) / fit : span);
+        p.splits = (span + p.chunk - 1) / p.chunk;
+    }
     p.units = owners * p.splits;
     return p;
 }
@@ -995,22 +1045,28 @@ bool plan_ok(const Shape& s, const Plan& p)
     return p.units <= 0x7FFFFFFFll / p.groups / 8;
 }
 
-// Workspace words (8 bytes): sums and (m, l) of every part of every row.
 int64_t plan_words(const Shape& s, const Plan& p)
 {
-    return p.splits > 1 ? s.N * s.Q * s.Hq * p.splits * (s.dim + 2) / 2 : 0;
+    return p.splits > 1 ? p.splits * words_a_part(s) : 0;
+}
+
+template <bool FP16, bool E4M3, int DP, int RW, bool ONCE, bool MANY>
+void launch_one(const AttnArgs& a, hipStream_t stream)
+{
+    const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
+    hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, ONCE, MANY>), dim3(grid), dim3(kThreads), 0,
+                       stream, a);
 }
 
 template <bool FP16, bool E4M3, int DP, int RW>
 void launch_waves(const AttnArgs& a, bool once, hipStream_t stream)
 {
-    const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
-    if (once) {
-        hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, true>), dim3(grid), dim3(kThreads), 0,
-                           stream, a);
+    if (a.chunk > (uint32_t)(RW > 1 ? kTableStaged : kTable)) {
+        launch_one<FP16, E4M3, DP, RW, false, true>(a, stream);
+    } else if (once) {
+        launch_one<FP16, E4M3, DP, RW, true, false>(a, stream);
     } else {
-        hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, false>), dim3(grid), dim3(kThreads), 0,
-                           stream, a);
+        launch_one<FP16, E4M3, DP, RW, false, false>(a, stream);
     }
 }
 
