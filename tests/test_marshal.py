@@ -148,3 +148,25 @@ def test_first_calls_of_two_threads(monkeypatch, op):
             monkeypatch.setattr(native, x, y)
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_device_than_the_current_one(monkeypatch):
+    """The current device's stream and workspace do not fit them: refused.  (The Python code, told
+    of another current device; with one GPU the module cannot be.)"""
+    d = inputs("cuda")
+    q, k, v = d["rows"][:, :4], d["rows"][:, 4:6], d["rows"][:, 6:]
+    n = torch.zeros(3, device="cuda")
+    out = torch.empty(2, 3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    q_out = torch.empty(6, 4, 64, dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setattr(native, "_marshal", Never())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        native.xpress_kv_append(q, k, v, q_out, d["kc"], d["vc"], d["table"], d["pos"], None, stream=0)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        native.xpress_paged_attention(q_out.view(2, 3, 4, 64), d["kc"], d["vc"], d["table"], d["lens"], out, 40,
+                                      stream=0)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        native.xpress_sample_to_blk(torch.zeros(3, 8, dtype=torch.bfloat16, device="cuda"), None,
+                                    torch.zeros(1, 4, dtype=torch.int64, device="cuda"), n, n.int(), n, n, n, 1, 4,
+                                    8, 8, stream=0)

@@ -11,6 +11,7 @@
 
 #include <Python.h>
 
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -44,6 +45,12 @@ int64_t code_of(const Tensor& t)
 }
 
 bool on(const Tensor& t, int64_t dev) { return t.is_cuda() && t.get_device() == dev; }
+
+// The library works on the current device, whose stream the binding takes too.
+bool on_current(int64_t dev)
+{
+    return c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice().index() == dev;
+}
 
 bool has_shape(const Tensor& t, std::initializer_list<int64_t> shape)
 {
@@ -87,6 +94,7 @@ bool cache(const Tensor* k, const Tensor* v, const Tensor* table, const Tensor* 
         !plain(ks, at::kFloat, {c->heads}, dev) || !plain(vs, at::kFloat, {c->heads}, dev)) {
         return false;
     }
+    if (!on_current(dev)) return false;
     c->k = k->data_ptr();
     c->v = v->data_ptr();
     c->k_scale = address<const float>(ks);
@@ -274,7 +282,7 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (rows == 0 || base > far || bias > far || !t[0]->is_cuda()) Py_RETURN_NONE;
         const int64_t dev = t[0]->get_device();
         if (!logits(t[0], (int64_t)base, dev) || !logits(t[1], (int64_t)bias, dev) ||
-            !numbers(t[2], at::kLong, N * B, dev)) {
+            !numbers(t[2], at::kLong, N * B, dev) || !on_current(dev)) {
             Py_RETURN_NONE;
         }
         for (int i = 3; i < 9; ++i) {

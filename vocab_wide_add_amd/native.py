@@ -394,7 +394,7 @@ def xpress_read_probe(base, bias, rows: int, V: int, stride: int, mode: int, sin
 
 # ---------------------------------------------------------------------------
 # Serving operators.  The two over the paged cache take tensors only: sizes,
-# strides and types come from them.  Their C argument structs are 8-byte
+# strides and types come from them.  Tensors are on the current device.  Their C argument structs are 8-byte
 # fields throughout, packed here in declaration order.
 # ---------------------------------------------------------------------------
 
@@ -460,6 +460,14 @@ def _elsewhere(t, what: str, dev: int):
                      % (what, "a GPU" if dev < 0 else "cuda:%d" % dev, t.device))
 
 
+def _on_current(dev: int):
+    """The library works on the current device, whose stream is taken too."""
+    now = _torch._C._cuda_getDevice()
+    if dev != now:
+        raise ValueError("the tensors are on cuda:%d and the current device is cuda:%d; call this "
+                         "under torch.cuda.device(%d)" % (dev, now, dev))
+
+
 def _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev: int):
     """The fields of xpress_kv_cache from [pages, heads, page_size, dim] caches
     (any strides with unit stride along dim) on device dev and an int32
@@ -483,6 +491,7 @@ def _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev: int):
         _elsewhere(v_cache, "v_cache", dev)
     if page_table.get_device() != dev:
         _elsewhere(page_table, "page_table", dev)
+    _on_current(dev)
     f32 = _torch.float32
     return (k_cache.data_ptr(), v_cache.data_ptr(), _plain(k_scale, "k_scale", f32, (heads,), dev),
             _plain(v_scale, "v_scale", f32, (heads,), dev), page_table.data_ptr(), pages, size, heads,
@@ -664,6 +673,8 @@ def xpress_sample_to_blk(base, bias, blk, temperature, top_k, top_p, min_p, u, N
         for x, what in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (u, "u"),
                         (prob, "prob")):
             _numbers(x, what, t.float32, rows, dev)
+        if dev is not None and dev.type == "cuda":
+            _on_current(dev.index)
     _check(load().xpress_sample_to_blk(_ptr(base), _ptr(bias), _ptr(blk), _ptr(prob),
                                        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
                                        _ptr(u), int(N), int(B), int(V), int(stride_base_r),
