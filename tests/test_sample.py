@@ -408,3 +408,21 @@ def test_errors_of_others_are_not_cleared():
     assert e.value.status == native.XPRESS_ENOMEM
     assert lib.hipPeekAtLastError() == 0
     assert np.array_equal(draw(base, bias, 1, 2, V, s)[0], want[0])
+
+
+@pytest.mark.gpu
+def test_more_rows_than_a_grid_has_threads_for():
+    """2^23 rows of 512 threads are 2^32."""
+    if torch.cuda.mem_get_info()[0] < 4 << 30:
+        pytest.skip("needs 4 GiB of GPU memory")
+    say("sample rows past a grid")
+    rng = np.random.default_rng(28)
+    rows, V = 2 ** 23 + 1000, 3
+    base = normal(rng, rows, V).cuda()
+    s = settings(rows, rng)
+    s["top_k"] = rng.choice([0, 1, 2], rows).astype(np.int32)
+    ids, probs = draw(base, None, rows, 2, V, s)
+    for part in (slice(0, 5000), slice(2 ** 21 - 2000, 2 ** 21 + 2000), slice(rows - 5000, rows)):
+        few = {k: v[part].copy() for k, v in s.items()}
+        got, p = draw(base[part], None, len(few["u"]), 2, V, few)
+        assert np.array_equal(got, ids[part]) and np.array_equal(p, probs[part])

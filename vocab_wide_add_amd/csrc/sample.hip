@@ -80,6 +80,7 @@ struct SampleArgs {
     const int32_t* top_k;
     int64_t stride_base, stride_bias;
     uint32_t rows, bm1, V;
+    uint32_t first;    // of the launch's rows
     // a row in parts
     uint32_t parts, part_vecs, list_room;
     uint32_t* lists;   // [rows, parts, list_room]
@@ -789,7 +790,7 @@ template <int THREADS, bool VEC, bool BIAS>
 __global__ void __launch_bounds__(THREADS, 4) sample_kernel(SampleArgs a)
 {
     __shared__ Shared s;
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64, r = blockIdx.x;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64, r = a.first + blockIdx.x;
     const uint32_t V = a.V, vecs = (V + 7) / 8;
     uint32_t wide = 0;
     while ((vecs + (2u << wide) - 1) >> (wide + 1) > kKeys) ++wide;
@@ -999,6 +1000,21 @@ int64_t part_words(const SampleArgs& a)
     return a.parts > 1 ? (int64_t)a.rows * a.parts * (2 + (a.list_room + 1) / 2) : 0;
 }
 
+// Rows of one launch: a grid has fewer than 2^32 threads.
+constexpr uint32_t kMostRows = 1u << 21;
+
+template <int THREADS, bool VEC, bool BIAS>
+hipError_t launch_rows(SampleArgs a, hipStream_t stream)
+{
+    for (a.first = 0; a.first < a.rows; a.first += kMostRows) {
+        const uint32_t n = a.rows - a.first < kMostRows ? a.rows - a.first : kMostRows;
+        hipLaunchKernelGGL((sample_kernel<THREADS, VEC, BIAS>), dim3(n), dim3(THREADS), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <bool VEC, bool BIAS>
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream)
 {
@@ -1007,15 +1023,13 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t stream)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((draw_kernel<VEC, BIAS>), dim3(a.rows), dim3(kDrawThreads), 0, stream, a);
-    } else if (a.rows > kUnits || a.V <= 32768u) {
-        // 512 threads: two rows to a compute unit (480 rows of 152064: 73 us, 112 with
-        // 1024), or short ones (2000 logits: 12 us and 14).  1024 else (200 rows of
-        // 152064: 41 us, 50 with 512).
-        hipLaunchKernelGGL((sample_kernel<kThreads, VEC, BIAS>), dim3(a.rows), dim3(kThreads), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((sample_kernel<kDrawThreads, VEC, BIAS>), dim3(a.rows), dim3(kDrawThreads), 0, stream, a);
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    // 512 threads: two rows to a compute unit (480 rows of 152064: 73 us, 112 with
+    // 1024), or short ones (2000 logits: 12 us and 14).  1024 else (200 rows of
+    // 152064: 41 us, 50 with 512).
+    if (a.rows > kUnits || a.V <= 32768u) return launch_rows<kThreads, VEC, BIAS>(a, stream);
+    return launch_rows<kDrawThreads, VEC, BIAS>(a, stream);
 }
 
 }  // namespace
@@ -1074,6 +1088,7 @@ extern "C" int xpress_sample_to_blk(const uint16_t* base, const uint16_t* bias, 
     a.rows = (uint32_t)rows;
     a.bm1 = (uint32_t)(B - 1);
     a.V = (uint32_t)V;
+    a.first = 0;
     plan_parts(&a, bias != nullptr);
     if (a.parts > 1) {
         // Without the memory, or in a capture that would have to allocate it, the
