@@ -406,3 +406,23 @@ def test_many_rows_under_a_high_bound(N, Q, Hq, Hk, D, dtype, cache):
     for n in far + [1, 2, 3, 4]:
         for at in {0, Q - 1}:
             near64(out, lse, q, kc, vc, table, lens, bound, at, n, **scales)
+
+
+@pytest.mark.gpu
+def test_more_owners_than_a_grid_has_threads_for():
+    """2^24 workgroups of 256 threads are 2^32."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GiB of GPU memory")
+    say("attention owners past a grid")
+    N, D, page = 2 ** 24 + 1000, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(93)
+    kc, vc = (torch.randn(64, 1, page, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(N, 1, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randint(0, 64, (N, 1), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(0, page + 1, (N,), generator=g, device="cuda", dtype=torch.int32)
+    out, lse = call(q, kc, vc, table, lens, page)
+    torch.cuda.synchronize()
+    for part in (slice(0, 3000), slice(2 ** 22 - 2000, 2 ** 22 + 2000), slice(N - 3000, N)):
+        got, l_got = call(q[part], kc, vc, table[part], lens[part], page)
+        torch.cuda.synchronize()
+        assert torch.equal(got, out[part]) and torch.equal(l_got, lse[part])

@@ -100,6 +100,7 @@ struct AttnArgs {
     int32_t max_len, window;
     float scale;      // times log2(e)
     uint32_t wide;    // q and out rows are 16-byte aligned
+    uint32_t first;   // of the launch's workgroups
 };
 
 // The keys that any query of a sequence sees, [lo, hi), and its parts.
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
 
     // Workgroup i runs on XCD i % 8: the row groups that read the same keys
     // follow each other on one XCD.
-    const uint32_t id = blockIdx.x;
+    const uint32_t id = a.first + blockIdx.x;
     const uint32_t unit = id / (8 * a.groups) * 8 + id % 8, group = id / 8 % a.groups;
     if (unit >= a.units) return;
     const uint32_t owner = unit % (a.N * a.Hk), split = unit / (a.N * a.Hk);
@@ -1050,12 +1051,19 @@ int64_t plan_words(const Shape& s, const Plan& p)
     return p.splits > 1 ? p.splits * words_a_part(s) : 0;
 }
 
+// Workgroups of one launch: a grid has fewer than 2^32 threads.  (A multiple of 8,
+// for the XCDs.)
+constexpr uint32_t kMostGroups = 1u << 22;
+
 template <bool FP16, bool E4M3, int DP, int RW, bool ONCE, bool MANY>
-void launch_one(const AttnArgs& a, hipStream_t stream)
+void launch_one(AttnArgs a, hipStream_t stream)
 {
     const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
-    hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, ONCE, MANY>), dim3(grid), dim3(kThreads), 0,
-                       stream, a);
+    for (a.first = 0; a.first < grid; a.first += kMostGroups) {
+        const uint32_t n = grid - a.first < kMostGroups ? grid - a.first : kMostGroups;
+        hipLaunchKernelGGL((attention_kernel<FP16, E4M3, DP, RW, ONCE, MANY>), dim3(n), dim3(kThreads), 0,
+                           stream, a);
+    }
 }
 
 template <bool FP16, bool E4M3, int DP, int RW>
@@ -1195,6 +1203,7 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
     a.splits = (uint32_t)p.splits;
     a.max_len = (int32_t)x.max_len;
     a.window = (int32_t)x.window;
+    a.first = 0;
     a.scale = (float)(x.scale * 1.4426950408889634);
     a.wide = is_aligned16(x.q) && is_aligned16(x.out) &&
              (x.stride_q_n | x.stride_q_i | x.stride_q_h | x.stride_o_n | x.stride_o_i | x.stride_o_h) % 8 == 0;
