@@ -119,3 +119,23 @@ def test_latent_2048_blocks_sampled():
     say("  exact fraction %.5f" % exact)
     assert ok, worst
     assert exact >= 0.99, exact
+
+
+@pytest.mark.parametrize("threads", [512, 1024])
+def test_more_rows_than_a_grid_has_threads_for(threads):
+    """2^22 rows of 1024 threads are 2^32 threads."""
+    import torch
+    say("large readout rows past a grid %d" % threads)
+    rows, v = 2 ** 22 + 1000, 2
+    g = torch.Generator(device="cuda").manual_seed(5)
+    base, bias = (torch.randn(rows, v, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    blk = torch.full((rows, 2), -5, dtype=torch.int64, device="cuda")
+    native.xpress_set_plan(native.XPRESS_COMBINE_SINGLE, 0, threads)
+    try:
+        native.xpress_add_argmax_to_blk(base, bias, blk, rows, 2, v, v, v)
+        torch.cuda.synchronize()
+    finally:
+        native.xpress_set_plan()
+    z = (base.float() + bias.float()).to(torch.bfloat16)
+    assert torch.equal(blk[:, 1], (z[:, 1] > z[:, 0]).long())
+    assert (blk[:, 0] == -5).all()

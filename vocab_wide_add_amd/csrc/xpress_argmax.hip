@@ -675,7 +675,9 @@ template <int T, bool VEC, int COMBINE>
 hipError_t launch_readout(const RowArgs& a, hipStream_t stream)
 {
     const uint64_t units = (uint64_t)a.rows * a.splits;
-    const uint32_t grid = (uint32_t)(units < (1u << 22) ? units : (1u << 22));
+    // a grid has fewer than 2^32 threads; workgroups take several units beyond it
+    constexpr uint64_t kMost = T > 512 ? 1u << 21 : 1u << 22;
+    const uint32_t grid = (uint32_t)(units < kMost ? units : kMost);
     hipLaunchKernelGGL((readout_kernel<T, kUnroll, VEC, COMBINE>), dim3(grid), dim3(T), 0,
                        stream, a);
     return hipGetLastError();
