@@ -426,3 +426,36 @@ def test_more_owners_than_a_grid_has_threads_for():
         got, l_got = call(q[part], kc, vc, table[part], lens[part], page)
         torch.cuda.synchronize()
         assert torch.equal(got, out[part]) and torch.equal(l_got, lse[part])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_strides_of_single_places_do_not_matter(cache):
+    """One key-value head, one page, pages of one token: their strides address nothing (torch's
+    channels-last form gives a single head the stride 1)."""
+    for Hk, page, length in ((1, 16, 90), (2, 128, 90), (2, 1, 90)):
+        args, scales = made(94, [length], 2, 4, Hk, 64, page, "bf16", cache)
+        q, kc, vc, table, lens = args
+        if Hk == 2 and page == 128:      # the sequence's one page alone
+            at = int(table[0, 0])
+            kc, vc, table = kc[at:at + 1].clone(), vc[at:at + 1].clone(), torch.zeros_like(table[:, :1])
+        scales = {k: up(v) for k, v in scales.items()}
+        want = call(up(q), up(kc), up(vc), up(table), up(lens), length, **scales)
+        odd = [up(x) for x in (kc, vc)]
+        odd = [x.as_strided(x.shape, [s if n > 1 else 3 for n, s in zip(x.shape[:3], x.stride()[:3])] + [1])
+               for x in odd]
+        got = call(up(q), *odd, up(table), up(lens), length, **scales)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_a_single_head_in_the_channels_last_form():
+    args, _ = made(95, [90, 33], 2, 4, 1, 64, 16, fill=0.0)
+    q, kc, vc, table, lens = [up(x) for x in args]
+    want = call(q, kc, vc, table, lens, 90)
+    last = [x.to(memory_format=torch.channels_last) for x in (kc, vc)]
+    assert last[0].stride(1) == 1
+    got = call(q, *last, table, lens, 90)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -1130,9 +1130,11 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
     if (!cache_ok(c, &cache_bytes)) return XPRESS_EINVAL;
     if (c.dtype != x.dtype && c.dtype != XPRESS_E4M3) return XPRESS_EINVAL;
     const int64_t e = element_bytes(c.dtype);
-    if (c.dim * e % 16 != 0 || !is_aligned16(c.k) || !is_aligned16(c.v) ||
-        c.stride_page * e % 16 != 0 || c.stride_head * e % 16 != 0 || c.stride_token * e % 16 != 0) {
-        return XPRESS_EINVAL;
+    // every row's start; the stride of a dimension of one place moves none
+    const Dim moves[3] = {{c.pages, c.stride_page}, {c.heads, c.stride_head}, {c.page_size, c.stride_token}};
+    if (c.dim * e % 16 != 0 || !is_aligned16(c.k) || !is_aligned16(c.v)) return XPRESS_EINVAL;
+    for (const Dim& d : moves) {
+        if (d.n > 1 && d.stride * e % 16 != 0) return XPRESS_EINVAL;
     }
     if (x.max_len > c.table_width * c.page_size || !isfinite(x.scale) || !isfinite((float)x.scale)) {
         return XPRESS_EINVAL;
