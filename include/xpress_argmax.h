@@ -362,8 +362,10 @@ typedef struct xpress_kv_cache {
  * A token whose sequence or position is out of range (negative, or past
  * cache.seqs, table_width * page_size, or max_pos) is padding: nothing is
  * stored and its q_out rows are 0.  A token whose page id is outside the
- * pool is rotated but not stored.  Two tokens at one place of one sequence
- * leave one of them there.  cache.dtype is `dtype` or XPRESS_E4M3.
+ * pool is rotated but not stored.  Tokens of one call must not share a place:
+ * their heads and 16-byte pieces are stored in no order, so each element there
+ * would come from one of them, and K and V not necessarily from the same one.
+ * cache.dtype is `dtype` or XPRESS_E4M3.
  *
  * Asynchronous; one launch; no workspace.  T == 0 queues nothing.  Any
  * alignment that suits the element types is accepted; accesses are of 8

@@ -232,3 +232,21 @@ def test_places_past_32_bits():
     assert torch.equal(out, small[0])
     for b, x in zip(big, small[1:]):
         assert torch.equal(b[shift:], x) and not b[:shift].any()
+
+
+@pytest.mark.gpu
+def test_two_tokens_at_one_place():
+    """Not for use: each element comes from one of them.  Nothing else changes."""
+    rng = np.random.default_rng(10)
+    rows, kc, vc, table, pos, seq, cs, sc = build(rng, [40], [2], 4, 8, 128, 0, 16, "bf16", "bf16")
+    pos = torch.tensor([37, 37], dtype=torch.int32)
+    dev, kcd, vcd = rows.cuda(), kc.cuda(), vc.cuda()
+    native.xpress_kv_append(None, dev[:, 4:12], dev[:, 12:], None, kcd, vcd, table.cuda(), pos.cuda(), None,
+                            seq_of=seq.cuda())
+    torch.cuda.synchronize()
+    page = int(table[0, 37 // 16])
+    for got, old, new in ((kcd.cpu(), kc, rows[:, 4:12]), (vcd.cpu(), vc, rows[:, 12:])):
+        here = got[page, :, 37 % 16]
+        assert ((here == new[0]) | (here == new[1])).all()
+        got[page, :, 37 % 16] = old[page, :, 37 % 16]
+        assert torch.equal(got, old)
