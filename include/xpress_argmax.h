@@ -415,7 +415,7 @@ int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t stream);
  *                [0, max_len].
  *   max_len      1 <= max_len <= table_width * page_size: an upper bound on
  *                lens that the split over the length is planned for.
- *   scale        fp32 factor of the scores, finite.
+ *   scale        fp32 factor of the scores; log2(e) times it is finite.
  *   dim          a multiple of 8 (of 16 with an XPRESS_E4M3 cache), at most
  *                256; cache.dtype is `dtype` or XPRESS_E4M3; the cache rows
  *                must start on 16-byte boundaries.

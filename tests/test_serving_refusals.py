@@ -311,3 +311,10 @@ def test_groups_of_rows_that_fill_the_chip_are_not_split():
     for shape in ((1, 4096, 32, 8, 128, 131072), (1, 512, 256, 8, 64, 5000), (1, 32768, 32, 8, 128, 32768, 4096)):
         p = native.xpress_paged_attention_plan(*shape)
         assert p["splits"] == 1 and p["launches"] == 1
+
+
+@no_gpu_only
+@pytest.mark.parametrize("scale", [3.3e38, -3.3e38, 2.4e38, float("-inf")])
+def test_attention_refuses_scales_that_pass_fp32_in_base_2(scale):
+    """The kernel would hold infinity, and 0 times it is NaN."""
+    assert attend(scale=scale) == native.XPRESS_EINVAL

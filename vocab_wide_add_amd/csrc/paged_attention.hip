@@ -1136,9 +1136,8 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
     for (const Dim& d : moves) {
         if (d.n > 1 && d.stride * e % 16 != 0) return XPRESS_EINVAL;
     }
-    if (x.max_len > c.table_width * c.page_size || !isfinite(x.scale) || !isfinite((float)x.scale)) {
-        return XPRESS_EINVAL;
-    }
+    const double scale2 = x.scale * 1.4426950408889634;   // scores are taken in base 2
+    if (x.max_len > c.table_width * c.page_size || !isfinite((float)scale2)) return XPRESS_EINVAL;
     if (!x.q || !x.out || !x.lens || !is_aligned(x.q, 2) || !is_aligned(x.out, 2) ||
         !is_aligned(x.lens, 4) || !is_aligned(x.lse, 4)) {
         return XPRESS_EINVAL;
@@ -1206,7 +1205,7 @@ int xpress_paged_attention(const xpress_paged_attention_args* args, hipStream_t 
     a.max_len = (int32_t)x.max_len;
     a.window = (int32_t)x.window;
     a.first = 0;
-    a.scale = (float)(x.scale * 1.4426950408889634);
+    a.scale = (float)scale2;
     a.wide = is_aligned16(x.q) && is_aligned16(x.out) &&
              (x.stride_q_n | x.stride_q_i | x.stride_q_h | x.stride_o_n | x.stride_o_i | x.stride_o_h) % 8 == 0;
     if (p.splits > 1) {
