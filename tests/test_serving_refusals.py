@@ -318,3 +318,15 @@ def test_groups_of_rows_that_fill_the_chip_are_not_split():
 def test_attention_refuses_scales_that_pass_fp32_in_base_2(scale):
     """The kernel would hold infinity, and 0 times it is NaN."""
     assert attend(scale=scale) == native.XPRESS_EINVAL
+
+
+@pytest.mark.parametrize("device", ["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+def test_append_takes_q_and_q_out_together(device):
+    bf = dict(dtype=torch.bfloat16, device=device)
+    kc, vc = torch.zeros(4, 2, 16, 64, **bf), torch.zeros(4, 2, 16, 64, **bf)
+    table = torch.zeros(1, 4, dtype=torch.int32, device=device)
+    q, k = torch.zeros(3, 4, 64, **bf), torch.zeros(3, 2, 64, **bf)
+    pos = torch.zeros(3, dtype=torch.int32, device=device)
+    for a, b in ((q, None), (None, q)):
+        with pytest.raises(ValueError, match="^q, q_out:"):
+            native.xpress_kv_append(a, k, k, b, kc, vc, table, pos, None)

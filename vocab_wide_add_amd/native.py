@@ -534,6 +534,8 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
                                 positions, cos_sin, seq_of, k_scale, v_scale, interleaved)
     if status is not None:
         return _check(status, "xpress_kv_append")
+    if (q is None) != (q_out is None):
+        raise ValueError("q, q_out: both or neither expected")
     shape, dev = k.shape, k_cache.get_device()
     T, heads, dim = shape
     cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
