@@ -250,3 +250,20 @@ def test_two_tokens_at_one_place():
         assert ((here == new[0]) | (here == new[1])).all()
         got[page, :, 37 % 16] = old[page, :, 37 % 16]
         assert torch.equal(got, old)
+
+
+@pytest.mark.gpu
+def test_one_token_in_place_under_another_stride():
+    """q_out on q for one token, and for one head: the strides that address nothing may differ."""
+    rng = np.random.default_rng(11)
+    for Hq, lens, new in ((4, [40], [1]), (1, [40], [5])):
+        rows, kc, vc, table, pos, seq, cs, sc = build(rng, lens, new, Hq, 2, 64, 64, 16, "bf16", "bf16")
+        dev = rows.cuda()
+        q, k, v = dev[:, :Hq], dev[:, Hq:Hq + 2], dev[:, Hq + 2:]
+        want = torch.empty(len(pos), Hq, 64, dtype=torch.bfloat16, device="cuda")
+        native.xpress_kv_append(q, k, v, want, kc.cuda(), vc.cuda(), table.cuda(), pos.cuda(), cs.cuda())
+        st = (q.stride(0) + 8, q.stride(1)) if len(pos) == 1 else (q.stride(0), q.stride(1) + 8)
+        onto = q.as_strided(q.shape, (*st, 1))
+        native.xpress_kv_append(q, k, v, onto, kc.cuda(), vc.cuda(), table.cuda(), pos.cuda(), cs.cuda())
+        torch.cuda.synchronize()
+        assert torch.equal(q, want)

@@ -270,8 +270,10 @@ extern "C" int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t s
         }
         Dim d[2] = {{x.T, x.stride_o_t}, {x.Hq, x.stride_o_h}};
         if (!is_disjoint(d, c.dim)) return XPRESS_EINVAL;
-        // q_out on q is allowed as q itself only
-        const bool same = x.q_out == x.q && x.stride_o_t == x.stride_q_t && x.stride_o_h == x.stride_q_h;
+        // q_out on q is allowed as q itself only (one token's or one head's stride
+        // addresses nothing)
+        const bool same = x.q_out == x.q && (x.T == 1 || x.stride_o_t == x.stride_q_t) &&
+                          (x.Hq == 1 || x.stride_o_h == x.stride_q_h);
         if (!same && ranges_overlap(x.q, nq, x.q_out, no)) return XPRESS_EINVAL;
     }
     if (!apart_from_cache(c, cache_bytes, x.k, nk) || !apart_from_cache(c, cache_bytes, x.v, nv) ||
