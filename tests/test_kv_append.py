@@ -267,3 +267,14 @@ def test_one_token_in_place_under_another_stride():
         native.xpress_kv_append(q, k, v, onto, kc.cuda(), vc.cuda(), table.cuda(), pos.cuda(), cs.cuda())
         torch.cuda.synchronize()
         assert torch.equal(q, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [682, 683])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_either_side_of_a_workgroup_a_token(T, cache):
+    """A thread a piece up to 2^18 pieces, a workgroup a token beyond: 48 heads of 8 pieces each."""
+    assert (682 * 48 * 8 <= 1 << 18) and (683 * 48 * 8 > 1 << 18)
+    rng = np.random.default_rng([12, T])
+    made = build(rng, [T - 40, 40], [T - 40, 40], 32, 8, 128, 128, 16, "bf16", cache)
+    check(*made, 32, 8, 128, False)
