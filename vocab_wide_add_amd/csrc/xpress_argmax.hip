@@ -39,6 +39,7 @@
 #include <stdlib.h>
 
 #include <atomic>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -622,7 +623,15 @@ int ensure_workspace_locked(int dev, hipStream_t stream, int64_t rows, int64_t t
     Workspace& w = g_ws[std::make_pair(dev, stream)];
     const bool grow_rows = rows > w.rows_cap;
     const bool grow_table = table > w.table_cap;
-    if (grow_rows || grow_table) {
+    if (!grow_rows && !grow_table) {
+        *out = &w;
+        return XPRESS_OK;
+    }
+    // host memory for the notes first: nothing below throws
+    std::vector<void*>& retired = g_retired[dev];
+    retired.reserve(retired.size() + 2);
+    int64_t& held = g_ws_bytes[dev];
+    {
         bool capturing = false;
         int rc = stream_capturing(stream, &capturing);
         if (rc != XPRESS_OK) return rc;
@@ -631,7 +640,7 @@ int ensure_workspace_locked(int dev, hipStream_t stream, int64_t rows, int64_t t
     hipError_t e;
     if (grow_rows) {
         const int64_t cap = grown_cap(rows, w.rows_cap, 4096);
-        if (g_ws_limit > 0 && g_ws_bytes[dev] + cap * 8 > g_ws_limit) return XPRESS_ENOMEM;
+        if (g_ws_limit > 0 && held + cap * 8 > g_ws_limit) return XPRESS_ENOMEM;
         void* p = nullptr;
         e = hipMalloc(&p, (size_t)cap * 8u);
         if (e != hipSuccess) return no_memory(e);
@@ -642,21 +651,21 @@ int ensure_workspace_locked(int dev, hipStream_t stream, int64_t rows, int64_t t
             (void)hipFree(p);
             return hip_fail(e);
         }
-        if (w.keys) g_retired[dev].push_back(w.keys);
+        if (w.keys) retired.push_back(w.keys);
         w.keys = static_cast<uint64_t*>(p);
         w.rows_cap = cap;
-        g_ws_bytes[dev] += cap * 8;
+        held += cap * 8;
     }
     if (grow_table) {
         const int64_t cap = grown_cap(table, w.table_cap, 65536);
-        if (g_ws_limit > 0 && g_ws_bytes[dev] + cap * 8 > g_ws_limit) return XPRESS_ENOMEM;
+        if (g_ws_limit > 0 && held + cap * 8 > g_ws_limit) return XPRESS_ENOMEM;
         void* p = nullptr;
         e = hipMalloc(&p, (size_t)cap * 8u);
         if (e != hipSuccess) return no_memory(e);
-        if (w.table) g_retired[dev].push_back(w.table);
+        if (w.table) retired.push_back(w.table);
         w.table = static_cast<uint64_t*>(p);
         w.table_cap = cap;
-        g_ws_bytes[dev] += cap * 8;
+        held += cap * 8;
     }
     *out = &w;
     return XPRESS_OK;
@@ -667,8 +676,13 @@ int ensure_workspace(hipStream_t stream, int64_t rows, int64_t table, Workspace*
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e);
-    std::lock_guard<std::mutex> lk(g_ws_mu);
-    return ensure_workspace_locked(dev, stream, rows, table, out);
+    // no exception leaves a C entry point: host memory that cannot be had is ENOMEM
+    try {
+        std::lock_guard<std::mutex> lk(g_ws_mu);
+        return ensure_workspace_locked(dev, stream, rows, table, out);
+    } catch (const std::exception&) {
+        return XPRESS_ENOMEM;
+    }
 }
 
 template <int T, bool VEC, int COMBINE>
