@@ -83,7 +83,9 @@ extern "C" {
  * When a later call needs more, the workspace grows (synchronously, outside
  * capture only) into a new allocation and the old one is retired, not freed:
  * queued work and HIP graphs captured before keep valid memory until
- * xpress_release.  The same rules hold for every entry point below that
+ * xpress_release.  A graph holds the workspace of the stream it was captured
+ * on: its replays must not run at the same time as other graphs captured there
+ * or calls queued there.  The same rules hold for every entry point below that
  * uses the workspace.
  * The caller keeps every buffer alive until the queued work has finished.
  * Host threads: the library's own tables are locked, but a call holds its
@@ -370,10 +372,10 @@ typedef struct xpress_kv_cache {
  * Asynchronous; one launch; no workspace.  T == 0 queues nothing.  Any
  * alignment that suits the element types is accepted; accesses are of 8
  * elements where dim, the strides and the pointers allow it and rot_dim is a
- * multiple of 16, of 4 at half of that, else single, with identical results.  XPRESS_EINVAL: a size or type outside the above, a
- * null pointer, a pointer not aligned to its element, a cache or q_out whose
- * elements share addresses, or a cache whose span overlaps q, k, v, q_out or
- * an index array.
+ * multiple of 16, of 4 at half of that, else single, with identical results.
+ * XPRESS_EINVAL: a size or type outside the above, a null pointer, a pointer not
+ * aligned to its element, a cache or q_out whose elements share addresses, or a
+ * cache whose span overlaps q, k, v, q_out or an index array.
  */
 typedef struct xpress_kv_append_args {
     xpress_kv_cache cache;

@@ -27,14 +27,14 @@
 //
 // Weights enter the product as two 16-bit parts (rounded weight, rounded
 // rest), 16 bits or more in all: with one part their rounding adds as much
-// error as the output's own, and the second product costs nothing that the
-// cache's bytes do not hide.  Scores, m, the sum l and O are fp32.  An fp16
-// weight is scaled by 2^kLift so that weights down to 2^-25 of the largest
-// stay normal numbers.
+// error as the output's own.  Up to 16 rows the cache's bytes hide the second
+// product; a block of queries, whose products come on top of its copies in part,
+// pays for it.  Scores, m, the sum l and O are fp32.  An fp16 weight is scaled by
+// 2^kLift so that weights down to 2^-25 of the largest stay normal numbers.
 //
-// Each key's place in the pool is worked out once per workgroup, into LDS
-// (one division by the page size per key, any page size), and a bit says
-// whether it exists.  A key on a missing page, or past the part's end, does
+// Each key's place in the pool is worked out once per workgroup, into a table in
+// LDS (one division by the page size per key, any page size), which a part of more
+// keys fills several times; a bit says whether the key exists.  A key on a missing page, or past the part's end, does
 // not: its place is the pool's first row, its score is masked and its value row
 // taken as zeros.
 //
@@ -53,7 +53,11 @@
 // of 131072 tokens with 4 heads 44 + 5, 6.2 TB/s; a block of 16 queries of the 32
 // sequences 78 + 11, where the copies to LDS set the pace; 128 sequences up to
 // 6000 on an e4m3 cache, heads of 64, 93 + 5, 4.9 TB/s, by instructions a byte;
-// one of 1009 tokens 7 + 4, latency.
+// one of 1009 tokens 7 + 4, latency.  Whole calls: heads of 256, one workgroup a
+// compute unit, 140 us for the 32 sequences (4.1 TB/s); their blocks of 128 and 256
+// rows a head 126 and 210, by what every wave does again for its 16 rows (operands
+// from LDS, the 8 x 8 blocks); one of 1009 under a bound of 131072, 8 parts of
+// 2048 for its 8 of 128, 16.
 
 #include <hip/hip_runtime.h>
 
@@ -650,8 +654,8 @@ constexpr int tiles_ahead()
 }
 
 // RW waves of the workgroup hold 16 rows each, KW = kWaves / RW waves share a
-// row's keys.  RW = 1: each wave loads its own tiles to registers, one tile
-// ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.  MANY: the
+// row's keys.  RW = 1: each wave loads its own tiles to registers, tiles_ahead()
+// of them ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.  MANY: the
 // part may have more keys than the table of places, which is then filled again.
 template <bool FP16, bool E4M3, int DP, int RW, bool ONCE, bool MANY>
 __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a)
@@ -992,8 +996,9 @@ struct Plan {
 // block of queries reads the cache once; more go to further workgroups, which
 // find the keys in their XCD's L2.
 //
-// Parts: whole rounds of a workgroup's four waves.  The chip holds two workgroups
-// a compute unit (one at 256 dims).  Where all sequences have the same number of
+// Parts: whole rounds of a workgroup's four waves.  A compute unit holds two
+// workgroups (one at 256 dims; three of the e4m3 form and of the staged forms at 64,
+// which the rule does not count on).  Where all sequences have the same number of
 // keys to read (one sequence, or a window), as many parts as fit at once (24
 // windows of 1777, 120 owners: 26 us with 4 parts, 33 with 5); where lengths may
 // differ, a quarter more, so that long ones do not run alone (32 sequences up to

@@ -19,7 +19,9 @@
 // temperature of 2^15 / 746 or less, their weight is at most exp(-746), 0 in 64
 // bits.  A row with anything else (a tinier value that is not 0, 2^16 or more, a
 // lower maximum, a higher temperature) is counted again over all 65536 values,
-// in seven windows of the order, a pass for each.
+// in seven windows of the order, a pass over the row for each, and another for a
+// search whose window has gone: 480 rows with bias 629 us at a temperature of 44
+// where 43 takes 146, one row 181 and 37; a +NaN in a row is as dear (596 and 180).
 //
 // The j-th id.  While the row goes by, the largest of each 16 logits is kept
 // (in 16 bits; a run doubles with every doubling of the row past 163840): only
@@ -32,9 +34,10 @@
 // Bound: many rows by their bytes, by the vector instructions (some 12 a logit in
 // all, half of the time) and by how little of a row's draw overlaps with the two
 // rows' counting, none of them alone; few rows by the chain of one workgroup.
-// Measured at V = 152064: 480 rows with bias 73 us, 4.0 TB/s; 15 rows with bias
-// 28 us, 9 of them the counting in parts, the rest the exponentials and searches of
-// one workgroup; one row without bias 25 us.
+// Measured at V = 152064: 480 rows with bias 67 (top-p alone) to 79 us, 3.7 to
+// 4.4 TB/s, without bias 48 us, 3.1 TB/s (half the bytes, the same instructions); 15
+// rows with bias 28 us, 9 of them the counting in parts, the rest the exponentials
+// and searches of one workgroup; one row without bias 23 to 27 us.
 
 #include <hip/hip_runtime.h>
 
