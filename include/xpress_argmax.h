@@ -422,8 +422,8 @@ int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t stream);
  *                256; cache.dtype is `dtype` or XPRESS_E4M3; the cache rows
  *                must start on 16-byte boundaries.
  *
- * Scores, softmax statistics and sums are fp32.  Asynchronous; one launch,
- * or two when the length is split (partial results meet in the (device,
+ * Scores, softmax statistics and sums are fp32.  Asynchronous; one launch (one
+ * for each 2^22 workgroups), or two when the length is split (partial results meet in the (device,
  * stream) workspace, in at most 1 GiB of it up to max_len 2^30;
  * xpress_paged_attention_reserve grows it before a capture).  The result does not depend on the order in which workgroups
  * run.  N == 0 or Q == 0 queues nothing.  Errors: XPRESS_EINVAL (sizes,
@@ -503,8 +503,8 @@ int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads,
  * Asynchronous.  With a bias, up to 32 rows of 98304 to about 2 million logits
  * are counted in parts by several workgroups each, in two launches, whose lists
  * meet in the (device, stream) workspace (xpress_sample_reserve grows it before
- * a capture); where the memory cannot be had, and else, one launch and no
- * workspace, with the same results.  Errors as for xpress_add_argmax_to_blk, but
+ * a capture); where the memory cannot be had, and else, one launch (one for each
+ * 2^21 rows) and no workspace, with the same results.  Errors as for xpress_add_argmax_to_blk, but
  * for XPRESS_ENOMEM and XPRESS_ECAPTURE, which are not returned (stride_bias_r is
  * not looked at without bias).
  */
