@@ -395,6 +395,18 @@ typedef struct xpress_kv_append_args {
 int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t stream);
 
 /*
+ * xpress_kv_append_at -- the same for tokens whose place in the sequence is not
+ * their position: the nodes of a tree of drafts, which stand one after the other
+ * in the cache while siblings share a position.  places, a device pointer to
+ * int32 [T], says where keys and values go: K(page_table, n, places[t]); the
+ * rotation takes args->positions, which only max_pos bounds.  A token is padding if
+ * its sequence or position is out of range; one whose place is out of range
+ * (negative, or past table_width * page_size), or on a page outside the pool, is
+ * rotated but not stored.  places null: xpress_kv_append.
+ */
+int xpress_kv_append_at(const xpress_kv_append_args* args, const int32_t* places, hipStream_t stream);
+
+/*
  * xpress_paged_attention -- attention of the Q newest tokens of every
  * sequence over its paged cache (Q = 1: decoding; Q = B: verifying a drafted
  * block).  With len = lens[n] (the new tokens included, already appended),
@@ -464,6 +476,191 @@ int xpress_paged_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t hea
 int xpress_paged_attention_plan(int64_t N, int64_t Q, int64_t Hq, int64_t heads, int64_t dim,
                                 int64_t max_len, int64_t window, int* chunk, int* splits,
                                 int* rows, int* launches);
+
+/*
+ * xpress_sink_attention -- the same, where a window leaves the first tokens
+ * visible: a query at position pos sees the keys 0 <= j <= pos with
+ *
+ *     j > pos - window   or   j < sinks              (all of them if window is 0)
+ *
+ * 0 <= sinks < 2^31.  What lies between is not read: pages there may have been
+ * given back.  All else as for xpress_paged_attention; the workspace is what
+ * xpress_sparse_attention_reserve with tree 0 grows it to.
+ */
+int xpress_sink_attention(const xpress_paged_attention_args* args, int64_t sinks, hipStream_t stream);
+
+/*
+ * xpress_tree_attention -- the same for a tree of drafted tokens: the Q newest
+ * tokens of a sequence are nodes, node i at place past + i, past = len - Q.
+ * Node i sees
+ *
+ *     the places j < past with j > pos - window or j < sinks (all if window is 0),
+ *         where pos = past + (the number of nodes it sees) - 1, its position;
+ *     node j, at place past + j, where bit j % 32 of tree[n, i, j / 32] is set
+ *         (itself only if its own bit is; the window does not apply).
+ *
+ * Any mask is accepted, not ancestors alone: a node that sees no key gives out = 0,
+ * lse = -inf.  Nodes at negative places (len < Q) do not exist.
+ *
+ *   tree     device pointer, int32 words [N, Q, ceil(Q / 32)], strides in words
+ *            (not negative, 0 for one tree of all sequences), unit stride along the
+ *            words; bits past Q are not looked at.
+ *
+ * A key that its window's and its tree's rule leave to no node takes no part,
+ * whatever it holds.  All else as for xpress_paged_attention; the workspace is what
+ * xpress_sparse_attention_reserve with tree 1 grows it to.
+ */
+int xpress_tree_attention(const xpress_paged_attention_args* args, const int32_t* tree,
+                          int64_t stride_tree_n, int64_t stride_tree_i, int64_t sinks,
+                          hipStream_t stream);
+
+/*
+ * xpress_sparse_attention_reserve -- grow the (device, stream) workspace to what
+ * xpress_sink_attention (tree 0) or xpress_tree_attention (tree not 0) needs.
+ * Synchronous.  Returns XPRESS_OK, XPRESS_EINVAL, XPRESS_ENOMEM or XPRESS_EHIP.
+ */
+int xpress_sparse_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t heads, int64_t dim,
+                                    int64_t max_len, int64_t window, int64_t sinks, int tree,
+                                    hipStream_t stream);
+
+/*
+ * The pages of a cache.  refs, int32 [pages] on the device, holds for each page how
+ * many entries of all tables name it; a page with refs 0 is free.  Free pages are
+ * taken lowest id first, in the order of the tables' rows (and of slots within a
+ * row), so that results do not depend on the order of the work.  Entries outside
+ * [0, pages) name no page.  Tables are int32 [rows, width] with a row stride of at
+ * least width (any with one row) and unit stride along width; width * page_size < 2^31.
+ * Where pages run out, the entries that lack one are -1 and *missing (int32 on the
+ * device, or null) receives their number; it is written by every call.  All
+ * functions are asynchronous and use no workspace.  XPRESS_EINVAL: a size or
+ * stride outside what is said here, a null or misaligned pointer, or an array that is
+ * written sharing bytes with another; nothing is queued.
+ *
+ * xpress_kv_fork -- M new rows of a table from N old ones.  Row m continues source
+ * n = src[m] (outside [0, N): an empty row, all -1) with its lens[n] tokens, clamped to
+ * [0, width * page_size]:
+ *
+ *     new_table[m, s] = table[n, s]    for whole pages, s < lens[n] / page_size;
+ *     a part-filled last page stays with the lowest m of its source if no other
+ *         entry names it (refs 1); the others, which will write to it, get a free page
+ *         each, and copies[m] = (old page, new page, tokens) says what to copy there;
+ *     -1 after that.
+ *
+ * copies [M, 3] is (-1, -1, 0) where nothing is to be copied.  new_refs [pages] are
+ * the counts with the new table in place of the old one: refs - (entries of table that
+ * name the page) + (entries of new_table).  refs, table and the pages themselves are
+ * left as they are, and pages are taken from those free in refs: a fork may be made
+ * again, as by a graph that is replayed.  Sources that no row continues give
+ * their pages back.  Two launches.  N, M < 2^24.
+ */
+int xpress_kv_fork(const int32_t* refs, int64_t pages, const int32_t* table, int64_t stride_table,
+                   const int32_t* lens, int64_t N, const int32_t* src, int64_t M, int64_t width,
+                   int64_t page_size, int32_t* new_refs, int32_t* new_table, int64_t stride_new,
+                   int32_t* copies, int32_t* missing, hipStream_t stream);
+
+/*
+ * xpress_kv_copy -- for each of copies [count, 3] = (from, to, tokens): the first
+ * `tokens` places (clamped to [0, page_size]) of page `from` are copied to page `to`,
+ * keys and values of all heads.  Entries with a page outside the pool do nothing.  A
+ * page that is written must be in one entry of a call only.  cache->page_table, seqs
+ * and the table's sizes are not looked at.  A page has fewer than 2^31 pieces (16
+ * bytes, or what alignment leaves).
+ */
+int xpress_kv_copy(const xpress_kv_cache* cache, const int32_t* copies, int64_t count, hipStream_t stream);
+
+/*
+ * xpress_kv_grow -- free pages for the tokens have[n] <= p < want[n] of each sequence:
+ * every slot s with ceil(have / page_size) <= s < ceil(want / page_size), s < width,
+ * whose entry names no page gets one, with refs 1.  One launch of one workgroup; for
+ * N > 0 width < 2^21.
+ */
+int xpress_kv_grow(int32_t* refs, int64_t pages, int32_t* table, int64_t stride_table, int64_t N,
+                   int64_t width, int64_t page_size, const int32_t* have, const int32_t* want,
+                   int32_t* missing, hipStream_t stream);
+
+/*
+ * xpress_kv_free -- gives back the pages of which no coming query sees a token: of
+ * sequence n's entries those stay whose slot s has s * page_size < lens[n] and, with
+ * window > 0, s * page_size < sinks or (s + 1) * page_size > lens[n] - window + 1
+ * (what the token at position lens[n] will see).  Every other entry becomes -1, and
+ * the count of the page it named goes down by one.  A finished sequence has lens 0;
+ * rejected drafts are behind lens.
+ */
+int xpress_kv_free(int32_t* refs, int64_t pages, int32_t* table, int64_t stride_table, int64_t N,
+                   int64_t width, int64_t page_size, const int32_t* lens, int64_t window, int64_t sinks,
+                   hipStream_t stream);
+
+/*
+ * xpress_kv_compact -- the tokens of a path through a tree of drafts move together:
+ * for j = 0, 1, .. below count[n] (clamped to [0, longest]) the key and value at place
+ * start[n] + path[n, j] go to place start[n] + j of sequence n.  A path ascends from
+ * 0 or more; it ends at the first entry that does not pass the one before.  A move
+ * from or to a place past the table, or on a page outside the pool, is left out; a
+ * negative start moves nothing.  Pages that other rows name too are written all the
+ * same.  path int32 [seqs, longest], row stride stride_path (0: one path for
+ * all), start and count int32 [seqs].
+ */
+int xpress_kv_compact(const xpress_kv_cache* cache, const int32_t* start, const int32_t* path,
+                      int64_t stride_path, const int32_t* count, int64_t longest, hipStream_t stream);
+
+/*
+ * xpress_beam_select -- beam search's selection.  Row r = n * beams + i holds the
+ * logits of beam i of sequence n, and
+ *
+ *     z_v = bf16(base[r, v] + bias[r, v])         (base[r, v] when bias is null)
+ *     score(r, v) = scores[r] + z_v - log sum_w exp(z_w)
+ *
+ * best, rows and ids [N, K] receive the K candidates of each sequence with the
+ * largest score, in descending order: the score, the row r and the id v.  Among equal
+ * scores the lower row comes first, in a row the larger logit, then the lower id.
+ * Scores are formed in 64 bits from sums of 32-bit terms (relative error of the sum
+ * about 1e-7 at most) and rounded once.
+ *
+ * NaN logits and -inf are no candidates and add nothing to the sum; a +inf logit
+ * leaves only the +inf ones, with equal shares.  A beam whose score is not finite
+ * takes no part (-inf: a beam that is not in use).  Where candidates run out: best
+ * -inf, rows -1, ids -1, which xpress_kv_fork and xpress_beam_reorder take as empty.
+ *
+ *   base, bias     as for xpress_add_argmax_to_blk; bias may be null.
+ *   scores         device pointer, fp32 [N * beams].
+ *   best           device pointer, fp32 [N, K] contiguous.
+ *   rows           device pointer, int32 [N, K] contiguous.
+ *   ids            device pointer, int64 [N, K] contiguous.
+ *   beams          1 .. 4096, and as many as LDS holds the lists of; K 1 .. 128.
+ *
+ * Asynchronous; two launches (one more of each for every 2^22 workgroups), whose lists
+ * meet in the (device, stream) workspace; xpress_beam_select_reserve grows it before
+ * a capture.  N == 0 queues nothing.  Errors as for xpress_add_argmax_to_blk
+ * (stride_bias_r is not looked at without bias).
+ */
+int xpress_beam_select(const uint16_t* base, const uint16_t* bias, const float* scores, float* best,
+                       int32_t* rows, int64_t* ids, int64_t N, int64_t beams, int64_t V, int64_t K,
+                       int64_t stride_base_r, int64_t stride_bias_r, hipStream_t stream);
+
+/*
+ * xpress_beam_select_reserve -- grow the (device, stream) workspace to what
+ * xpress_beam_select needs.  Synchronous.  Returns XPRESS_OK, XPRESS_EINVAL,
+ * XPRESS_ENOMEM or XPRESS_EHIP.
+ */
+int xpress_beam_select_reserve(int64_t N, int64_t beams, int64_t V, int64_t K, hipStream_t stream);
+
+/* One state of all beams: rows of `bytes` bytes, step_from and step_to bytes apart. */
+typedef struct xpress_beam_state {
+    const void* from;
+    void* to;
+    int64_t step_from, step_to, bytes;
+} xpress_beam_state;
+
+/*
+ * xpress_beam_reorder -- every state's row src[m] of N goes to its row m of M; where
+ * src[m] is outside [0, N), row m becomes zeros.  states is host memory, read during
+ * the call; up to 4096 of them.  src is int32 [M] on the device.  What is written
+ * must not share bytes with anything that the call reads or writes besides.
+ * Asynchronous; one launch for every 8 states; accesses are of 16 bytes where rows and
+ * steps allow it, else of 4 or 1.
+ */
+int xpress_beam_reorder(const xpress_beam_state* states, int64_t count, const int32_t* src, int64_t N,
+                        int64_t M, hipStream_t stream);
 
 /*
  * xpress_sample_to_blk -- the sampled readout: one token per draft row, drawn

@@ -6,9 +6,11 @@ Usage: ``python -m vocab_wide_add_amd.build`` (or ``__graft_entry__.build()``).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,12 +19,16 @@ SRCS = [os.path.join(PKG, "csrc", "xpress_argmax.hip"),
         os.path.join(PKG, "csrc", "latent.hip"),
         os.path.join(PKG, "csrc", "kv_append.hip"),
         os.path.join(PKG, "csrc", "paged_attention.hip"),
+        os.path.join(PKG, "csrc", "sparse_attention.hip"),
+        os.path.join(PKG, "csrc", "kv_pages.hip"),
+        os.path.join(PKG, "csrc", "beams.hip"),
         os.path.join(PKG, "csrc", "sample.hip"),
         os.path.join(PKG, "csrc", "read_probe.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libxpress_argmax.so")
 MARSHAL_SRC = os.path.join(PKG, "csrc", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+JOBS = max(1, min(8, os.cpu_count() or 1))
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -30,7 +36,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # IEEE behaviour the readout depends on: no flush of fp32 denormals, no
     # fast-math reassociation.
     "-fno-gpu-flush-denormals-to-zero",
@@ -69,9 +74,17 @@ def build_marshal(verbose: bool = False) -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile the library and the host module; returns the library's path
-    (always recompiles)."""
-    _run([HIPCC] + FLAGS + ["-I", INCLUDE, "-o", LIB] + SRCS, LIB, verbose)
-    build_marshal(verbose)
+    (always recompiles).  The sources are compiled side by side: the two forms of
+    the attention take a minute and a half each."""
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="build_") as tmp, \
+            concurrent.futures.ThreadPoolExecutor(JOBS) as pool:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SRCS]
+        jobs = [pool.submit(build_marshal, verbose)]
+        jobs += [pool.submit(_run, [HIPCC] + FLAGS + ["-I", INCLUDE, "-c", "-o", obj, src], obj, verbose)
+                 for src, obj in zip(SRCS, objects)]
+        for job in jobs:
+            job.result()
+        _run([HIPCC] + FLAGS + ["-shared", "-o", LIB] + objects, LIB, verbose)
     return LIB
 
 

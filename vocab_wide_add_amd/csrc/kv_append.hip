@@ -39,7 +39,7 @@ struct AppendArgs {
     uint16_t* q_out;
     void *kc, *vc;
     const float *k_scale, *v_scale;
-    const int32_t *positions, *seq_of, *page_table;
+    const int32_t *positions, *places, *seq_of, *page_table;
     const float* cos_sin;
     int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
     int64_t page, head, token, table;  // cache strides, page table row stride
@@ -54,12 +54,27 @@ struct Place {
     int64_t at;       // offset of its place in head 0 of the caches; < 0: not stored
 };
 
+template <bool PLACES>
 __device__ __forceinline__ Place place_of(const AppendArgs& a, uint32_t t)
 {
     Place p;
     p.pos = a.positions[t];
     p.at = -1;
     const uint32_t n = a.seq_of ? (uint32_t)a.seq_of[t] : t / a.per_seq;
+    if constexpr (PLACES) {
+        const int32_t place = a.places[t];
+        const uint32_t slot = (uint32_t)place / a.page_size;   // a negative place is past any table
+        if (p.pos < 0 || p.pos >= a.max_pos || n >= a.seqs) {
+            p.pos = -1;
+            return p;
+        }
+        if (place < 0 || slot >= a.width) return p;
+        const uint32_t page = (uint32_t)a.page_table[(int64_t)n * a.table + slot];
+        if (page < a.pages) {
+            p.at = (int64_t)page * a.page + (int64_t)((uint32_t)place - slot * a.page_size) * a.token;
+        }
+        return p;
+    }
     const uint32_t slot = (uint32_t)p.pos / a.page_size;  // a negative position is past any table
     if (p.pos < 0 || p.pos >= a.max_pos || n >= a.seqs || slot >= a.width) {
         p.pos = -1;
@@ -118,7 +133,7 @@ struct alignas(W * sizeof(E)) Row {
     E e[W];
 };
 
-template <bool FP16, bool E4M3, bool INTER, int W>
+template <bool FP16, bool E4M3, bool INTER, int W, bool PLACES>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a)
 {
     using Half = Row<W, uint16_t>;
@@ -129,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a)
     const uint32_t h0 = i0 / a.pieces, j0 = i0 - h0 * a.pieces;
     const uint32_t dh = step / a.pieces, dj = step - dh * a.pieces;
     for (uint32_t t = blockIdx.y; t < a.T; t += gridDim.y) {
-        const Place p = place_of(a, t);
+        const Place p = place_of<PLACES>(a, t);
         const float* cs = a.cos_sin + (int64_t)p.pos * a.rot;
         uint32_t h = h0, j = j0;
         for (uint32_t i = i0; i < items; i += step, h += dh, j += dj) {
@@ -215,8 +230,13 @@ hipError_t launch_pieces(const AppendArgs& a, hipStream_t stream)
     const bool few = (uint64_t)a.T * items <= kSlots;
     const uint32_t threads = ((items + rounds - 1) / rounds + 63) / 64 * 64;
     const uint32_t gy = a.T < 65535u ? a.T : 65535u;
-    hipLaunchKernelGGL((append_kernel<FP16, E4M3, INTER, W>), dim3(few ? rounds : 1, gy), dim3(threads),
-                       0, stream, a);
+    if (a.places) {
+        hipLaunchKernelGGL((append_kernel<FP16, E4M3, INTER, W, true>), dim3(few ? rounds : 1, gy), dim3(threads),
+                           0, stream, a);
+    } else {
+        hipLaunchKernelGGL((append_kernel<FP16, E4M3, INTER, W, false>), dim3(few ? rounds : 1, gy), dim3(threads),
+                           0, stream, a);
+    }
     return hipGetLastError();
 }
 
@@ -242,6 +262,11 @@ bool input_ok(const void* p, int64_t T, int64_t H, int64_t D, int64_t st, int64_
 
 extern "C" int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t stream)
 {
+    return xpress_kv_append_at(args, nullptr, stream);
+}
+
+extern "C" int xpress_kv_append_at(const xpress_kv_append_args* args, const int32_t* places, hipStream_t stream)
+{
     if (!args) return XPRESS_EINVAL;
     const xpress_kv_append_args& x = *args;
     const xpress_kv_cache& c = x.cache;
@@ -255,7 +280,9 @@ extern "C" int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t s
     if (x.rot_dim < 0 || x.rot_dim > c.dim || x.rot_dim % 2 != 0) return XPRESS_EINVAL;
     if (x.max_pos < 1 || x.max_pos > most) return XPRESS_EINVAL;
     if (x.rot_dim > 0 && (!x.cos_sin || !is_aligned(x.cos_sin, 4))) return XPRESS_EINVAL;
-    if (!x.positions || !is_aligned(x.positions, 4) || !is_aligned(x.seq_of, 4)) return XPRESS_EINVAL;
+    if (!x.positions || !is_aligned(x.positions, 4) || !is_aligned(x.seq_of, 4) || !is_aligned(places, 4)) {
+        return XPRESS_EINVAL;
+    }
     if (!x.seq_of && (c.seqs < 1 || x.T % c.seqs != 0)) return XPRESS_EINVAL;
     // work items of one token in 32 bits
     if ((x.Hq + 2 * c.heads) * c.dim > most) return XPRESS_EINVAL;
@@ -283,6 +310,7 @@ extern "C" int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t s
                       !apart_from_cache(c, cache_bytes, x.q_out, no))) ||
         !apart_from_cache(c, cache_bytes, x.positions, (size_t)x.T * 4u) ||
         !apart_from_cache(c, cache_bytes, x.seq_of, (size_t)x.T * 4u) ||
+        !apart_from_cache(c, cache_bytes, places, (size_t)x.T * 4u) ||
         !apart_from_cache(c, cache_bytes, c.page_table,
                           c.seqs ? (size_t)((c.seqs - 1) * c.stride_table + c.table_width) * 4u : 0)) {
         return XPRESS_EINVAL;
@@ -298,6 +326,7 @@ extern "C" int xpress_kv_append(const xpress_kv_append_args* args, hipStream_t s
     a.k_scale = c.k_scale;
     a.v_scale = c.v_scale;
     a.positions = x.positions;
+    a.places = places;
     a.seq_of = x.seq_of;
     a.page_table = c.page_table;
     a.cos_sin = x.cos_sin;

@@ -51,20 +51,18 @@ inline bool is_disjoint(Dim (&d)[K], int64_t inner)
     return true;
 }
 
-// The layout and pointers of a cache; *bytes receives the span of each of
-// its two arrays.
-inline bool cache_ok(const xpress_kv_cache& c, size_t* bytes)
+// The layout and pointers of a cache's two arrays; *bytes receives the span of
+// each.
+inline bool pool_ok(const xpress_kv_cache& c, size_t* bytes)
 {
     const int64_t most = 0x7FFFFFFFll;
     if (c.pages < 1 || c.pages > most || c.page_size < 1 || c.page_size > most || c.heads < 1 ||
-        c.heads > 65536 || c.dim < 1 || c.dim > 65536 || c.seqs < 0 || c.seqs > most ||
-        c.table_width < 1 || c.table_width > most / c.page_size) {
+        c.heads > 65536 || c.dim < 1 || c.dim > 65536) {
         return false;
     }
     if (c.dtype != XPRESS_BF16 && c.dtype != XPRESS_FP16 && c.dtype != XPRESS_E4M3) return false;
     if (c.stride_page < 1 || c.stride_head < 1 || c.stride_token < 1) return false;
-    if (c.stride_table < 0 || (c.seqs > 1 && c.stride_table < c.table_width)) return false;
-    if (!c.k || !c.v || c.k == c.v || !c.page_table || !is_aligned(c.page_table, 4)) return false;
+    if (!c.k || !c.v || c.k == c.v) return false;
     const int64_t e = element_bytes(c.dtype);
     if (!is_aligned(c.k, (size_t)e) || !is_aligned(c.v, (size_t)e)) return false;
     if (c.dtype != XPRESS_E4M3 && (c.k_scale || c.v_scale)) return false;
@@ -74,6 +72,34 @@ inline bool cache_ok(const xpress_kv_cache& c, size_t* bytes)
     if (span < 0 || !is_disjoint(d, c.dim)) return false;
     *bytes = (size_t)(span * e);
     return true;
+}
+
+// A table [seqs, width] of pages of page_size tokens: positions in 32 bits.
+inline bool table_ok(const int32_t* table, int64_t seqs, int64_t width, int64_t stride, int64_t page_size)
+{
+    const int64_t most = 0x7FFFFFFFll;
+    return seqs >= 0 && seqs <= most && page_size >= 1 && page_size <= most && width >= 1 &&
+           width <= most / page_size && stride >= 0 && (seqs <= 1 || stride >= width) &&
+           stride <= ((int64_t)1 << 58) / (seqs > 0 ? seqs : 1) && table && is_aligned(table, 4);
+}
+
+// The layout and pointers of a cache with its table; *bytes as above.
+inline bool cache_ok(const xpress_kv_cache& c, size_t* bytes)
+{
+    const int64_t most = 0x7FFFFFFFll;
+    if (c.page_size < 1 || c.seqs < 0 || c.seqs > most || c.table_width < 1 ||
+        c.table_width > most / c.page_size) {
+        return false;
+    }
+    if (c.stride_table < 0 || (c.seqs > 1 && c.stride_table < c.table_width)) return false;
+    if (!c.page_table || !is_aligned(c.page_table, 4)) return false;
+    return pool_ok(c, bytes);
+}
+
+// Bytes from a table's first entry to its last.
+inline size_t table_bytes(int64_t seqs, int64_t width, int64_t stride)
+{
+    return seqs > 0 ? (size_t)((seqs - 1) * stride + width) * 4u : 0;
 }
 
 // Whether [p, p + n) lies apart from both arrays of the cache (a null p does).

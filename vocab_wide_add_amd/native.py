@@ -120,6 +120,23 @@ def load():
         lib.xpress_sample_to_blk.restype = i32
         lib.xpress_sample_reserve.argtypes = [i64, i64, i64, vp]
         lib.xpress_sample_reserve.restype = i32
+        lib.xpress_kv_append_at.argtypes = [cp, vp, vp]
+        lib.xpress_sink_attention.argtypes = [cp, i64, vp]
+        lib.xpress_tree_attention.argtypes = [cp, vp, i64, i64, i64, vp]
+        lib.xpress_sparse_attention_reserve.argtypes = [i64] * 8 + [i32, vp]
+        lib.xpress_kv_fork.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, i64, vp, vp, vp]
+        lib.xpress_kv_copy.argtypes = [cp, vp, i64, vp]
+        lib.xpress_kv_grow.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp]
+        lib.xpress_kv_free.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i64, i64, vp]
+        lib.xpress_kv_compact.argtypes = [cp, vp, vp, i64, vp, i64, vp]
+        lib.xpress_beam_select.argtypes = [vp] * 6 + [i64] * 6 + [vp]
+        lib.xpress_beam_select_reserve.argtypes = [i64] * 4 + [vp]
+        lib.xpress_beam_reorder.argtypes = [cp, i64, vp, i64, i64, vp]
+        for f in (lib.xpress_kv_append_at, lib.xpress_sink_attention, lib.xpress_tree_attention,
+                  lib.xpress_sparse_attention_reserve, lib.xpress_kv_fork, lib.xpress_kv_copy,
+                  lib.xpress_kv_grow, lib.xpress_kv_free, lib.xpress_kv_compact, lib.xpress_beam_select,
+                  lib.xpress_beam_select_reserve, lib.xpress_beam_reorder):
+            f.restype = i32
         lib.append_at, lib.attention_at, lib.sample_at = [
             ctypes.cast(f, vp).value for f in (lib.xpress_kv_append, lib.xpress_paged_attention,
                                                lib.xpress_sample_to_blk)]
@@ -534,6 +551,13 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
                                 positions, cos_sin, seq_of, k_scale, v_scale, interleaved)
     if status is not None:
         return _check(status, "xpress_kv_append")
+    args = _append_args(q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin, seq_of, k_scale,
+                        v_scale, interleaved)
+    _check(lib.xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
+
+
+def _append_args(q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin, seq_of, k_scale, v_scale,
+                 interleaved) -> bytes:
     if (q is None) != (q_out is None):
         raise ValueError("q, q_out: both or neither expected")
     shape, dev = k.shape, k_cache.get_device()
@@ -542,7 +566,7 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
     if cache[7] != heads or cache[8] != dim:
         raise ValueError("k: [T, %d, %d] expected for this cache, got %s"
                          % (cache[7], cache[8], tuple(shape)))
-    code, dtype, i32 = _dtype(k, "k"), k.dtype, torch.int32
+    code, dtype, i32 = _dtype(k, "k"), k.dtype, _torch.int32
     kp, (kt, kh, _) = _rows(k, "k", shape, dtype, dev)
     vp, (vt, vh, _) = _rows(v, "v", shape, dtype, dev)
     if q is None:
@@ -555,12 +579,26 @@ def xpress_kv_append(q, k, v, q_out, k_cache, v_cache, page_table, positions, co
         cp, max_pos, rot = 0, 2 ** 31 - 1, 0
     else:
         max_pos, rot = cos_sin.shape
-        cp = _plain(cos_sin, "cos_sin", torch.float32, (max_pos, rot), dev)
-    args = _APPEND_ARGS.pack(
+        cp = _plain(cos_sin, "cos_sin", _torch.float32, (max_pos, rot), dev)
+    return _APPEND_ARGS.pack(
         *cache, qp, kp, vp, op, _plain(positions, "positions", i32, (T,), dev),
         _plain(seq_of, "seq_of", i32, (T,), dev), cp, T, hq, code, rot, max_pos,
         1 if interleaved else 0, qt, qh, kt, kh, vt, vh, ot, oh)
-    _check(lib.xpress_kv_append(args, _stream(stream)), "xpress_kv_append")
+
+
+def xpress_kv_append_at(q, k, v, q_out, k_cache, v_cache, page_table, places, positions, cos_sin,
+                        seq_of=None, k_scale=None, v_scale=None, interleaved: bool = False,
+                        stream=None) -> None:
+    """xpress_kv_append with places apart from positions: keys and values of token t go
+    to place places[t] (int32 [T]) of its sequence, rotated to positions[t]."""
+    lib = _lib or load()
+    _use_torch()
+    args = _append_args(q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin, seq_of, k_scale,
+                        v_scale, interleaved)
+    at = _plain(places, "places", _torch.int32, (k.shape[0],), k_cache.get_device())
+    if not at and k.shape[0]:
+        raise ValueError("places: an int32 tensor expected")
+    _check(lib.xpress_kv_append_at(args, at, _stream(stream)), "xpress_kv_append_at")
 
 
 def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: int, lse=None,
@@ -583,7 +621,16 @@ def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: 
                                       out, lse, k_scale, v_scale, max_len, window, scale)
     if status is not None:
         return _check(status, "xpress_paged_attention")
+    args = _attention_args(q, k_cache, v_cache, page_table, lens, out, max_len, lse, scale, window, k_scale,
+                           v_scale)
+    _check(lib.xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
+
+
+def _attention_args(q, k_cache, v_cache, page_table, lens, out, max_len, lse, scale, window, k_scale,
+                    v_scale) -> bytes:
     shape, dev = q.shape, k_cache.get_device()
+    if len(shape) != 4:
+        raise ValueError("q: [N, Q, Hq, dim] expected, got %s" % (tuple(shape),))
     N, Q, hq, dim = shape
     cache = _kv_cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
     if cache[8] != dim or cache[13] != N:
@@ -592,11 +639,155 @@ def xpress_paged_attention(q, k_cache, v_cache, page_table, lens, out, max_len: 
     code, dtype = _dtype(q, "q"), q.dtype
     qp, (qn, qi, qh, _) = _rows(q, "q", shape, dtype, dev)
     op, (on, oi, oh, _) = _rows(out, "out", shape, dtype, dev)
-    args = _ATTENTION_ARGS.pack(
-        *cache, qp, op, _plain(lse, "lse", torch.float32, (N, Q, hq), dev),
-        _plain(lens, "lens", torch.int32, (N,), dev), Q, hq, code, int(max_len), int(window),
+    return _ATTENTION_ARGS.pack(
+        *cache, qp, op, _plain(lse, "lse", _torch.float32, (N, Q, hq), dev),
+        _plain(lens, "lens", _torch.int32, (N,), dev), Q, hq, code, int(max_len), int(window),
         1.0 / math.sqrt(dim) if scale is None else float(scale), qn, qi, qh, on, oi, oh)
-    _check(lib.xpress_paged_attention(args, _stream(stream)), "xpress_paged_attention")
+
+
+def xpress_sink_attention(q, k_cache, v_cache, page_table, lens, out, max_len: int, window: int,
+                          sinks: int, lse=None, scale: float = None, k_scale=None, v_scale=None,
+                          stream=None) -> None:
+    """xpress_paged_attention with a window that leaves the first ``sinks`` tokens
+    visible: a query at position pos sees j <= pos with j > pos - window or j < sinks."""
+    lib = _lib or load()
+    _use_torch()
+    args = _attention_args(q, k_cache, v_cache, page_table, lens, out, max_len, lse, scale, window, k_scale,
+                           v_scale)
+    _check(lib.xpress_sink_attention(args, int(sinks), _stream(stream)), "xpress_sink_attention")
+
+
+def xpress_tree_attention(q, k_cache, v_cache, page_table, lens, tree, out, max_len: int, lse=None,
+                          scale: float = None, window: int = 0, sinks: int = 0, k_scale=None, v_scale=None,
+                          stream=None) -> None:
+    """xpress_paged_attention for a tree: the Q newest tokens of a sequence are nodes,
+    and node i sees node j where bit j % 32 of tree[n, i, j // 32] is set (int32 [N, Q,
+    ceil(Q / 32)], any strides, unit along the words; ``expand`` one tree to share it),
+    beside the tokens before the tree, windowed with sinks.  See the header."""
+    lib = _lib or load()
+    _use_torch()
+    args = _attention_args(q, k_cache, v_cache, page_table, lens, out, max_len, lse, scale, window, k_scale,
+                           v_scale)
+    N, Q = q.shape[0], q.shape[1]
+    at, (tn, ti, _) = _rows(tree, "tree", (N, Q, (Q + 31) // 32), _torch.int32, k_cache.get_device())
+    _check(lib.xpress_tree_attention(args, at, tn, ti, int(sinks), _stream(stream)), "xpress_tree_attention")
+
+
+def xpress_sparse_attention_reserve(N: int, Q: int, Hq: int, heads: int, dim: int, max_len: int,
+                                    window: int = 0, sinks: int = 0, tree: bool = False,
+                                    stream=None) -> None:
+    """Workspace of xpress_sink_attention, or with tree of xpress_tree_attention."""
+    _check(load().xpress_sparse_attention_reserve(int(N), int(Q), int(Hq), int(heads), int(dim), int(max_len),
+                                                  int(window), int(sinks), 1 if tree else 0, _stream(stream)),
+           "xpress_sparse_attention_reserve")
+
+
+def _pages_of(refs) -> tuple:
+    """(address, pages, device) of a page's counts, on the current device."""
+    if refs.dim() != 1:
+        raise ValueError("refs: int32 [pages] expected, got shape %s" % (tuple(refs.shape),))
+    dev = refs.get_device()
+    if dev < 0:
+        _elsewhere(refs, "refs", dev)
+    at = _plain(refs, "refs", _torch.int32, refs.shape, dev)
+    _on_current(dev)
+    return at, refs.shape[0], dev
+
+
+def _table(t, what: str, dev: int) -> tuple:
+    """(address, rows, width, row stride) of an int32 table."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s: int32 [rows, width] expected, got shape %s" % (what, tuple(shape)))
+    at, st = _rows(t, what, shape, _torch.int32, dev)
+    return at, shape[0], shape[1], st[0]
+
+
+def xpress_kv_fork(refs, table, lens, src, new_refs, new_table, copies, page_size: int, missing=None,
+                   stream=None) -> None:
+    """Row m of new_table continues row src[m] of table: whole pages are shared, the
+    part-filled last page stays with the source's first row, the others get a free page
+    and a line in copies (from, to, tokens) for xpress_kv_copy.  refs, new_refs int32
+    [pages], table int32 [N, width], new_table [M, width], lens [N], src [M] (or a tensor
+    of M elements, as xpress_beam_select's rows), copies [M, 3], missing [1] or None, all
+    int32.  See the header."""
+    lib = _lib or load()
+    _use_torch()
+    i32 = _torch.int32
+    rp, pages, dev = _pages_of(refs)
+    tp, N, width, st = _table(table, "table", dev)
+    np_, M, w2, sn = _table(new_table, "new_table", dev)
+    if w2 != width:
+        raise ValueError("new_table: [M, %d] expected as table, got %s" % (width, tuple(new_table.shape)))
+    src = src.reshape(-1) if src.is_contiguous() else src
+    _check(lib.xpress_kv_fork(
+        rp, pages, tp, st, _plain(lens, "lens", i32, (N,), dev), N, _plain(src, "src", i32, (M,), dev), M, width,
+        int(page_size), _plain(new_refs, "new_refs", i32, (pages,), dev), np_, sn,
+        _plain(copies, "copies", i32, (M, 3), dev), _plain(missing, "missing", i32, (1,), dev), _stream(stream)),
+        "xpress_kv_fork")
+
+
+def _pool_fields(k_cache, v_cache) -> bytes:
+    """xpress_kv_cache without a table."""
+    dev = k_cache.get_device()
+    none = _torch.empty((0, 1), dtype=_torch.int32, device=k_cache.device)
+    return struct.pack(_KV_CACHE, *_kv_cache(k_cache, v_cache, none, None, None, dev))
+
+
+def xpress_kv_copy(k_cache, v_cache, copies, stream=None) -> None:
+    """For every line (from, to, tokens) of copies (int32 [count, 3]) the first `tokens`
+    places of page `from` go to page `to`, keys and values of all heads; lines with a
+    page outside the pool do nothing."""
+    lib = _lib or load()
+    _use_torch()
+    cache = _pool_fields(k_cache, v_cache)
+    if copies.dim() != 2:
+        raise ValueError("copies: int32 [count, 3] expected, got shape %s" % (tuple(copies.shape),))
+    count = copies.shape[0]
+    at = _plain(copies, "copies", _torch.int32, (count, 3), k_cache.get_device())
+    _check(lib.xpress_kv_copy(cache, at, count, _stream(stream)), "xpress_kv_copy")
+
+
+def xpress_kv_grow(refs, table, have, want, page_size: int, missing=None, stream=None) -> None:
+    """Free pages for the tokens have[n] <= p < want[n] of each row of table, in place;
+    have, want int32 [N], missing int32 [1] or None: the pages that there were not."""
+    lib = _lib or load()
+    _use_torch()
+    i32 = _torch.int32
+    rp, pages, dev = _pages_of(refs)
+    tp, N, width, st = _table(table, "table", dev)
+    _check(lib.xpress_kv_grow(rp, pages, tp, st, N, width, int(page_size), _plain(have, "have", i32, (N,), dev),
+                              _plain(want, "want", i32, (N,), dev), _plain(missing, "missing", i32, (1,), dev),
+                              _stream(stream)), "xpress_kv_grow")
+
+
+def xpress_kv_free(refs, table, lens, page_size: int, window: int = 0, sinks: int = 0, stream=None) -> None:
+    """Gives back, in place, the pages of which no query at or after position lens[n]
+    sees a token; lens int32 [N], 0 for a finished sequence."""
+    lib = _lib or load()
+    _use_torch()
+    rp, pages, dev = _pages_of(refs)
+    tp, N, width, st = _table(table, "table", dev)
+    _check(lib.xpress_kv_free(rp, pages, tp, st, N, width, int(page_size),
+                              _plain(lens, "lens", _torch.int32, (N,), dev), int(window), int(sinks),
+                              _stream(stream)), "xpress_kv_free")
+
+
+def xpress_kv_compact(k_cache, v_cache, page_table, start, path, count, stream=None) -> None:
+    """The kept nodes of a tree move together: the token at place start[n] + path[n, j]
+    goes to place start[n] + j, for j < count[n].  start, count int32 [N], path int32
+    [N, longest] of ascending nodes."""
+    lib = _lib or load()
+    _use_torch()
+    i32, dev = _torch.int32, k_cache.get_device()
+    cache = struct.pack(_KV_CACHE, *_kv_cache(k_cache, v_cache, page_table, None, None, dev))
+    N = page_table.shape[0]
+    if path.dim() != 2 or path.shape[0] != N:
+        raise ValueError("path: int32 [%d, longest] expected, got shape %s" % (N, tuple(path.shape)))
+    at, st = _rows(path, "path", path.shape, i32, dev)
+    _check(lib.xpress_kv_compact(cache, _plain(start, "start", i32, (N,), dev), at, st[0],
+                                 _plain(count, "count", i32, (N,), dev), path.shape[1], _stream(stream)),
+           "xpress_kv_compact")
 
 
 def xpress_paged_attention_reserve(N: int, Q: int, Hq: int, heads: int, dim: int, max_len: int,
@@ -689,6 +880,74 @@ def xpress_sample_reserve(N: int, B: int, V: int, stream=None) -> None:
     spread few rows over the chip, as before a capture."""
     _check(load().xpress_sample_reserve(int(N), int(B), int(V), _stream(stream)),
            "xpress_sample_reserve")
+
+
+def xpress_beam_select(base, bias, scores, best, rows, ids, N: int, beams: int, V: int, K: int,
+                       stride_base_r: int, stride_bias_r: int = 0, stream=None) -> None:
+    """The K best of each sequence's continuations, by scores[r] + log softmax(bf16(base +
+    bias))[v] of its rows r = n * beams + i: best fp32 [N, K], rows int32 [N, K], ids
+    int64 [N, K], in descending order.  bias may be None; base and bias as for
+    xpress_sample_to_blk; scores fp32 [N * beams]."""
+    lib = _lib or load()
+    t = _use_torch()
+    r, n = int(N) * int(beams), int(N) * int(K)
+    if n > 0 and r > 0:
+        dev = base.device if hasattr(base, "data_ptr") else None
+        _logits(base, "base", ((r - 1) * int(stride_base_r) + int(V)) * 2, dev)
+        if bias is not None:
+            _logits(bias, "bias", ((r - 1) * int(stride_bias_r) + int(V)) * 2, dev)
+        _numbers(scores, "scores", t.float32, r, dev)
+        _numbers(best, "best", t.float32, n, dev)
+        _numbers(rows, "rows", t.int32, n, dev)
+        _numbers(ids, "ids", t.int64, n, dev)
+        if dev is not None and dev.type == "cuda":
+            _on_current(dev.index)
+    _check(lib.xpress_beam_select(_ptr(base), _ptr(bias), _ptr(scores), _ptr(best), _ptr(rows), _ptr(ids), int(N),
+                                  int(beams), int(V), int(K), int(stride_base_r), int(stride_bias_r),
+                                  _stream(stream)), "xpress_beam_select")
+
+
+def xpress_beam_select_reserve(N: int, beams: int, V: int, K: int, stream=None) -> None:
+    """Grow the (device, stream) workspace to what xpress_beam_select needs."""
+    _check(load().xpress_beam_select_reserve(int(N), int(beams), int(V), int(K), _stream(stream)),
+           "xpress_beam_select_reserve")
+
+
+_STATE = struct.Struct("2Q3q")
+
+
+def xpress_beam_reorder(states, src, stream=None) -> None:
+    """For every pair (old, new) of states: new[m] = old[src[m]], zeros where src[m] is no
+    row of old.  old [N, ...] and new [M, ...] of one type and shape behind the first
+    dimension, contiguous there; src int32 of M elements, as xpress_beam_select's rows."""
+    lib = _lib or load()
+    _use_torch()
+    dev = src.get_device()
+    if dev < 0:
+        _elsewhere(src, "src", dev)
+    _on_current(dev)
+    M = src.numel()
+    at = _plain(src, "src", _torch.int32, src.shape, dev)
+    N, packed = None, []
+    for i, (old, new) in enumerate(states):
+        what = "states[%d]" % i
+        if old.dtype is not new.dtype or old.dim() < 1 or new.dim() < 1 or old.shape[1:] != new.shape[1:] \
+                or new.shape[0] != M or (N is not None and old.shape[0] != N):
+            raise ValueError("%s: (old [N, ...], new [%d, ...]) of one type, row shape and N expected, got %s "
+                             "of %s and %s of %s" % (what, M, old.dtype, tuple(old.shape), new.dtype,
+                                                     tuple(new.shape)))
+        for t in (old, new):
+            if t.get_device() != dev:
+                _elsewhere(t, what, dev)
+            if t.shape[0] > 0 and not t[0].is_contiguous():
+                raise ValueError("%s: contiguous rows expected, got strides %s" % (what, t.stride()))
+        N, size = old.shape[0], old.element_size()
+        row = size
+        for x in old.shape[1:]:
+            row *= x
+        packed.append(_STATE.pack(old.data_ptr(), new.data_ptr(), old.stride(0) * size, new.stride(0) * size, row))
+    _check(lib.xpress_beam_reorder(b"".join(packed), len(packed), at, N or 0, M, _stream(stream)),
+           "xpress_beam_reorder")
 
 
 def xpress_last_hip_error() -> int:
