@@ -83,7 +83,7 @@ CASES = [
     (5, 2, 32000, 2, True, 32011, 0), (1, 1, 152064, 128, True, None, 0), (2, 5, 9000, 5, False, None, 1),
     (1, 16, 20000, 32, False, None, 8), (4, 1, 300, 128, True, None, 0), (1, 2, 140001, 7, True, 140008, 0),
     (70, 8, 600, 8, False, None, 0), (1, 300, 64, 100, False, None, 0), (2, 2, 131073, 3, False, None, 0),
-    (40, 16, 4500, 3, True, None, 0),
+    (40, 16, 4500, 3, True, None, 0), (1, 600, 40, 8, False, None, 0), (1, 1100, 3, 20, True, None, 0),
 ]
 
 
@@ -105,6 +105,9 @@ def test_ties_go_to_the_lower_row_then_the_lower_id(V, K):
     one = torch.randint(0, 4, (1, V), generator=g).to(torch.bfloat16)
     verify(one.expand(6, V), None, torch.zeros(6), 2, 3, K)
     verify(torch.full((6, V), -2.5, dtype=torch.bfloat16), None, torch.zeros(6), 2, 3, K)
+    # more equal candidates, and more lists, than are ranked by counting
+    verify(one.expand(300, V), None, torch.zeros(300), 1, 300, K)
+    verify(one.expand(600, V), None, torch.zeros(600), 1, 600, K)
     # -0 equals +0
     zero = torch.zeros(2, V, dtype=torch.bfloat16)
     zero[:, ::2] = -0.0

@@ -41,12 +41,16 @@ namespace {
 
 using namespace xpress;
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 constexpr uint32_t kThreads = 512;
 constexpr uint32_t kWaves = kThreads / 64;
 constexpr uint32_t kRuns = 16384;          // of a part: 131072 logits
 constexpr uint32_t kMostK = 128;
 constexpr uint32_t kAbove = 4096;          // runs above T0: fewer than K threads', 32 each
 constexpr uint32_t kFound = 2304;          // logits that are ranked
+constexpr uint32_t kFew = 512;             // runs of the common case
+constexpr uint32_t kAhead = 4;             // vectors that a thread has on their way
 constexpr float kLh = 0x1.7154p+0f;        // log2(e) to 15 bits
 constexpr double kRest = 1.4426950408889634074 - 0x1.7154p+0;
 constexpr double kLn2 = 0.69314718055994530942;
@@ -150,14 +154,14 @@ __device__ __forceinline__ double wave_sum(double v)
 }
 
 struct PartShared {
-    uint16_t runs[kRuns];
-    uint32_t above[kAbove];              // runs above T0
-    uint64_t found[kFound];
+    __align__(16) uint16_t runs[kRuns];
+    uint16_t above[kAbove];
+    __align__(16) uint64_t found[kFound];
     uint32_t maxima[kThreads];
     uint32_t firsts[kMostK];
     uint32_t counts[kWaves];
     double part[kWaves];
-    uint32_t n_above, n_found, threshold, counted;
+    uint32_t n_above, n_found, threshold, n_runs, counted;
 };
 
 // Sum of v over the threads before this one; *total over all.
@@ -184,20 +188,176 @@ __device__ __forceinline__ uint32_t ranks(uint32_t v, uint32_t* sums, uint32_t* 
     return before + x - v;
 }
 
+__device__ __forceinline__ uint32_t wave_most(uint32_t v)
+{
+    v = max(v, dpp_u32<0xB1>(v));   // lane ^ 1, ^ 2, the other quad of 8, the other 8 of 16
+    v = max(v, dpp_u32<0x4E>(v));
+    v = max(v, dpp_u32<0x141>(v));
+    v = max(v, dpp_u32<0x140>(v));
+    v = max(v, (uint32_t)__shfl_xor(v, 16));
+    return max(v, (uint32_t)__shfl_xor(v, 32));
+}
+
+// Adds the logits of a run that are not below `low` to the found ones.
+template <typename R>
+__device__ __forceinline__ void take_run(PartShared& s, const R& z, uint32_t e, uint32_t low)
+{
+    const u32x4 v = z.at(e);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const uint32_t o = order_of(x & 1 ? bf16_hi(v[x / 2]) : bf16_lo(v[x / 2]));
+        if (o > 0 && o >= low) {
+            const uint32_t to = atomicAdd(&s.n_found, 1u);
+            if (to < kFound) s.found[to] = (uint64_t)o << 32 | (kNoIndex - (e + x));
+        }
+    }
+}
+
+// The K largest logits of a part, by the largest of its runs: see the top of the file.
+// Whatever the values are; the common case does without most of it.
+template <typename R>
+__device__ void find_any(PartShared& s, const R& z, uint32_t vec0, uint32_t vecs, uint32_t K, uint32_t best)
+{
+    const uint32_t tid = threadIdx.x;
+    __syncthreads();
+    s.maxima[tid] = best;
+    if (tid == 0) s.n_above = s.n_found = s.threshold = 0;
+    __syncthreads();
+    // T0: the largest value that fewer than K of the threads' maxima pass, but K or
+    // more reach
+    uint32_t better = 0, equal = 0;
+    for (uint32_t i = 0; i < kThreads; ++i) {
+        better += s.maxima[i] > best;
+        equal += s.maxima[i] == best;
+    }
+    if (better < K && better + equal >= K) s.threshold = best;
+    __syncthreads();
+    uint32_t low = s.threshold;   // 0: fewer than K threads have a logit
+    const uint32_t span = (vecs + kThreads - 1) / kThreads;   // runs of a thread, one after the other
+    const uint32_t run0 = min(tid * span, vecs), run1 = min(run0 + span, vecs);
+    for (uint32_t i = run0; i < run1; ++i) {
+        // fewer than K threads' runs: fewer than kAbove
+        if (s.runs[i] > low) s.above[atomicAdd(&s.n_above, 1u) % kAbove] = (uint16_t)i;
+    }
+    __syncthreads();
+    const uint32_t n0 = s.n_above;
+    __syncthreads();
+    if (n0 >= K) {
+        // T: the K-th largest of these runs
+        for (uint32_t i = tid; i < n0; i += kThreads) {
+            const uint32_t o = s.runs[s.above[i]];
+            uint32_t more = 0, same = 0;
+            for (uint32_t j = 0; j < n0; ++j) {
+                const uint32_t p = s.runs[s.above[j]];
+                more += p > o;
+                same += p == o;
+            }
+            if (more < K && more + same >= K) s.threshold = o;
+        }
+        __syncthreads();
+        low = s.threshold;
+    }
+    // the first K runs, in order, whose largest is T
+    uint32_t reach = 0;
+    for (uint32_t i = run0; i < run1; ++i) reach += low > 0 && s.runs[i] == low;
+    uint32_t reached;
+    uint32_t at = ranks(reach, s.counts, &reached);
+    for (uint32_t i = run0; i < run1 && at < K; ++i) {
+        if (low > 0 && s.runs[i] == low) s.firsts[at++] = i;
+    }
+    __syncthreads();
+    reached = min(reached, K);
+    for (uint32_t i = tid; i < n0 + reached; i += kThreads) {
+        const uint32_t run = i < n0 ? s.above[i] : s.firsts[i - n0];
+        if (i >= n0 || s.runs[run] > low) take_run(s, z, (vec0 + run) * 8, low);
+    }
+    __syncthreads();
+}
+
+// The same where few runs come into question (false: they do not, nothing is done).
+// T0 from the waves instead of the threads: the least of the waves' q-th largest, q =
+// K / waves, is below K runs too, and costs q rounds over a wave.
+template <typename R>
+__device__ bool find_few(PartShared& s, const R& z, uint32_t vec0, uint32_t vecs, uint32_t K, uint32_t best)
+{
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    const uint32_t waves = min(kWaves, (vecs + 63) / 64), q = (K + waves - 1) / waves;
+    uint32_t key = best << 6 | lane, least = 0;
+    for (uint32_t i = 0; i < min(q, 64u); ++i) {
+        const uint32_t m = wave_most(key);
+        key = key == m ? 0 : key;
+        least = m >> 6;
+    }
+    if (lane == 0) s.counts[wave] = q > 64 ? 0 : least;
+    __syncthreads();   // and the runs are all there
+    uint32_t low = s.counts[0];
+    for (uint32_t w = 1; w < waves; ++w) low = min(low, s.counts[w]);
+    low = max(low, 1u);
+    const uint32_t words = (vecs + 7) / 8;
+    for (uint32_t i = tid; i < words; i += kThreads) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(&s.runs[i * 8]);
+        u16x2 top = {0, 0};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t two = v[w];   // (a bit cast of a vector's element takes its first one)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, two));
+        }
+        if (max((uint32_t)top.x, (uint32_t)top.y) < low) continue;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            if ((x & 1 ? v[x / 2] >> 16 : v[x / 2] & 0xFFFFu) >= low) {
+                const uint32_t at = atomicAdd(&s.n_above, 1u);
+                if (at < kFew) s.above[at] = (uint16_t)(i * 8 + x);
+            }
+        }
+    }
+    __syncthreads();
+    const uint32_t n0 = s.n_above;
+    if (n0 > kFew) return false;
+    uint32_t runs = n0;
+    if (n0 > K) {
+        for (uint32_t i = tid; i < n0; i += kThreads) {
+            const uint32_t o = s.runs[s.above[i]];
+            uint32_t more = 0, same = 0;
+            for (uint32_t j = 0; j < n0; ++j) {
+                const uint32_t p = s.runs[s.above[j]];
+                more += p > o;
+                same += p == o;
+            }
+            if (more < K && more + same >= K) {
+                s.threshold = o;
+                s.n_runs = more + same;
+            }
+        }
+        __syncthreads();
+        low = s.threshold;
+        runs = s.n_runs;
+    }
+    if (runs > kFound / 8) return false;
+    for (uint32_t i = tid; i < n0; i += kThreads) {
+        const uint32_t run = s.above[i];
+        if (s.runs[run] >= low) take_run(s, z, (vec0 + run) * 8, low);
+    }
+    __syncthreads();
+    return true;
+}
+
 template <bool VEC, bool BIAS>
-__global__ void __launch_bounds__(kThreads) part_kernel(BeamArgs a)
+__global__ void __launch_bounds__(kThreads, 4) part_kernel(BeamArgs a)
 {
     __shared__ PartShared s;
     const uint32_t unit = a.first + blockIdx.x, tid = threadIdx.x;
     const uint32_t row = unit / a.parts, part = unit - row * a.parts;
     const Row<VEC, BIAS> z = {a.base + row * a.stride_base, BIAS ? a.bias + row * a.stride_bias : nullptr, a.V};
     const uint32_t all_vecs = (a.V + 7) / 8, vec0 = part * a.part_vecs;
-    const uint32_t vecs = vec0 < all_vecs ? min(a.part_vecs, all_vecs - vec0) : 0;
+    const uint32_t vecs = min(a.part_vecs, all_vecs - vec0);
+    if (tid == 0) s.n_above = s.n_found = s.counted = 0;
+    if (tid < 8) s.runs[min(vecs + tid, kRuns - 1)] = 0;   // the last word of runs; a run there comes after
+    __syncthreads();
 
     Sum sum;
     uint32_t best = 0;   // the thread's largest, in the order
-    for (uint32_t i = tid; i < vecs; i += kThreads) {
-        const u32x4 v = z.at((vec0 + i) * 8);
+    auto go = [&](const u32x4& v, uint32_t i) {
         float x[8], top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -209,79 +369,54 @@ __global__ void __launch_bounds__(kThreads) part_kernel(BeamArgs a)
         const uint32_t o = order_of(top);
         s.runs[i] = (uint16_t)o;
         best = max(best, o);
-    }
-    if (tid == 0) s.n_above = s.n_found = s.threshold = s.counted = 0;
-    s.maxima[tid] = best;
-    __syncthreads();
-
-    // T0: the K-th largest of the threads' maxima
-    uint32_t better = 0, most = 0;
-    for (uint32_t i = 0; i < kThreads; ++i) {
-        const uint32_t o = s.maxima[i];
-        better += o > best;
-        most = max(most, o);
-    }
-    // the largest value that fewer than K maxima pass but K or more reach
-    if (better < a.K) {
-        uint32_t equal = 0;
-        for (uint32_t i = 0; i < kThreads; ++i) equal += s.maxima[i] == best;
-        if (better + equal >= a.K) s.threshold = best;
-    }
-    __syncthreads();
-    uint32_t low = s.threshold;   // 0: fewer than K threads have a logit
-    uint32_t span = (vecs + kThreads - 1) / kThreads;   // runs of a thread, one after the other
-    const uint32_t run0 = min(tid * span, vecs), run1 = min(run0 + span, vecs);
-    for (uint32_t i = run0; i < run1; ++i) {
-        if (s.runs[i] > low) {
-            const uint32_t at = atomicAdd(&s.n_above, 1u);
-            if (at < kAbove) s.above[at] = i;
-        }
-    }
-    __syncthreads();
-    const uint32_t n0 = s.n_above;
-    __syncthreads();
-    if (n0 >= a.K) {
-        // T: the K-th largest of these runs' maxima
-        for (uint32_t i = tid; i < n0; i += kThreads) {
-            const uint32_t o = s.runs[s.above[i]];
-            uint32_t more = 0, same = 0;
-            for (uint32_t j = 0; j < n0; ++j) {
-                const uint32_t p = s.runs[s.above[j]];
-                more += p > o;
-                same += p == o;
-            }
-            if (more < a.K && more + same >= a.K) s.threshold = o;
-        }
-        __syncthreads();
-        low = s.threshold;
-    }
-    // the first K runs, in order, whose largest is T (none where T is none)
-    uint32_t reach = 0;
-    for (uint32_t i = run0; i < run1; ++i) reach += low > 0 && s.runs[i] == low;
-    uint32_t reached;
-    uint32_t at = ranks(reach, s.counts, &reached);
-    for (uint32_t i = run0; i < run1 && at < a.K; ++i) {
-        if (low > 0 && s.runs[i] == low) s.firsts[at++] = i;
-    }
-    __syncthreads();
-    reached = min(reached, a.K);
-    // their logits from T on
-    for (uint32_t i = tid; i < n0 + reached; i += kThreads) {
-        const uint32_t run = i < n0 ? s.above[i] : s.firsts[i - n0];
-        if (i < n0 && s.runs[run] <= low) continue;
-        const uint32_t e = (vec0 + run) * 8;
-        const u32x4 v = z.at(e);
+    };
+    if constexpr (VEC) {
+        // whole vectors, kAhead of a thread at once and as many on their way
+        const uint32_t whole = min(vecs, a.V / 8 - min(a.V / 8, vec0));
+        u32x4 b[kAhead], c[kAhead];
+        auto load = [&](uint32_t i0) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const float f = x & 1 ? bf16_hi(v[x / 2]) : bf16_lo(v[x / 2]);
-            const uint32_t o = order_of(f);
-            if (o > 0 && o >= low) {
-                const uint32_t to = atomicAdd(&s.n_found, 1u);
-                if (to < kFound) s.found[to] = (uint64_t)o << 32 | (kNoIndex - (e + x));
+            for (uint32_t u = 0; u < kAhead; ++u) {
+                const uint32_t i = min(i0 + u * kThreads + tid, whole - 1);
+                b[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.base + (vec0 + i) * 8));
+                if constexpr (BIAS) {
+                    c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(z.bias + (vec0 + i) * 8));
+                }
+            }
+        };
+        if (whole > 0) {
+            load(0);
+            for (uint32_t i0 = 0; i0 < whole; i0 += kAhead * kThreads) {
+                u32x4 v[kAhead];
+#pragma unroll
+                for (uint32_t u = 0; u < kAhead; ++u) {
+                    v[u] = b[u];
+                    if constexpr (BIAS) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) v[u][w] = add_round2(v[u][w], c[u][w]);
+                    }
+                }
+                if (i0 + kAhead * kThreads < whole) load(i0 + kAhead * kThreads);
+#pragma unroll
+                for (uint32_t u = 0; u < kAhead; ++u) {
+                    const uint32_t i = i0 + u * kThreads + tid;
+                    if (i < whole) go(v[u], i);
+                }
             }
         }
+        if (whole < vecs && tid == 0) go(z.at((vec0 + whole) * 8), whole);   // the row's end
+    } else {
+        for (uint32_t i = tid; i < vecs; i += kThreads) go(z.at((vec0 + i) * 8), i);
     }
-    __syncthreads();
+
+    uint32_t most = wave_most(best);
+    if ((tid & 63) == 0) s.maxima[tid / 64] = most;
+    if (!find_few(s, z, vec0, vecs, a.K, best)) {
+        for (uint32_t w = 0; w < kWaves; ++w) most = max(most, s.maxima[w]);
+        find_any(s, z, vec0, vecs, a.K, best);
+    } else {
+        for (uint32_t w = 0; w < kWaves; ++w) most = max(most, s.maxima[w]);
+    }
     const uint32_t n = min(s.n_found, kFound);
     uint64_t* list = a.lists + (int64_t)unit * a.K;
     for (uint32_t i = tid; i < n; i += kThreads) {
@@ -311,9 +446,9 @@ __global__ void __launch_bounds__(kThreads) part_kernel(BeamArgs a)
         __syncthreads();
         total = (double)s.counted;
     } else {
-        // 2^(z L - r) against 2^(m L - R): R the integer next to m L
+        // 2^(z Lh - r) against 2^(m Lh - R): R the integer next to m Lh
         const double R = rint((double)m * (double)kLh);
-        double v = ((double)sum.y + kRest * kLn2 * ((double)sum.yz - (double)m * (double)sum.y));
+        double v = (double)sum.y + kRest * kLn2 * ((double)sum.yz - (double)m * (double)sum.y);
         v = best ? ldexp(v, (int)((double)sum.r - R)) : 0.0;
         v = wave_sum(v);
         if ((tid & 63) == 0) s.part[tid / 64] = v;
@@ -327,11 +462,14 @@ __global__ void __launch_bounds__(kThreads) part_kernel(BeamArgs a)
 }
 
 constexpr uint32_t kJoinThreads = 256;
+constexpr uint32_t kRanked = 512;    // candidates, and lists, that are ranked by counting
+constexpr uint32_t kDirect = 32;     // candidates that are all ranked
 
-// A candidate of the join.
+// A candidate of the join: larger first.  rest: the beam, reversed, in 16 bits, over the
+// 48 of the list's key; 0: none.
 struct Candidate {
     double score;
-    uint64_t rest;   // larger first: row, then logit and id
+    uint64_t rest;
 
     __device__ __forceinline__ bool before(const Candidate& o) const
     {
@@ -339,89 +477,148 @@ struct Candidate {
     }
 };
 
-__device__ __forceinline__ Candidate better_of(const Candidate& x, const Candidate& y)
+struct Beams {
+    const BeamArgs& a;
+    const double *shift, *top;   // of a beam: its score less the log of its sum, and its largest
+    uint32_t n;
+
+    __device__ __forceinline__ Candidate of(uint32_t list, uint64_t key) const
+    {
+        const uint32_t b = list / a.parts;
+        const double z = (double)value_at((uint32_t)(key >> 32)), d = z == top[b] ? 0.0 : z - top[b];
+        // shift -inf: not in use; d -inf: beside +inf
+        if (key == 0 || shift[b] == -INFINITY || d == -INFINITY) return Candidate{-INFINITY, 0};
+        return Candidate{shift[b] + d, (uint64_t)(65535u - b) << 48 | key};
+    }
+
+    __device__ __forceinline__ uint64_t key(uint32_t list, uint32_t at) const
+    {
+        return a.lists[((int64_t)n * (a.beams * a.parts) + list) * a.K + at];
+    }
+
+    __device__ __forceinline__ void put(uint32_t k, const Candidate& c) const
+    {
+        const int64_t to = (int64_t)n * a.K + k;
+        a.best[to] = c.rest ? (float)c.score : -INFINITY;
+        a.rows_out[to] = c.rest ? (int32_t)(n * a.beams + 65535u - (uint32_t)(c.rest >> 48)) : -1;
+        a.ids[to] = c.rest ? key_index(c.rest) : -1;
+    }
+};
+
+// Every list's first candidate that is not taken yet meets the others', K times.
+__device__ void join_by_turns(const Beams& beams, uint32_t* taken)
 {
-    return x.before(y) ? x : y;
+    __shared__ Candidate won[kJoinThreads / 64];
+    const BeamArgs& a = beams.a;
+    const uint32_t tid = threadIdx.x, lists = a.beams * a.parts;
+    for (uint32_t i = tid; i < lists; i += kJoinThreads) taken[i] = 0;
+    for (uint32_t k = 0; k < a.K; ++k) {
+        Candidate mine = {-INFINITY, 0};
+        uint32_t list = 0;
+        for (uint32_t l = tid; l < lists; l += kJoinThreads) {
+            if (taken[l] >= a.K) continue;
+            const Candidate c = beams.of(l, beams.key(l, taken[l]));
+            if (c.before(mine)) {
+                mine = c;
+                list = l;
+            }
+        }
+        Candidate w = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const Candidate o = {__shfl_xor(w.score, d), (uint64_t)__shfl_xor((unsigned long long)w.rest, d)};
+            if (o.before(w)) w = o;
+        }
+        if ((tid & 63) == 0) won[tid / 64] = w;
+        __syncthreads();
+        w = won[0];
+        for (uint32_t i = 1; i < kJoinThreads / 64; ++i) {
+            if (won[i].before(w)) w = won[i];
+        }
+        if (tid == 0) beams.put(k, w);
+        if (w.rest != 0 && mine.rest == w.rest) taken[list] += 1;
+        __syncthreads();
+    }
 }
 
-// A workgroup takes a sequence: every list's first candidate that is not taken yet
-// meets the others', K times.
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(BeamArgs a)
+// A workgroup takes a sequence.  Of its lists' candidates those that can be among the K
+// best are ranked by counting.  With d = K / lists rounded up, the K / d-th largest of
+// the lists' d-th candidates is below K candidates or equal to some, and few others
+// pass it.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(BeamArgs a, uint32_t group)
 {
-    extern __shared__ double shift[];   // of a beam: its score less the log of its sum, and its largest
-    __shared__ double win_score[kJoinThreads / 64];
-    __shared__ uint64_t win_key[kJoinThreads / 64];
+    extern __shared__ double shift[];
+    __shared__ __align__(16) Candidate few[kRanked];
+    __shared__ uint32_t count;
+    __shared__ double least;
     const uint32_t n = a.first + blockIdx.x, tid = threadIdx.x;
     const uint32_t lists = a.beams * a.parts;
     double* top = shift + a.beams;
     uint32_t* taken = reinterpret_cast<uint32_t*>(top + a.beams);   // of each list
-    for (uint32_t i = tid; i < lists; i += kJoinThreads) taken[i] = 0;
-    for (uint32_t b = tid; b < a.beams; b += kJoinThreads) {
-        const int64_t unit = (int64_t)(n * a.beams + b) * a.parts;
+    if (tid == 0) {
+        count = 0;
+        least = -INFINITY;
+    }
+    // `group` lanes a beam, a power of two
+    const uint32_t lane = tid % group;
+    for (uint32_t b0 = 0; b0 < a.beams; b0 += kJoinThreads / group) {
+        const uint32_t b = b0 + tid / group;
+        const bool on = b < a.beams;
+        const int64_t unit = (int64_t)(n * a.beams + (on ? b : 0)) * a.parts;
         uint32_t o = 0;
-        for (uint32_t p = 0; p < a.parts; ++p) o = max(o, (uint32_t)(a.lists[(unit + p) * a.K] >> 32));
+        for (uint32_t p = lane; p < a.parts; p += group) o = max(o, (uint32_t)(a.lists[(unit + p) * a.K] >> 32));
+        for (uint32_t d = 1; d < group; d *= 2) o = max(o, (uint32_t)__shfl_xor(o, d));
         const double m = (double)value_at(o);
         double total = 0.0;
-        for (uint32_t p = 0; p < a.parts; ++p) {
+        for (uint32_t p = lane; p < a.parts; p += group) {
             const uint32_t q = (uint32_t)(a.lists[(unit + p) * a.K] >> 32);
             if (q) total += a.sums[unit + p] * (q == o ? 1.0 : exp((double)value_at(q) - m));
         }
-        const double score = (double)a.scores[n * a.beams + b];
-        const bool lives = o && fabs(score) < INFINITY;
-        shift[b] = lives ? score - log(total) : -INFINITY;
-        top[b] = m;
+        for (uint32_t d = 1; d < group; d *= 2) total += __shfl_xor(total, d);
+        if (on && lane == 0) {
+            const double score = (double)a.scores[n * a.beams + b];
+            shift[b] = o && fabs(score) < INFINITY ? score - log(total) : -INFINITY;
+            top[b] = m;
+        }
     }
     __syncthreads();
-    for (uint32_t k = 0; k < a.K; ++k) {
-        Candidate mine = {-INFINITY, 0};
-        uint32_t list = ~0u, beam = 0;
-        uint64_t key = 0;
-        for (uint32_t l = tid; l < lists; l += kJoinThreads) {
-            const uint32_t at = taken[l];
-            if (at >= a.K) continue;
-            const uint32_t b = l / a.parts;
-            const uint64_t x = a.lists[((int64_t)n * lists + l) * a.K + at];
-            if (x == 0 || shift[b] == -INFINITY) continue;
-            const float z = value_at((uint32_t)(x >> 32));
-            const double d = (double)z == top[b] ? 0.0 : (double)z - top[b];
-            if (d == -INFINITY) continue;   // beside +inf
-            // 16 bits of the beam, reversed, above the key's 48
-            const Candidate c = {shift[b] + d, (uint64_t)(65535u - b) << 48 | x};
-            if (list == ~0u || c.before(mine)) {
-                mine = c;
-                list = l;
-                beam = b;
-                key = x;
-            }
-        }
-        Candidate w = list == ~0u ? Candidate{-INFINITY, 0} : mine;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const Candidate o = {__shfl_xor(w.score, d), (uint64_t)__shfl_xor((unsigned long long)w.rest, d)};
-            w = better_of(w, o);
-        }
-        if ((tid & 63) == 0) {
-            win_score[tid / 64] = w.score;
-            win_key[tid / 64] = w.rest;
-        }
+    const Beams beams = {a, shift, top, n};
+    const uint32_t all = lists * a.K;
+    if (lists > kRanked) return join_by_turns(beams, taken);
+    if (all > kDirect) {
+        const uint32_t deep = (a.K + lists - 1) / lists, need = (a.K + deep - 1) / deep;
+        for (uint32_t l = tid; l < lists; l += kJoinThreads) few[l] = beams.of(l, beams.key(l, deep - 1));
         __syncthreads();
-        w = Candidate{win_score[0], win_key[0]};
-        for (uint32_t i = 1; i < kJoinThreads / 64; ++i) w = better_of(w, Candidate{win_score[i], win_key[i]});
-        const int64_t to = (int64_t)n * a.K + k;
-        if (w.rest == 0) {   // nothing is left
-            if (tid == 0) {
-                a.best[to] = -INFINITY;
-                a.rows_out[to] = -1;
-                a.ids[to] = -1;
+        for (uint32_t l = tid; l < lists; l += kJoinThreads) {
+            const double mine = few[l].score;
+            uint32_t more = 0, same = 0;
+            for (uint32_t i = 0; i < lists; ++i) {
+                more += few[i].score > mine;
+                same += few[i].score == mine;
             }
-        } else if (list != ~0u && mine.rest == w.rest) {
-            taken[list] += 1;
-            a.best[to] = (float)w.score;
-            a.rows_out[to] = (int32_t)(n * a.beams + beam);
-            a.ids[to] = key_index(key);
+            if (more < need && more + same >= need) least = mine;
         }
         __syncthreads();
     }
+    const double from = least;
+    for (uint32_t i = tid; i < all; i += kJoinThreads) {
+        const uint32_t l = i / a.K;
+        const Candidate c = beams.of(l, beams.key(l, i - l * a.K));
+        if (c.rest && c.score >= from) {
+            const uint32_t at = atomicAdd(&count, 1u);
+            if (at < kRanked) few[at] = c;
+        }
+    }
+    __syncthreads();
+    const uint32_t found = count;
+    if (found > kRanked) return join_by_turns(beams, taken);
+    for (uint32_t i = tid; i < found; i += kJoinThreads) {
+        const Candidate c = few[i];
+        uint32_t rank = 0;
+        for (uint32_t j = 0; j < found; ++j) rank += few[j].before(c);
+        if (rank < a.K) beams.put(rank, c);
+    }
+    for (uint32_t k = found + tid; k < a.K; k += kJoinThreads) beams.put(k, Candidate{-INFINITY, 0});
 }
 
 constexpr int kMostStates = 8;   // of one launch
@@ -491,7 +688,9 @@ Plan plan_of(const Shape& s)
     const int64_t more = fill < fits ? fill : fits;
     if (more > parts) parts = more;
     Plan p;
+    // whole rounds of a workgroup's threads, if a part has more than one
     p.part_vecs = (vecs + parts - 1) / parts;
+    if (p.part_vecs > kThreads) p.part_vecs = (p.part_vecs + kThreads - 1) / kThreads * kThreads;
     p.parts = (vecs + p.part_vecs - 1) / p.part_vecs;
     return p;
 }
@@ -503,7 +702,7 @@ int64_t join_bytes(const Shape& s, const Plan& p) { return s.beams * 16 + s.beam
 
 bool plan_ok(const Shape& s, const Plan& p)
 {
-    return s.N * s.beams <= kMost / p.parts && join_bytes(s, p) <= 60 * 1024;
+    return s.N * s.beams <= kMost / p.parts && join_bytes(s, p) <= 48 * 1024;
 }
 
 constexpr int64_t kMostUnits = 1 << 22;   // a grid has fewer than 2^32 threads
@@ -562,7 +761,9 @@ int xpress_beam_select(const uint16_t* base, const uint16_t* bias, const float* 
     for (int64_t first = 0; first < N; first += kMostUnits) {
         a.first = (uint32_t)first;
         const dim3 grid((uint32_t)(N - first < kMostUnits ? N - first : kMostUnits)), block(kJoinThreads);
-        hipLaunchKernelGGL(join_kernel, grid, block, (size_t)join_bytes(s, p), stream, a);
+        uint32_t group = 1;   // lanes for a beam's parts
+        while (group < 64 && group < p.parts) group *= 2;
+        hipLaunchKernelGGL(join_kernel, grid, block, (size_t)join_bytes(s, p), stream, a, group);
     }
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? XPRESS_OK : hip_fail(e);
