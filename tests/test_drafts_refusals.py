@@ -264,7 +264,7 @@ def test_the_binding_refuses_other_shapes_and_types():
     native.xpress_beam_select(x, None, s, *out, 2, 3, 100, 4, 100)
     for args in ((x.float(), None, s, *out), (x, None, s[:5], *out), (x, None, s.double(), *out),
                  (x, None, s, out[0][:1], *out[1:]), (x, None, s, out[0], out[1].long(), out[2]),
-                 (x, None, s, *out[:2], out[2].int()), (x[:5], None, s, *out), (x, x.cpu(), s, *out)):
+                 (x, None, s, *out[:2], out[2].int()), (x[:5].clone(), None, s, *out), (x, x.cpu(), s, *out)):
         with pytest.raises(ValueError):
             native.xpress_beam_select(*args, 2, 3, 100, 4, 100, 100)
     src = i32(3)

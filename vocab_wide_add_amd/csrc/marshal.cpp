@@ -23,6 +23,8 @@ namespace {
 
 using at::Tensor;
 
+PyObject* none() { Py_RETURN_NONE; }
+
 // A tensor argument, null for None; *ok falls for anything else.
 const Tensor* tensor(PyObject* o, bool* ok)
 {
@@ -109,8 +111,9 @@ bool cache(const Tensor* k, const Tensor* v, const Tensor* table, const Tensor* 
     return true;
 }
 
-template <typename Args>
-PyObject* call(PyObject* entry, PyObject* stream, const Args& args)
+// The C entry point with these arguments and the stream.
+template <typename... Args>
+PyObject* call(PyObject* entry, PyObject* stream, Args... args)
 {
     void* fn = PyLong_AsVoidPtr(entry);
     if (!fn && PyErr_Occurred()) return nullptr;
@@ -118,9 +121,21 @@ PyObject* call(PyObject* entry, PyObject* stream, const Args& args)
     if (!st && PyErr_Occurred()) return nullptr;
     int status = 0;
     Py_BEGIN_ALLOW_THREADS
-    status = reinterpret_cast<int (*)(const Args*, hipStream_t)>(fn)(&args, static_cast<hipStream_t>(st));
+    status = reinterpret_cast<int (*)(Args..., hipStream_t)>(fn)(args..., static_cast<hipStream_t>(st));
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(status);
+}
+
+// Whole numbers from a on; false where one is none (or, with an error set, too large).
+template <size_t K>
+bool whole(PyObject* const* a, int64_t (&to)[K])
+{
+    for (size_t i = 0; i < K; ++i) {
+        if (!PyLong_Check(a[i])) return false;
+        to[i] = PyLong_AsLongLong(a[i]);
+        if (to[i] == -1 && PyErr_Occurred()) return false;
+    }
+    return true;
 }
 
 bool expect(Py_ssize_t have, Py_ssize_t want)
@@ -131,10 +146,11 @@ bool expect(Py_ssize_t have, Py_ssize_t want)
 }
 
 // entry, stream, q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin,
-// seq_of, k_scale, v_scale, interleaved
-PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
+// seq_of, k_scale, v_scale, interleaved, and of kv_append_at places
+template <bool AT>
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (!expect(n, 15)) return nullptr;
+    if (!expect(n, AT ? 16 : 15)) return nullptr;
     try {
         bool ok = true;
         const Tensor* t[12];
@@ -182,7 +198,12 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
         x.stride_k_h = k->stride(1);
         x.stride_v_t = v->stride(0);
         x.stride_v_h = v->stride(1);
-        return call(a[0], a[1], x);
+        if constexpr (AT) {
+            const Tensor* at = tensor(a[15], &ok);
+            if (!ok || !at || !plain(at, at::kInt, {T}, dev)) Py_RETURN_NONE;
+            return call<const xpress_kv_append_args*, const int32_t*>(a[0], a[1], &x, address<const int32_t>(at));
+        }
+        return call<const xpress_kv_append_args*>(a[0], a[1], &x);
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -190,10 +211,14 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
 }
 
 // entry, stream, q, k_cache, v_cache, page_table, lens, out, lse, k_scale, v_scale,
-// max_len, window, scale (None: 1 / sqrt(dim))
-PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
+// max_len, window, scale (None: 1 / sqrt(dim)), and of the sparse forms sinks, of the
+// tree's the tree
+enum class Form { kDense, kSinks, kTree };
+
+template <Form FORM>
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (!expect(n, 14)) return nullptr;
+    if (!expect(n, 14 + (int)FORM)) return nullptr;
     try {
         bool ok = true;
         const Tensor* t[9];
@@ -228,7 +253,22 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
         x.stride_o_n = out->stride(0);
         x.stride_o_i = out->stride(1);
         x.stride_o_h = out->stride(2);
-        return call(a[0], a[1], x);
+        using Args = const xpress_paged_attention_args*;
+        if constexpr (FORM == Form::kDense) {
+            return call<Args>(a[0], a[1], &x);
+        } else {
+            int64_t sinks[1];
+            if (!whole(a + 14, sinks)) return PyErr_Occurred() ? nullptr : none();
+            if constexpr (FORM == Form::kSinks) return call<Args, int64_t>(a[0], a[1], &x, sinks[0]);
+            if constexpr (FORM == Form::kTree) {
+                const Tensor* tree = tensor(a[15], &ok);
+                if (!ok || !tree || tree->dim() != 3 || !rows(*tree, at::kInt, {N, Q, (Q + 31) / 32}, dev)) {
+                    Py_RETURN_NONE;
+                }
+                return call<Args, const int32_t*, int64_t, int64_t, int64_t>(
+                    a[0], a[1], &x, address<const int32_t>(tree), tree->stride(0), tree->stride(1), sinks[0]);
+            }
+        }
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -257,8 +297,8 @@ bool numbers(const Tensor* t, at::ScalarType type, int64_t n, int64_t dev)
 // V, stride_base_r, stride_bias_r
 PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    using Entry = int (*)(const void*, const void*, void*, void*, const void*, const void*, const void*,
-                          const void*, const void*, int64_t, int64_t, int64_t, int64_t, int64_t, hipStream_t);
+    using In = const void*;
+    using Out = void*;
     if (!expect(n, 16)) return nullptr;
     try {
         bool ok = true;
@@ -289,32 +329,294 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n)
             const at::ScalarType type = i == 5 ? at::kInt : at::kFloat;   // top_k; the others
             if (t[i] ? !numbers(t[i], type, rows, dev) : i != 3) Py_RETURN_NONE;
         }
-        void* fn = PyLong_AsVoidPtr(a[0]);
-        if (!fn && PyErr_Occurred()) return nullptr;
-        void* st = PyLong_AsVoidPtr(a[1]);
-        if (!st && PyErr_Occurred()) return nullptr;
-        int status = 0;
-        Py_BEGIN_ALLOW_THREADS
-        status = reinterpret_cast<Entry>(fn)(
-            address<void>(t[0]), address<void>(t[1]), address<void>(t[2]), address<void>(t[3]), address<void>(t[4]),
-            address<void>(t[5]), address<void>(t[6]), address<void>(t[7]), address<void>(t[8]), N, B, V, d[3], d[4],
-            static_cast<hipStream_t>(st));
-        Py_END_ALLOW_THREADS
-        return PyLong_FromLong(status);
+        return call<In, In, Out, Out, In, In, In, In, In, int64_t, int64_t, int64_t, int64_t, int64_t>(
+            a[0], a[1], address<void>(t[0]), address<void>(t[1]), address<void>(t[2]), address<void>(t[3]),
+            address<void>(t[4]), address<void>(t[5]), address<void>(t[6]), address<void>(t[7]), address<void>(t[8]),
+            N, B, V, d[3], d[4]);
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
     }
 }
 
+// The counts of a pool's pages on the current device; *dev is the device.
+bool counts(const Tensor* t, int64_t* dev)
+{
+    if (!t || t->dim() != 1 || t->scalar_type() != at::kInt || !t->is_cuda() || !t->is_contiguous()) return false;
+    *dev = t->get_device();
+    return on_current(*dev);
+}
+
+// An int32 table [rows, width].
+bool table(const Tensor* t, int64_t dev)
+{
+    return t && t->dim() == 2 && rows(*t, at::kInt, {t->size(0), t->size(1)}, dev);
+}
+
+// n int32 numbers one after the other, in any shape.
+bool flat(const Tensor* t, int64_t n, int64_t dev)
+{
+    return t && t->scalar_type() == at::kInt && t->is_contiguous() && on(*t, dev) && t->numel() == n;
+}
+
+using Ints = const int32_t*;
+using IntsOut = int32_t*;
+
+// entry, stream, refs, table, lens, src, new_refs, new_table, copies, missing, page_size
+PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 11)) return nullptr;
+    try {
+        bool ok = true;
+        const Tensor* t[8];
+        for (int i = 0; i < 8; ++i) t[i] = tensor(a[2 + i], &ok);
+        int64_t dev = 0, page[1];
+        if (!whole(a + 10, page)) return PyErr_Occurred() ? nullptr : none();
+        if (!ok || !counts(t[0], &dev) || !table(t[1], dev) || !table(t[5], dev)) Py_RETURN_NONE;
+        const int64_t pages = t[0]->size(0), N = t[1]->size(0), W = t[1]->size(1), M = t[5]->size(0);
+        if (t[5]->size(1) != W || !t[2] || !plain(t[2], at::kInt, {N}, dev) || !flat(t[3], M, dev) || !t[4] ||
+            !plain(t[4], at::kInt, {pages}, dev) || !t[6] || !plain(t[6], at::kInt, {M, 3}, dev) ||
+            !plain(t[7], at::kInt, {1}, dev)) {
+            Py_RETURN_NONE;
+        }
+        return call<Ints, int64_t, Ints, int64_t, Ints, int64_t, Ints, int64_t, int64_t, int64_t, IntsOut, IntsOut,
+                    int64_t, IntsOut, IntsOut>(
+            a[0], a[1], address<const int32_t>(t[0]), pages, address<const int32_t>(t[1]), t[1]->stride(0),
+            address<const int32_t>(t[2]), N, address<const int32_t>(t[3]), M, W, page[0], address<int32_t>(t[4]),
+            address<int32_t>(t[5]), t[5]->stride(0), address<int32_t>(t[6]), address<int32_t>(t[7]));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// A cache without its table.
+bool pool(const Tensor* k, const Tensor* v, xpress_kv_cache* c)
+{
+    if (!k || !v || k->dim() != 4 || !k->is_cuda() || v->sizes() != k->sizes() || v->strides() != k->strides() ||
+        v->scalar_type() != k->scalar_type()) {
+        return false;
+    }
+    c->dtype = code_of(*k);
+    c->pages = k->size(0);
+    c->heads = k->size(1);
+    c->page_size = k->size(2);
+    c->dim = k->size(3);
+    if (c->dtype < 0 || (k->stride(3) != 1 && c->dim > 1) || !on(*v, k->get_device()) || !on_current(k->get_device())) {
+        return false;
+    }
+    c->k = k->data_ptr();
+    c->v = v->data_ptr();
+    c->stride_page = k->stride(0);
+    c->stride_head = k->stride(1);
+    c->stride_token = k->stride(2);
+    return true;
+}
+
+// entry, stream, k_cache, v_cache, copies
+PyObject* kv_copy(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 5)) return nullptr;
+    try {
+        bool ok = true;
+        const Tensor* t[3];
+        for (int i = 0; i < 3; ++i) t[i] = tensor(a[2 + i], &ok);
+        xpress_kv_cache c = {};
+        if (!ok || !t[2] || t[2]->dim() != 2 || !pool(t[0], t[1], &c) ||
+            !plain(t[2], at::kInt, {t[2]->size(0), 3}, t[0]->get_device())) {
+            Py_RETURN_NONE;
+        }
+        return call<const xpress_kv_cache*, Ints, int64_t>(a[0], a[1], &c, address<const int32_t>(t[2]),
+                                                           t[2]->size(0));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// entry, stream, refs, table, have, want, missing, page_size
+PyObject* kv_grow(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 8)) return nullptr;
+    try {
+        bool ok = true;
+        const Tensor* t[5];
+        for (int i = 0; i < 5; ++i) t[i] = tensor(a[2 + i], &ok);
+        int64_t dev = 0, page[1];
+        if (!whole(a + 7, page)) return PyErr_Occurred() ? nullptr : none();
+        if (!ok || !counts(t[0], &dev) || !table(t[1], dev)) Py_RETURN_NONE;
+        const int64_t N = t[1]->size(0);
+        if (!t[2] || !plain(t[2], at::kInt, {N}, dev) || !t[3] || !plain(t[3], at::kInt, {N}, dev) ||
+            !plain(t[4], at::kInt, {1}, dev)) {
+            Py_RETURN_NONE;
+        }
+        return call<IntsOut, int64_t, IntsOut, int64_t, int64_t, int64_t, int64_t, Ints, Ints, IntsOut>(
+            a[0], a[1], address<int32_t>(t[0]), t[0]->size(0), address<int32_t>(t[1]), t[1]->stride(0), N,
+            t[1]->size(1), page[0], address<const int32_t>(t[2]), address<const int32_t>(t[3]),
+            address<int32_t>(t[4]));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// entry, stream, refs, table, lens, page_size, window, sinks
+PyObject* kv_free(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 8)) return nullptr;
+    try {
+        bool ok = true;
+        const Tensor* t[3];
+        for (int i = 0; i < 3; ++i) t[i] = tensor(a[2 + i], &ok);
+        int64_t dev = 0, d[3];
+        if (!whole(a + 5, d)) return PyErr_Occurred() ? nullptr : none();
+        if (!ok || !counts(t[0], &dev) || !table(t[1], dev) || !t[2] ||
+            !plain(t[2], at::kInt, {t[1]->size(0)}, dev)) {
+            Py_RETURN_NONE;
+        }
+        return call<IntsOut, int64_t, IntsOut, int64_t, int64_t, int64_t, int64_t, Ints, int64_t, int64_t>(
+            a[0], a[1], address<int32_t>(t[0]), t[0]->size(0), address<int32_t>(t[1]), t[1]->stride(0),
+            t[1]->size(0), t[1]->size(1), d[0], address<const int32_t>(t[2]), d[1], d[2]);
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// entry, stream, k_cache, v_cache, page_table, start, path, count
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 8)) return nullptr;
+    try {
+        bool ok = true;
+        const Tensor* t[6];
+        for (int i = 0; i < 6; ++i) t[i] = tensor(a[2 + i], &ok);
+        xpress_kv_cache c = {};
+        if (!ok || !cache(t[0], t[1], t[2], nullptr, nullptr, &c)) Py_RETURN_NONE;
+        const int64_t dev = t[0]->get_device(), N = c.seqs;
+        if (!table(t[4], dev) || t[4]->size(0) != N || !t[3] || !plain(t[3], at::kInt, {N}, dev) || !t[5] ||
+            !plain(t[5], at::kInt, {N}, dev)) {
+            Py_RETURN_NONE;
+        }
+        return call<const xpress_kv_cache*, Ints, Ints, int64_t, Ints, int64_t>(
+            a[0], a[1], &c, address<const int32_t>(t[3]), address<const int32_t>(t[4]), t[4]->stride(0),
+            address<const int32_t>(t[5]), t[4]->size(1));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// entry, stream, base, bias, scores, best, rows, ids, N, beams, V, K, stride_base_r,
+// stride_bias_r
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 14)) return nullptr;
+    try {
+        bool ok = true;
+        const Tensor* t[6];
+        for (int i = 0; i < 6; ++i) t[i] = tensor(a[2 + i], &ok);
+        int64_t d[6];
+        if (!whole(a + 8, d)) return PyErr_Occurred() ? nullptr : none();
+        const int64_t most = 0x7FFFFFFFll, N = d[0], beams = d[1], V = d[2], K = d[3];
+        if (!ok || !t[0] || !t[2] || !t[3] || !t[4] || !t[5] || N < 1 || beams < 1 || N > most / beams || V < 1 ||
+            V > most || K < 1 || K > most || d[4] < V || d[4] > (most << 16) || d[5] < 0 || d[5] > (most << 16) ||
+            N > most / K || !t[0]->is_cuda()) {
+            Py_RETURN_NONE;
+        }
+        const int64_t R = N * beams, dev = t[0]->get_device();
+        const unsigned __int128 base = ((unsigned __int128)(R - 1) * d[4] + V) * 2u,
+                                bias = ((unsigned __int128)(R - 1) * d[5] + V) * 2u,
+                                far = (unsigned __int128)1 << 62;
+        if (base > far || bias > far || !logits(t[0], (int64_t)base, dev) || !logits(t[1], (int64_t)bias, dev) ||
+            !numbers(t[2], at::kFloat, R, dev) || !numbers(t[3], at::kFloat, N * K, dev) ||
+            !numbers(t[4], at::kInt, N * K, dev) || !numbers(t[5], at::kLong, N * K, dev) || !on_current(dev)) {
+            Py_RETURN_NONE;
+        }
+        return call<const void*, const void*, const float*, float*, int32_t*, void*, int64_t, int64_t, int64_t,
+                    int64_t, int64_t, int64_t>(
+            a[0], a[1], address<const void>(t[0]), address<const void>(t[1]), address<const float>(t[2]),
+            address<float>(t[3]), address<int32_t>(t[4]), address<void>(t[5]), N, beams, V, K, d[4], d[5]);
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// Rows behind the first dimension, each one after the other in memory.
+bool whole_rows(const Tensor& t)
+{
+    int64_t step = 1;
+    for (int64_t i = t.dim() - 1; i > 0; --i) {
+        if (t.size(i) != 1 && t.stride(i) != step) return false;
+        step *= t.size(i);
+    }
+    return true;
+}
+
+// entry, stream, states, src
+PyObject* beam_reorder(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!expect(n, 4)) return nullptr;
+    constexpr Py_ssize_t kMost = 64;
+    if ((!PyList_CheckExact(a[2]) && !PyTuple_CheckExact(a[2])) || Py_SIZE(a[2]) > kMost) Py_RETURN_NONE;
+    try {
+        bool ok = true;
+        const Tensor* src = tensor(a[3], &ok);
+        if (!ok || !src || !src->is_cuda()) Py_RETURN_NONE;
+        const int64_t dev = src->get_device(), M = src->numel();
+        if (!flat(src, M, dev) || !on_current(dev)) Py_RETURN_NONE;
+        xpress_beam_state x[kMost];
+        const Py_ssize_t count = Py_SIZE(a[2]);
+        int64_t N = 0;
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            PyObject* pair = PySequence_Fast_GET_ITEM(a[2], i);
+            if (!PyTuple_CheckExact(pair) || Py_SIZE(pair) != 2) Py_RETURN_NONE;
+            const Tensor *from = tensor(PyTuple_GET_ITEM(pair, 0), &ok), *to = tensor(PyTuple_GET_ITEM(pair, 1), &ok);
+            if (!ok || !from || !to || from->dim() < 1 || from->dim() != to->dim() ||
+                from->sizes().slice(1) != to->sizes().slice(1) || from->scalar_type() != to->scalar_type() ||
+                to->size(0) != M || (i > 0 && from->size(0) != N) || !on(*from, dev) || !on(*to, dev) ||
+                !whole_rows(*from) || !whole_rows(*to)) {
+                Py_RETURN_NONE;
+            }
+            N = from->size(0);
+            const int64_t e = from->element_size();
+            int64_t row = e;
+            for (int64_t d = 1; d < from->dim(); ++d) row *= from->size(d);
+            x[i] = xpress_beam_state{from->data_ptr(), to->data_ptr(), from->stride(0) * e, to->stride(0) * e, row};
+        }
+        return call<const xpress_beam_state*, int64_t, Ints, int64_t, int64_t>(
+            a[0], a[1], x, (int64_t)count, address<const int32_t>(src), N, M);
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
+
+PyMethodDef method(const char* name, PyCFunction f)
+{
+    return {name, f, METH_FASTCALL,
+            "the C entry point of this name from tensors: its status, or None where the arguments are not regular"};
+}
+
+PyCFunction of(Fast f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
+
 PyMethodDef methods[] = {
-    {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL,
-     "xpress_kv_append from tensors: the status, or None where the arguments are not regular"},
-    {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)),
-     METH_FASTCALL,
-     "xpress_paged_attention from tensors: the status, or None where the arguments are not regular"},
-    {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL,
-     "xpress_sample_to_blk from tensors: the status, or None where the arguments are not regular"},
+    method("kv_append", of(append<false>)),
+    method("kv_append_at", of(append<true>)),
+    method("paged_attention", of(attention<Form::kDense>)),
+    method("sink_attention", of(attention<Form::kSinks>)),
+    method("tree_attention", of(attention<Form::kTree>)),
+    method("sample", of(sample)),
+    method("kv_fork", of(kv_fork)),
+    method("kv_copy", of(kv_copy)),
+    method("kv_grow", of(kv_grow)),
+    method("kv_free", of(kv_free)),
+    method("kv_compact", of(kv_compact)),
+    method("beam_select", of(beam_select)),
+    method("beam_reorder", of(beam_reorder)),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

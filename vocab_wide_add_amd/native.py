@@ -140,6 +140,9 @@ def load():
         lib.append_at, lib.attention_at, lib.sample_at = [
             ctypes.cast(f, vp).value for f in (lib.xpress_kv_append, lib.xpress_paged_attention,
                                                lib.xpress_sample_to_blk)]
+        lib.at = {x: ctypes.cast(getattr(lib, "xpress_" + x), vp).value for x in (
+            "kv_append_at", "sink_attention", "tree_attention", "kv_fork", "kv_copy", "kv_grow", "kv_free",
+            "kv_compact", "beam_select", "beam_reorder")}
         lib.xpress_last_hip_error.argtypes = []
         lib.xpress_last_hip_error.restype = i32
         lib.xpress_error_string.argtypes = [i32]
@@ -592,7 +595,12 @@ def xpress_kv_append_at(q, k, v, q_out, k_cache, v_cache, page_table, places, po
     """xpress_kv_append with places apart from positions: keys and values of token t go
     to place places[t] (int32 [T]) of its sequence, rotated to positions[t]."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.kv_append_at(lib.at["kv_append_at"], _stream_of_tensors(stream), q, k, v, q_out, k_cache,
+                                   v_cache, page_table, positions, cos_sin, seq_of, k_scale, v_scale, interleaved, places)
+    if status is not None:
+        return _check(status, "xpress_kv_append_at")
     args = _append_args(q, k, v, q_out, k_cache, v_cache, page_table, positions, cos_sin, seq_of, k_scale,
                         v_scale, interleaved)
     at = _plain(places, "places", _torch.int32, (k.shape[0],), k_cache.get_device())
@@ -651,7 +659,12 @@ def xpress_sink_attention(q, k_cache, v_cache, page_table, lens, out, max_len: i
     """xpress_paged_attention with a window that leaves the first ``sinks`` tokens
     visible: a query at position pos sees j <= pos with j > pos - window or j < sinks."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.sink_attention(lib.at["sink_attention"], _stream_of_tensors(stream), q, k_cache, v_cache,
+                                     page_table, lens, out, lse, k_scale, v_scale, max_len, window, scale, sinks)
+    if status is not None:
+        return _check(status, "xpress_sink_attention")
     args = _attention_args(q, k_cache, v_cache, page_table, lens, out, max_len, lse, scale, window, k_scale,
                            v_scale)
     _check(lib.xpress_sink_attention(args, int(sinks), _stream(stream)), "xpress_sink_attention")
@@ -665,7 +678,12 @@ def xpress_tree_attention(q, k_cache, v_cache, page_table, lens, tree, out, max_
     ceil(Q / 32)], any strides, unit along the words; ``expand`` one tree to share it),
     beside the tokens before the tree, windowed with sinks.  See the header."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.tree_attention(lib.at["tree_attention"], _stream_of_tensors(stream), q, k_cache, v_cache,
+                                     page_table, lens, out, lse, k_scale, v_scale, max_len, window, scale, sinks, tree)
+    if status is not None:
+        return _check(status, "xpress_tree_attention")
     args = _attention_args(q, k_cache, v_cache, page_table, lens, out, max_len, lse, scale, window, k_scale,
                            v_scale)
     N, Q = q.shape[0], q.shape[1]
@@ -712,7 +730,12 @@ def xpress_kv_fork(refs, table, lens, src, new_refs, new_table, copies, page_siz
     of M elements, as xpress_beam_select's rows), copies [M, 3], missing [1] or None, all
     int32.  See the header."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.kv_fork(lib.at["kv_fork"], _stream_of_tensors(stream), refs, table, lens, src, new_refs,
+                              new_table, copies, missing, page_size)
+    if status is not None:
+        return _check(status, "xpress_kv_fork")
     i32 = _torch.int32
     rp, pages, dev = _pages_of(refs)
     tp, N, width, st = _table(table, "table", dev)
@@ -739,7 +762,11 @@ def xpress_kv_copy(k_cache, v_cache, copies, stream=None) -> None:
     places of page `from` go to page `to`, keys and values of all heads; lines with a
     page outside the pool do nothing."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.kv_copy(lib.at["kv_copy"], _stream_of_tensors(stream), k_cache, v_cache, copies)
+    if status is not None:
+        return _check(status, "xpress_kv_copy")
     cache = _pool_fields(k_cache, v_cache)
     if copies.dim() != 2:
         raise ValueError("copies: int32 [count, 3] expected, got shape %s" % (tuple(copies.shape),))
@@ -752,7 +779,12 @@ def xpress_kv_grow(refs, table, have, want, page_size: int, missing=None, stream
     """Free pages for the tokens have[n] <= p < want[n] of each row of table, in place;
     have, want int32 [N], missing int32 [1] or None: the pages that there were not."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.kv_grow(lib.at["kv_grow"], _stream_of_tensors(stream), refs, table, have, want, missing,
+                              page_size)
+    if status is not None:
+        return _check(status, "xpress_kv_grow")
     i32 = _torch.int32
     rp, pages, dev = _pages_of(refs)
     tp, N, width, st = _table(table, "table", dev)
@@ -765,7 +797,12 @@ def xpress_kv_free(refs, table, lens, page_size: int, window: int = 0, sinks: in
     """Gives back, in place, the pages of which no query at or after position lens[n]
     sees a token; lens int32 [N], 0 for a finished sequence."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.kv_free(lib.at["kv_free"], _stream_of_tensors(stream), refs, table, lens, page_size,
+                              window, sinks)
+    if status is not None:
+        return _check(status, "xpress_kv_free")
     rp, pages, dev = _pages_of(refs)
     tp, N, width, st = _table(table, "table", dev)
     _check(lib.xpress_kv_free(rp, pages, tp, st, N, width, int(page_size),
@@ -778,7 +815,12 @@ def xpress_kv_compact(k_cache, v_cache, page_table, start, path, count, stream=N
     goes to place start[n] + j, for j < count[n].  start, count int32 [N], path int32
     [N, longest] of ascending nodes."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.kv_compact(lib.at["kv_compact"], _stream_of_tensors(stream), k_cache, v_cache,
+                                 page_table, start, path, count)
+    if status is not None:
+        return _check(status, "xpress_kv_compact")
     i32, dev = _torch.int32, k_cache.get_device()
     cache = struct.pack(_KV_CACHE, *_kv_cache(k_cache, v_cache, page_table, None, None, dev))
     N = page_table.shape[0]
@@ -889,7 +931,13 @@ def xpress_beam_select(base, bias, scores, best, rows, ids, N: int, beams: int, 
     int64 [N, K], in descending order.  bias may be None; base and bias as for
     xpress_sample_to_blk; scores fp32 [N * beams]."""
     lib = _lib or load()
-    t = _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.beam_select(lib.at["beam_select"], _stream_of_tensors(stream), base, bias, scores, best,
+                                  rows, ids, N, beams, V, K, stride_base_r, stride_bias_r)
+    if status is not None:
+        return _check(status, "xpress_beam_select")
+    t = _torch
     r, n = int(N) * int(beams), int(N) * int(K)
     if n > 0 and r > 0:
         dev = base.device if hasattr(base, "data_ptr") else None
@@ -921,7 +969,11 @@ def xpress_beam_reorder(states, src, stream=None) -> None:
     row of old.  old [N, ...] and new [M, ...] of one type and shape behind the first
     dimension, contiguous there; src int32 of M elements, as xpress_beam_select's rows."""
     lib = _lib or load()
-    _use_torch()
+    if _marshal is None:
+        _use_torch()
+    status = _marshal.beam_reorder(lib.at["beam_reorder"], _stream_of_tensors(stream), states, src)
+    if status is not None:
+        return _check(status, "xpress_beam_reorder")
     dev = src.get_device()
     if dev < 0:
         _elsewhere(src, "src", dev)
