@@ -110,6 +110,12 @@ CASES = [
     ([500, 64], 4, 4, 1, 8, 8, "head", 1, 2),
     ([77, 400], 33, 3, 1, 40, 16, "head", 20, 500),               # more sinks than what the window leaves
     ([2600], 3, 4, 2, 64, 16, "head", 1000, 130),
+    # more than 64 rows a key-value head
+    ([100, 64, 65, 1, 0], 9, 16, 2, 128, 16, "token", 0, 0),      # 72 rows
+    ([1500, 40], 20, 4, 1, 256, 16, "head", 0, 0),
+    ([333, 20], 33, 9, 3, 192, 1, "head", 50, 7),
+    ([200] * 9 + [35, 0, 700], 17, 8, 2, 64, 7, "token", 60, 20), # more parts than XCDs
+    ([65, 63], 129, 2, 1, 96, 32, "head", 0, 0),                  # more nodes than tokens, five words
 ]
 
 
@@ -232,6 +238,71 @@ def test_long_contexts_in_parts():
     wide = torch.full((2, 4000), -1, dtype=torch.int32)
     wide[:, :table.shape[1]] = table
     verify(q, kc, vc, wide, lens, 200000, sees=sees)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache,page", [("bf16", "bf16", 64), ("fp16", "e4m3", 5), ("bf16", "bf16", 1)])
+def test_long_contexts_under_many_rows(dtype, cache, page):
+    """More stages than the ring of places has, in one part and in several."""
+    say("many rows %s %s %d" % (dtype, cache, page))
+    (q, kc, vc, table, lens), scales, sees, _ = made(88, [4500, 70, 1300, 600], 18, 8, 2, 64, page, dtype, cache)
+    verify(q, kc, vc, table, lens, 4500, sees=sees, **scales)
+    kc, vc, table = without(kc, vc, table, lens, 18, 2000, 70, 0)
+    verify(q, kc, vc, table, lens, 4500, 2000, 70, sees=sees, **scales)
+    verify(q[:1, -1:].expand(1, 18, 8, 64).contiguous(), kc, vc, table[:1], lens[:1], 4500, 900, 33, **scales)
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_are_ranked():
+    say("300 sequences")
+    rng = np.random.default_rng(4)
+    (q, kc, vc, table, lens), _, sees, _ = made(89, rng.integers(0, 40, 300).tolist(), 33, 2, 1, 32, 16)
+    verify(q, kc, vc, table, lens, 40, sees=sees)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+@pytest.mark.parametrize("Q", [3, 40])
+def test_other_scales(scale, Q):
+    (q, kc, vc, table, lens), _, sees, _ = made(90, [300, 50], Q, 4, 2, 64, 16)
+    verify(q, kc, vc, table, lens, 300, sees=sees, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_not_finite_values_under_many_rows(cache):
+    """As above with 40 nodes: 80 rows a head, four words of them in two waves and more."""
+    (q, kc, vc, table, lens), scales, sees, _ = made(91, [700, 90], 40, 4, 2, 64, 16, "bf16", cache)
+    kc, vc = kc.clone(), vc.clone()
+    sees = sees.copy()
+    sees[:, :, 7] = False
+    sees[:, 7, 7] = sees[:, 30, 7] = True
+    for n, length in enumerate((700, 90)):
+        at = length - 40 + 7
+        kc[table[n, at // 16], :, at % 16] = 1.0
+        vc[table[n, at // 16], :, at % 16] = float("nan")
+    out, lse = call(q, kc, vc, table, lens, 700, 0, 0, ref.words_of(sees), **scales)
+    hit = [7, 30]
+    rest = [i for i in range(40) if i not in hit]
+    assert np.isnan(out[:, hit]).all() and np.isfinite(out[:, rest]).all() and np.isfinite(lse).all()
+    clean = torch.nan_to_num(vc.float(), nan=0.0).to(vc.dtype)
+    kc2 = torch.nan_to_num(kc.float(), nan=0.0).to(kc.dtype)
+    want, _ = call(q, kc2, clean, table, lens, 700, 0, 0, ref.words_of(sees), **scales)
+    # the careful form adds its products in another order: two roundings apart at most
+    assert np.allclose(out[:, rest], want[:, rest], rtol=2.0 ** -7, atol=2.0 ** -12)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Q", [6, 40])
+def test_missing_pages_take_no_part(Q):
+    (q, kc, vc, table, lens), _, sees, _ = made(92, [400, 70 + Q, 48 + Q], Q, 4, 2, 64, 16)
+    table = table.clone()
+    table[0, 3], table[0, 7], table[0, 12] = -1, kc.shape[0], 2 ** 31 - 1
+    table[1, :] = -5
+    table[2, 2] = -2 ** 31
+    out, lse = verify(q, kc, vc, table, lens, 400, sees=sees)
+    assert (out[1] == 0).all() and np.isneginf(lse[1]).all()
+    verify(q, kc, vc, table, lens, 400, 37, 20)
 
 
 @pytest.mark.gpu

@@ -247,13 +247,13 @@ struct Stage : Lines<E4M3, DP> {
         const char *k[kCopies], *v[kCopies];
     };
     static __device__ __forceinline__ From find(const AttnArgs& a, const int64_t* place, uint32_t t,
-                                                const char* kbase, const char* vbase)
+                                                const char* kbase, const char* vbase, uint32_t thread)
     {
         const uint32_t used = a.D * (E4M3 ? 1 : 2);
         From f;
 #pragma unroll
         for (uint32_t x = 0; x < kCopies; ++x) {
-            const uint32_t at = x * kThreads + threadIdx.x, row = at / L::kPieces, piece = at % L::kPieces;
+            const uint32_t at = x * kThreads + thread, row = at / L::kPieces, piece = at % L::kPieces;
             const uint32_t kd = (piece ^ L::turn(row)) * 16, vd = piece * 16;
             f.k[x] = kbase + place[t + row] + (kd < used ? kd : 0);
             f.v[x] = vbase + place[t + L::slot(row)] + (vd < used ? vd : 0);
@@ -890,8 +890,8 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
             // addresses are looked up before the wait, so that the copies follow it at once
             typename S::From from = {};
             if (padded > 0) {
-                S::template copy<ONCE>(S::find(a, place, 0, t.kbase, t.vbase), to);
-                if (S::kKeys < padded) from = S::find(a, place, S::kKeys, t.kbase, t.vbase);
+                S::template copy<ONCE>(S::find(a, place, 0, t.kbase, t.vbase, threadIdx.x), to);
+                if (S::kKeys < padded) from = S::find(a, place, S::kKeys, t.kbase, t.vbase, threadIdx.x);
             }
             for (uint32_t at = 0; at < padded; at += S::kKeys) {
                 // this stage's copies have landed, and every wave is through with
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
                 const char* here = pool + half * (2 * S::kBytes);
                 if (at + S::kKeys < padded) {
                     S::template copy<ONCE>(from, to + (1 - half) * (2 * S::kBytes));
-                    if (at + 2 * S::kKeys < padded) from = S::find(a, place, at + 2 * S::kKeys, t.kbase, t.vbase);
+                    if (at + 2 * S::kKeys < padded) from = S::find(a, place, at + 2 * S::kKeys, t.kbase, t.vbase, threadIdx.x);
                 }
                 if (!some) continue;
 #pragma unroll
@@ -1068,13 +1068,13 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
 // Which of the kernels.
 struct Way {
     int rw;
-    bool e4m3, once;
+    bool e4m3, once, wide;
 };
 
 struct Shape {
     int64_t N, Q, Hq, heads, dim, max_len, window;
     int64_t sinks = 0;
-    bool tree = false;
+    bool tree = false, sparse = false;
 };
 
 bool shape_ok(const Shape& s)
@@ -1088,8 +1088,9 @@ bool shape_ok(const Shape& s)
 }
 
 struct Plan {
-    int rw;                        // waves of 16 rows in a workgroup
+    int rw;                        // waves of 16 rows (wide: 32) in a workgroup
     int64_t rows, groups, chunk, splits, units;
+    bool wide = false;             // attention_wide.h
 };
 
 // Rows: as many waves of 16 as hold them, up to the workgroup's 4, so that a
@@ -1118,7 +1119,8 @@ Plan plan_of(const Shape& s)
 {
     Plan p;
     p.rows = s.Q * (s.Hq / s.heads);
-    const int64_t tiles = (p.rows + 15) / 16;
+    p.wide = s.sparse && p.rows > 64;
+    const int64_t tiles = p.wide ? (p.rows + 31) / 32 : (p.rows + 15) / 16;
     p.rw = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;
     p.groups = (tiles + p.rw - 1) / p.rw;
     int64_t span = s.max_len;
@@ -1135,7 +1137,7 @@ Plan plan_of(const Shape& s)
         return up < (1 << 30) ? up : (int64_t)1 << 30;
     };
     p.chunk = rounds((span + want - 1) / want);
-    if (p.chunk > table && !(s.N == 1 && wide >= 4 * slots)) p.chunk = table;
+    if (!p.wide && p.chunk > table && !(s.N == 1 && wide >= 4 * slots)) p.chunk = table;
     p.splits = (span + p.chunk - 1) / p.chunk;
     if (p.splits > 1 && p.splits * words_a_part(s) > kMostWords) {
         const int64_t fit = kMostWords / words_a_part(s);
@@ -1184,9 +1186,16 @@ void launch_waves(const AttnArgs& a, bool once, hipStream_t stream)
     }
 }
 
+// attention_wide.h's.
+template <bool FP16, bool E4M3, int DP>
+void launch_wide(AttnArgs a, const Way& way, hipStream_t stream);
+
 template <bool FP16, bool E4M3, int DP, bool SPARSE>
 void launch_rows(const AttnArgs& a, const Way& way, hipStream_t stream)
 {
+    if constexpr (SPARSE) {
+        if (way.wide) return launch_wide<FP16, E4M3, DP>(a, way, stream);
+    }
     if (way.rw == 1) launch_waves<FP16, E4M3, DP, 1, SPARSE>(a, way.once, stream);
     else if (way.rw == 2) launch_waves<FP16, E4M3, DP, 2, SPARSE>(a, way.once, stream);
     else launch_waves<FP16, E4M3, DP, 4, SPARSE>(a, way.once, stream);
@@ -1233,7 +1242,8 @@ int call_attention(const xpress_paged_attention_args* args, const Sparse& more, 
     if (!args) return XPRESS_EINVAL;
     const xpress_paged_attention_args& x = *args;
     const xpress_kv_cache& c = x.cache;
-    const Shape s = {c.seqs, x.Q, x.Hq, c.heads, c.dim, x.max_len, x.window, more.sinks, more.tree != nullptr};
+    const Shape s = {c.seqs, x.Q, x.Hq, c.heads, c.dim, x.max_len, x.window, more.sinks, more.tree != nullptr,
+                     SPARSE};
     if (!shape_ok(s)) return XPRESS_EINVAL;
     if (x.dtype != XPRESS_BF16 && x.dtype != XPRESS_FP16) return XPRESS_EINVAL;
     if (s.N == 0 || s.Q == 0) return XPRESS_OK;
@@ -1344,7 +1354,7 @@ int call_attention(const xpress_paged_attention_args* args, const Sparse& more, 
     // (token-major rows of 160 bytes: 62 us through the caches, 80 past them;
     // head-major rows of 256 bytes: 69 and 63).
     const Way way = {p.rw, c.dtype == XPRESS_E4M3,
-                     p.groups == 1 && (c.stride_token == c.dim || c.dim * e % 128 == 0)};
+                     p.groups == 1 && (c.stride_token == c.dim || c.dim * e % 128 == 0), p.wide};
     const hipError_t err = x.dtype == XPRESS_FP16 ? launch_attention<true, SPARSE>(a, way, stream)
                                                   : launch_attention<false, SPARSE>(a, way, stream);
     return err == hipSuccess ? XPRESS_OK : hip_fail(err);

@@ -2,7 +2,7 @@
 // all that came before them: the nodes of a tree, and a window with sinks.  The
 // sparse form of attention.h.
 
-#include "attention.h"
+#include "attention_wide.h"
 
 extern "C" {
 
@@ -22,7 +22,7 @@ int xpress_sparse_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t he
                                     int64_t max_len, int64_t window, int64_t sinks, int tree,
                                     hipStream_t stream)
 {
-    const Shape s = {N, Q, Hq, heads, dim, max_len, window, sinks, tree != 0};
+    const Shape s = {N, Q, Hq, heads, dim, max_len, window, sinks, tree != 0, true};
     if (!shape_ok(s)) return XPRESS_EINVAL;
     if (N == 0 || Q == 0) return XPRESS_OK;
     const Plan p = plan_of(s);
