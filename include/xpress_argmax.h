@@ -551,7 +551,7 @@ int xpress_sparse_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t he
  * name the page) + (entries of new_table).  refs, table and the pages themselves are
  * left as they are, and pages are taken from those free in refs: a fork may be made
  * again, as by a graph that is replayed.  Sources that no row continues give
- * their pages back.  Two launches.  N, M < 2^24.
+ * their pages back.  Two launches.  N and M are 65536 at most.
  */
 int xpress_kv_fork(const int32_t* refs, int64_t pages, const int32_t* table, int64_t stride_table,
                    const int32_t* lens, int64_t N, const int32_t* src, int64_t M, int64_t width,

@@ -104,7 +104,7 @@ def changed(base, at):
 @no_gpu_only
 @pytest.mark.parametrize("at", [
     {0: 0}, {0: MiB + 2}, {1: 0}, {1: 2 ** 31}, {2: 0}, {2: 2 * MiB + 1}, {3: 7}, {3: -1}, {4: 0}, {5: -1},
-    {5: 2 ** 24}, {6: 0}, {7: -1}, {7: 2 ** 24}, {8: 0}, {8: 2 ** 28, 3: 2 ** 28, 12: 2 ** 28}, {9: 0}, {9: -16},
+    {5: 2 ** 24}, {5: 65537}, {6: 0}, {7: -1}, {7: 2 ** 24}, {7: 65537}, {8: 0}, {8: 2 ** 28, 3: 2 ** 28, 12: 2 ** 28}, {9: 0}, {9: -16},
     {10: 0}, {11: 0}, {12: 7}, {13: 0}, {13: 7 * MiB + 2}, {14: 8 * MiB + 1},
     {10: MiB}, {10: MiB + 396}, {11: 2 * MiB}, {11: 2 * MiB + 100}, {13: 6 * MiB + 100}, {14: 6 * MiB}, {14: MiB},
     {13: 4 * MiB}, {11: 3 * MiB}, {10: 4 * MiB},

@@ -484,9 +484,9 @@ int xpress_kv_fork(const int32_t* refs, int64_t pages, const int32_t* table, int
                    int64_t page_size, int32_t* new_refs, int32_t* new_table, int64_t stride_new,
                    int32_t* copies, int32_t* missing, hipStream_t stream)
 {
-    // a workgroup a row: a grid has fewer than 2^32 threads
+    // every row looks through all of src
     const int64_t rows = N > M ? N : M;
-    if (N < 0 || M < 0 || rows >= ((int64_t)1 << 24) || pages < 1 || pages > kMost) return XPRESS_EINVAL;
+    if (N < 0 || M < 0 || rows > 65536 || pages < 1 || pages > kMost) return XPRESS_EINVAL;
     if (!numbers_ok(refs) || !numbers_ok(new_refs) || !is_aligned(missing, 4)) return XPRESS_EINVAL;
     if (N > 0 && (!table_ok(table, N, width, stride_table, page_size) || !numbers_ok(lens))) return XPRESS_EINVAL;
     if (M > 0 && (!table_ok(new_table, M, width, stride_new, page_size) || !numbers_ok(src) ||
