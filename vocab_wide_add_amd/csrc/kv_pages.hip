@@ -10,8 +10,11 @@
 // workgroup for the pages' ranks.  (The counts are few: 7399 pages of the 32 sequences
 // of 8 beams are two steps.)  All other work is spread over the chip.
 //
-// Bound by latency: a handful of dependent loads a launch; copies and moves by their
-// bytes.
+// Bound by latency: a handful of dependent loads a launch.  Measured: a fork of 256 rows
+// (pages of 16 tokens, 83 slots a row, 7399 pages) 5.0 us for the plan, 3.8 for the rows and
+// 5.6 for the copies, 9 MB; of 4 rows 4.1, 3.0 and 2.9.  256 sequences of up to 8192 tokens
+// give back what left their window in 2.8 us and take 64 tokens' pages in 7.0.  64 paths of up
+// to 12 nodes move in 5.7 us (with 8 moves at once 6.4).
 
 #include <hip/hip_runtime.h>
 
@@ -29,6 +32,7 @@ using namespace xpress;
 constexpr uint32_t kThreads = 1024;     // of a workgroup that hands pages out
 constexpr uint32_t kWaves = kThreads / 64;
 constexpr uint32_t kStep = kThreads * 4;   // counts looked at in one step
+constexpr uint32_t kMostWanted = kThreads * 2;   // pages asked for at once
 constexpr uint32_t kWindow = 8192;      // sources whose first child is looked for at once
 constexpr uint32_t kRowThreads = 256;
 
@@ -56,18 +60,19 @@ __device__ __forceinline__ uint32_t ranks(uint32_t v, uint32_t* sums, uint32_t* 
     return before + x - v;
 }
 
-// The pool's free pages in ascending order, found as they are asked for.
+// The pool's free pages in ascending order, found as they are asked for.  (Counts loaded
+// a step ahead: 7.9 us for 256 sequences' pages where this takes 7.0; each barrier waits
+// for them.)
 struct FreePages {
     struct Shared {
-        int32_t list[kStep + kThreads];
+        int32_t list[kStep + kMostWanted];
         uint32_t sums[kWaves];
     };
     Shared& s;
     const int32_t* refs;
     uint32_t pages, next, have;   // counts looked at; pages in the list
 
-    // At least `want` (of at most a workgroup's threads) in the list, if there are as
-    // many.
+    // At least `want`, kMostWanted or fewer, in the list, if there are as many.
     __device__ void fill(uint32_t want)
     {
         while (have < want && next < pages) {
@@ -90,17 +95,18 @@ struct FreePages {
     // The first n leave the list.
     __device__ void drop(uint32_t n)
     {
+        constexpr uint32_t kEach = (kStep + kMostWanted) / kThreads;
         __syncthreads();
         const uint32_t left = have - n;
-        int32_t keep[(kStep + kThreads) / kThreads];
+        int32_t keep[kEach];
 #pragma unroll
-        for (uint32_t i = 0; i < (kStep + kThreads) / kThreads; ++i) {
+        for (uint32_t i = 0; i < kEach; ++i) {
             const uint32_t at = i * kThreads + threadIdx.x;
             keep[i] = at < left ? s.list[n + at] : 0;
         }
         __syncthreads();
 #pragma unroll
-        for (uint32_t i = 0; i < (kStep + kThreads) / kThreads; ++i) {
+        for (uint32_t i = 0; i < kEach; ++i) {
             const uint32_t at = i * kThreads + threadIdx.x;
             if (at < left) s.list[at] = keep[i];
         }
@@ -307,30 +313,41 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(GrowArgs a)
         begin[threadIdx.x] = at;
         slot0[threadIdx.x] = lo;
         __syncthreads();
-        for (uint32_t i0 = 0; i0 < all; i0 += kThreads) {
-            const uint32_t i = i0 + threadIdx.x;
-            bool lacks = false;
-            int32_t* entry = nullptr;
-            if (i < all) {
-                uint32_t x = 0;   // the last sequence that begins at or before slot i
+        for (uint32_t i0 = 0; i0 < all; i0 += 2 * kThreads) {
+            // two slots a thread, one after the other
+            bool lacks[2];
+            int32_t* entry[2];
 #pragma unroll
-                for (uint32_t d = kThreads / 2; d > 0; d /= 2) {
-                    if (begin[x + d] <= i) x += d;
+            for (uint32_t e = 0; e < 2; ++e) {
+                const uint32_t i = i0 + 2 * threadIdx.x + e;
+                lacks[e] = false;
+                entry[e] = nullptr;
+                if (i < all) {
+                    uint32_t x = 0;   // the last sequence that begins at or before slot i
+#pragma unroll
+                    for (uint32_t d = kThreads / 2; d > 0; d /= 2) {
+                        if (begin[x + d] <= i) x += d;
+                    }
+                    entry[e] = a.table + (int64_t)(n0 + x) * a.stride_table + slot0[x] + (i - begin[x]);
+                    lacks[e] = (uint32_t)*entry[e] >= a.pages;
                 }
-                entry = a.table + (int64_t)(n0 + x) * a.stride_table + slot0[x] + (i - begin[x]);
-                lacks = (uint32_t)*entry >= a.pages;
             }
             uint32_t total;
-            const uint32_t rank = ranks(lacks, s.sums, &total);
+            uint32_t rank = ranks((uint32_t)lacks[0] + lacks[1], s.sums, &total);
             if (total == 0) continue;
             pool.fill(total);
-            if (lacks && rank < pool.have) {
-                const int32_t p = s.list[rank];
-                *entry = p;
-                a.refs[p] = 1;
+#pragma unroll
+            for (uint32_t e = 0; e < 2; ++e) {
+                if (lacks[e] && rank < pool.have) {
+                    const int32_t p = s.list[rank];
+                    *entry[e] = p;
+                    a.refs[p] = 1;
+                }
+                rank += lacks[e];
             }
             const uint32_t used = min(total, pool.have);
             short_of += total - used;
+            if (i0 + 2 * kThreads >= all && a.N - n0 <= kThreads) break;   // the last
             pool.drop(used);
         }
         __syncthreads();
@@ -371,7 +388,7 @@ struct CompactArgs {
 };
 
 constexpr uint32_t kPath = 256;    // kept nodes whose places LDS holds at once
-constexpr uint32_t kAtOnce = 8;    // rows a thread reads before it writes them
+constexpr uint32_t kAtOnce = 16;   // rows a thread reads before it writes them
 
 // A thread owns a piece of W bytes of one head's keys or values of one sequence and
 // moves it for the kept nodes in order.  Nodes ascend and so do their places, each at
