@@ -20,6 +20,7 @@ SRCS = [os.path.join(PKG, "csrc", "xpress_argmax.hip"),
         os.path.join(PKG, "csrc", "kv_append.hip"),
         os.path.join(PKG, "csrc", "paged_attention.hip"),
         os.path.join(PKG, "csrc", "sparse_attention.hip"),
+        os.path.join(PKG, "csrc", "wide_attention.hip"),
         os.path.join(PKG, "csrc", "kv_pages.hip"),
         os.path.join(PKG, "csrc", "beams.hip"),
         os.path.join(PKG, "csrc", "sample.hip"),

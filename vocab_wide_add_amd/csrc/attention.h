@@ -74,24 +74,7 @@
 #include "kv_common.h"
 #include "xpress_argmax.h"
 
-namespace {
-
-using namespace xpress;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
-constexpr int kTile = 32;        // keys of one tile
-constexpr int kRound = kTile * kWaves;
-constexpr int kUnits = 256;       // compute units of the chip
-constexpr int kTable = 2048;     // keys whose places LDS holds at once
-constexpr int kTableStaged = 1024;  // the same where LDS also holds the keys
-constexpr float kNone = -INFINITY;
+namespace xpress {
 
 struct AttnArgs {
     const uint16_t* q;
@@ -115,6 +98,30 @@ struct AttnArgs {
     int64_t tree_n, tree_i;   // strides in words
     int32_t sinks;
 };
+
+// wide_attention.hip's: the sparse form for more than 64 rows a key-value head.
+XPRESS_INTERNAL void launch_wide(AttnArgs a, bool fp16, bool e4m3, bool once, hipStream_t stream);
+
+}  // namespace xpress
+
+namespace {
+
+using namespace xpress;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * 64;
+constexpr int kTile = 32;        // keys of one tile
+constexpr int kRound = kTile * kWaves;
+constexpr int kUnits = 256;       // compute units of the chip
+constexpr int kTable = 2048;     // keys whose places LDS holds at once
+constexpr int kTableStaged = 1024;  // the same where LDS also holds the keys
+constexpr float kNone = -INFINITY;
 
 // The keys that any query of a sequence sees, [lo, hi), and its parts.  SPARSE:
 // the sinks and the window's keys under one numbering, [0, hi); number i is key i
@@ -1143,7 +1150,7 @@ struct Shape {
     bool tree = false, sparse = false;
 };
 
-bool shape_ok(const Shape& s)
+[[maybe_unused]] bool shape_ok(const Shape& s)
 {
     const int64_t most = 0x7FFFFFFFll;
     return s.N >= 0 && s.N <= most && s.Q >= 0 && s.Q <= most && s.heads >= 1 && s.Hq >= 1 &&
@@ -1156,7 +1163,7 @@ bool shape_ok(const Shape& s)
 struct Plan {
     int rw;                        // waves of 16 rows (wide: 32) in a workgroup
     int64_t rows, groups, chunk, splits, units;
-    bool wide = false;             // attention_wide.h
+    bool wide = false;             // wide_attention.hip
 };
 
 // Rows: as many waves of 16 as hold them, up to the workgroup's 4, so that a
@@ -1179,9 +1186,9 @@ struct Plan {
 constexpr int64_t kMostWords = (int64_t)1 << 27;   // 1 GiB
 
 // Workspace words (8 bytes) of one part of every row: sums and (m, l).
-int64_t words_a_part(const Shape& s) { return s.N * s.Q * s.Hq * (s.dim + 2) / 2; }
+[[maybe_unused]] int64_t words_a_part(const Shape& s) { return s.N * s.Q * s.Hq * (s.dim + 2) / 2; }
 
-Plan plan_of(const Shape& s)
+[[maybe_unused]] Plan plan_of(const Shape& s)
 {
     Plan p;
     p.rows = s.Q * (s.Hq / s.heads);
@@ -1215,12 +1222,12 @@ Plan plan_of(const Shape& s)
 }
 
 // Workgroups and part sums in 32 bits.
-bool plan_ok(const Shape& s, const Plan& p)
+[[maybe_unused]] bool plan_ok(const Shape& s, const Plan& p)
 {
     return p.units <= 0x7FFFFFFFll / p.groups / 8;
 }
 
-int64_t plan_words(const Shape& s, const Plan& p)
+[[maybe_unused]] int64_t plan_words(const Shape& s, const Plan& p)
 {
     return p.splits > 1 ? p.splits * words_a_part(s) : 0;
 }
@@ -1252,16 +1259,9 @@ void launch_waves(const AttnArgs& a, bool once, hipStream_t stream)
     }
 }
 
-// attention_wide.h's.
-template <bool FP16, bool E4M3, int DP>
-void launch_wide(AttnArgs a, const Way& way, hipStream_t stream);
-
 template <bool FP16, bool E4M3, int DP, bool SPARSE>
 void launch_rows(const AttnArgs& a, const Way& way, hipStream_t stream)
 {
-    if constexpr (SPARSE) {
-        if (way.wide) return launch_wide<FP16, E4M3, DP>(a, way, stream);
-    }
     if (way.rw == 1) launch_waves<FP16, E4M3, DP, 1, SPARSE>(a, way.once, stream);
     else if (way.rw == 2) launch_waves<FP16, E4M3, DP, 2, SPARSE>(a, way.once, stream);
     else launch_waves<FP16, E4M3, DP, 4, SPARSE>(a, way.once, stream);
@@ -1278,7 +1278,8 @@ void launch_dims(const AttnArgs& a, const Way& way, hipStream_t stream)
 template <bool FP16, bool SPARSE>
 hipError_t launch_attention(const AttnArgs& a, const Way& way, hipStream_t stream)
 {
-    if (way.e4m3) launch_dims<FP16, true, SPARSE>(a, way, stream);
+    if (way.wide) launch_wide(a, FP16, way.e4m3, way.once, stream);
+    else if (way.e4m3) launch_dims<FP16, true, SPARSE>(a, way, stream);
     else launch_dims<FP16, false, SPARSE>(a, way, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;

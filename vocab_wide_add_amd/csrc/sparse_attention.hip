@@ -1,8 +1,8 @@
 // sparse_attention.hip -- attention over the paged cache where the queries do not see
 // all that came before them: the nodes of a tree, and a window with sinks.  The
-// sparse form of attention.h.
+// sparse form of attention.h, and for many rows that of wide_attention.hip.
 
-#include "attention_wide.h"
+#include "attention.h"
 
 extern "C" {
 

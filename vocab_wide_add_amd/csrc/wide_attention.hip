@@ -1,4 +1,4 @@
-// attention_wide.h -- the sparse form of the attention for more than 64 rows (queries
+// wide_attention.hip -- the sparse form of the attention for more than 64 rows (queries
 // times query heads) a key-value head: 32 rows to a wave (gfx950, MFMA 32x32).
 //
 // As attention.h with LDS stages, but a wave has twice the rows, so that the operands
@@ -31,8 +31,6 @@
 // A negative scale turns the queries' signs and a scale of zero the queries into zeros,
 // so that the largest score is the largest product, and weights are 2^(s scale - m) by
 // one fused step.
-#pragma once
-
 #include "attention.h"
 
 namespace {
@@ -667,13 +665,13 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
 }
 
 template <bool FP16, bool E4M3, int DP>
-void launch_wide(AttnArgs a, const Way& way, hipStream_t stream)
+void launch_dims_of(AttnArgs a, bool once, hipStream_t stream)
 {
     if (a.N * a.splits >= 8) a.units = (a.N * a.splits + 7) / 8 * 8 * a.Hk;   // see the kernel
     const uint32_t grid = (a.units + 7) / 8 * 8 * a.groups;
     for (a.first = 0; a.first < grid; a.first += kMostGroups) {
         const uint32_t n = grid - a.first < kMostGroups ? grid - a.first : kMostGroups;
-        if (way.once) {
+        if (once) {
             hipLaunchKernelGGL((wide_kernel<FP16, E4M3, DP, true>), dim3(n), dim3(kThreads), 0, stream, a);
         } else {
             hipLaunchKernelGGL((wide_kernel<FP16, E4M3, DP, false>), dim3(n), dim3(kThreads), 0, stream, a);
@@ -681,4 +679,22 @@ void launch_wide(AttnArgs a, const Way& way, hipStream_t stream)
     }
 }
 
+template <bool FP16, bool E4M3>
+void launch_types(const AttnArgs& a, bool once, hipStream_t stream)
+{
+    if (a.D <= 64) return launch_dims_of<FP16, E4M3, 64>(a, once, stream);
+    if (a.D <= 128) return launch_dims_of<FP16, E4M3, 128>(a, once, stream);
+    launch_dims_of<FP16, E4M3, 256>(a, once, stream);
+}
+
 }  // namespace
+
+namespace xpress {
+
+void launch_wide(AttnArgs a, bool fp16, bool e4m3, bool once, hipStream_t stream)
+{
+    if (fp16) e4m3 ? launch_types<true, true>(a, once, stream) : launch_types<true, false>(a, once, stream);
+    else e4m3 ? launch_types<false, true>(a, once, stream) : launch_types<false, false>(a, once, stream);
+}
+
+}  // namespace xpress
