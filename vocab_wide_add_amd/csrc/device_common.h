@@ -194,6 +194,22 @@ __device__ __forceinline__ void dma16(const uint16_t* gsrc, uint32_t lds_base)
         : "memory");
 }
 
+// One 4-byte load to LDS: lane l's word lands at LDS byte address lds_base + 4 l.  As
+// dma16: the wait state after M0 is kept, and the compiler adds no wait.
+__device__ __forceinline__ void dma4(const int32_t* gsrc, uint32_t lds_base)
+{
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %1, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(gsrc), "s"(lds_base)
+        : "memory");
+}
+
 // LDS byte address of a __shared__ element, made wave-uniform.
 __device__ __forceinline__ uint32_t lds_addr(const uint16_t* p)
 {

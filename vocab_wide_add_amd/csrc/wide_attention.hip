@@ -52,22 +52,6 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
     }
 }
 
-// One 4-byte load to LDS: lane l's word lands at LDS byte address lds_base + 4 l.  As
-// dma16: the wait state after M0 is kept, and the compiler adds no wait.
-__device__ __forceinline__ void dma4(const int32_t* gsrc, uint32_t lds_base)
-{
-    uint32_t saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %2\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dword %1, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "v"(gsrc), "s"(lds_base)
-        : "memory");
-}
-
 // The two lanes of a row.
 __device__ __forceinline__ float pair_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
 
