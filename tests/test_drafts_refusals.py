@@ -207,6 +207,28 @@ def test_beam_reorder_refuses():
     assert go([], src=0) == 0 and go([good], M=0, src=0) == 0
 
 
+@no_gpu_only
+@pytest.mark.parametrize("count", [2, 33, 300, 4096])
+def test_beam_reorder_refuses_overlaps_among_many_states(count):
+    lib = native.load()
+
+    def go(states):
+        return lib.xpress_beam_reorder(b"".join(native._STATE.pack(*s) for s in states), count, MiB, 4, 6, None)
+    good = [((2 * i + 2) * MiB, (2 * i + 3) * MiB, 64, 64, 64) for i in range(count)]
+    for at, other in ((0, count - 1), (count - 1, 0), (count // 2, 0)):
+        if at == other:
+            continue
+        for to in (good[other][1], good[other][1] + 383, good[other][1] - 383,     # written twice
+                   good[other][0], good[other][0] + 255, good[other][0] - 383):    # written where another reads
+            s = list(good)
+            s[at] = (s[at][0], to, 64, 64, 64)
+            assert go(s) == BAD
+    # a long span that ends past the ones which begin after it
+    s = list(good)
+    s[0] = (s[0][0], s[0][1], 64, MiB, 64)
+    assert go(s) == BAD
+
+
 def test_the_binding_refuses_tensors_on_the_cpu():
     t = torch.zeros(4, 8, dtype=torch.int32)
     one = torch.zeros(4, dtype=torch.int32)
