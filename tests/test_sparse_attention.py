@@ -269,6 +269,20 @@ def test_other_scales(scale, Q):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("Q", [3, 40])
+def test_a_scale_of_zero_keeps_queries_that_are_not_finite(Q, dtype):
+    (q, kc, vc, table, lens), _, sees, _ = made(90, [300, 50], Q, 4, 2, 64, 16, dtype, dtype)
+    q = q.clone()
+    q[0, 1, 2, 5], q[1, 2, 0, 60], q[1, 0, 1, 0] = float("nan"), float("inf"), float("-inf")
+    out, lse = call(q, kc, vc, table, lens, 300, 0, 0, ref.words_of(sees), 0.0)
+    hit = np.zeros(q.shape[:3], bool)
+    hit[0, 1, 2] = hit[1, 2, 0] = hit[1, 0, 1] = True
+    assert np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
+    assert np.isfinite(out[~hit]).all() and np.isfinite(lse[~hit]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_not_finite_values_under_many_rows(cache):
     """As above with 40 nodes: 80 rows a head, four words of them in two waves and more."""

@@ -21,15 +21,16 @@
 // and page ids come by LDS.
 //
 // Measured (32 query and 8 key-value heads of 128, bf16): 64 nodes of 32 sequences up to
-// 4096 tokens 165 us and 22 for the join, where 16 rows a wave took 200 and 30; without
-// products and weights the copies take 90, without copies the rest 125.  77 rows of heads
-// of 64 on an e4m3 cache, 48 sequences up to 6001: 77 and 8 (92 and 11).  Tried: eight
+// 4096 tokens 165 us and 11 for the join, where 16 rows a wave took 200: 0.7 PFLOP/s
+// with the weights' second part, and 0.34 GB of cache that two workgroups each read.
+// Without products and weights the copies take 90, without copies the rest 125.  77 rows of heads
+// of 64 on an e4m3 cache, 48 sequences up to 6001: 77 and 5 (92 with 16 rows).  Tried: eight
 // waves of 32 rows, which read the cache once, 205 for the 187; weights of one tile
 // beside the products of the next 209; three workgroups a compute unit at 64 dims 93 for
 // the 90.
 //
-// A negative scale turns the queries' signs and a scale of zero the queries into zeros,
-// so that the largest score is the largest product, and weights are 2^(s scale - m) by
+// A negative scale turns the queries' signs and a scale of zero the queries into zeros
+// (what is not finite of them into NaN, as 0 times it is), so that the largest score is the largest product, and weights are 2^(s scale - m) by
 // one fused step.
 #include "attention.h"
 
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
     {
         const float scale = a.scale * (a.k_scale ? a.k_scale[hk] : 1.0f);
         t.scale = scale == 0.0f ? 1.0f : __builtin_fabsf(scale);
-        const uint32_t sign = scale < 0.0f ? 0x80008000u : 0u, keep = scale == 0.0f ? 0u : ~0u;
+        const uint32_t sign = scale < 0.0f ? 0x80008000u : 0u;
         const uint32_t r = row0 + t.c;
         const bool on = r < a.rows;
         const uint32_t i = on ? r / a.G : 0, h = hk * a.G + (on ? r - i * a.G : 0);
@@ -532,7 +533,14 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = (w[e] ^ sign) & keep;
+            for (int e = 0; e < 4; ++e) {
+                if (scale == 0.0f) {
+                    const uint32_t lo = (w[e] & H::kExp & 0xFFFFu) == (H::kExp & 0xFFFFu) ? 0x7FFFu : 0;
+                    const uint32_t hi = (w[e] & H::kExp & 0xFFFF0000u) == (H::kExp & 0xFFFF0000u) ? 0x7FFF0000u : 0;
+                    w[e] = lo | hi;
+                }
+                w[e] ^= sign;
+            }
             t.q[x] = w;
         }
     }
