@@ -582,7 +582,8 @@ int xpress_kv_grow(int32_t* refs, int64_t pages, int32_t* table, int64_t stride_
  * xpress_kv_free -- gives back the pages of which no coming query sees a token: of
  * sequence n's entries those stay whose slot s has s * page_size < lens[n] and, with
  * window > 0, s * page_size < sinks or (s + 1) * page_size > lens[n] - window + 1
- * (what the token at position lens[n] will see).  Every other entry becomes -1, and
+ * (what the token at position lens[n] will see; a node of a tree that sees no node, not
+ * itself either, would see one place more).  Every other entry becomes -1, and
  * the count of the page it named goes down by one.  A finished sequence has lens 0;
  * rejected drafts are behind lens.
  */
