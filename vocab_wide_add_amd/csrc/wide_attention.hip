@@ -24,10 +24,11 @@
 // 4096 tokens 165 us and 11 for the join, where 16 rows a wave took 200: 0.7 PFLOP/s
 // with the weights' second part, and 0.34 GB of cache that two workgroups each read.
 // Without products and weights the copies take 90, without copies the rest 125.  77 rows of heads
-// of 64 on an e4m3 cache, 48 sequences up to 6001: 77 and 5 (92 with 16 rows).  Tried: eight
+// of 64 on an e4m3 cache, 48 sequences up to 6001: 66 and 5 (92 with 16 rows;
+// 77 while each value row's place in LDS was worked out by itself).  Tried: eight
 // waves of 32 rows, which read the cache once, 205 for the 187; weights of one tile
-// beside the products of the next 209; three workgroups a compute unit at 64 dims 93 for
-// the 90.
+// beside the products of the next 209; three workgroups a compute unit at 64 dims: no
+// change.
 //
 // A negative scale turns the queries' signs and a scale of zero the queries into zeros
 // (what is not finite of them into NaN, as 0 times it is), so that the largest score is the largest product, and weights are 2^(s scale - m) by
@@ -39,7 +40,7 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kRing = 8;      // stages whose keys' places are known
-constexpr uint32_t kRanked = 256;  // parts that are taken by size
+constexpr uint32_t kRanked = kThreads;  // parts that are taken by size
 
 template <bool FP16>
 __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
@@ -271,13 +272,18 @@ struct WideTile {
             }
             s = mfma32<FP16>(y, q[i], s);
         }
+        // slot(row + 4 g) less slot(row) is 4, and where slot turns rows 1 more or less
+        const uint32_t at_c = lane_c * kOuts * (E4M3 ? 1 : 2), turned = S::kRow < 256 ? S::kRow : 0;
+        const uint32_t even_at = at_c + lane_g * (4 * S::kRow + turned), odd_at = at_c + lane_g * (4 * S::kRow - turned);
         uint32_t v[2][8][kWords];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t row = 16 * h + key_of(e, lane_g);
-                load_value(v[h][e], vs + S::slot(row) * S::kRow, lane_c * kOuts * (E4M3 ? 1 : 2));
+                // slot(16 h + key_of(e, lane_g)), where lane_g only turns its last bit: two
+                // lanes' offsets serve all rows
+                const uint32_t row = 16 * h + key_of(e, 0), slot = S::slot(row);
+                load_value(v[h][e], vs + slot * S::kRow, slot & 1 ? odd_at : even_at);
             }
         __builtin_amdgcn_sched_barrier(0);
         u32x4 big[2], rest[2];
@@ -459,16 +465,17 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
         if (tid < all) {
             const uint32_t x = tid / a.N;
             const int32_t from = (int32_t)(x * a.chunk), hi = keys_of<true>(a, tid - x * a.N).hi;
-            mine = (uint32_t)min(max(hi - from, 0), (int32_t)a.chunk) + 1;
+            // sizes in 128 keys, the first of equal ones first
+            mine = (uint32_t)min(max(hi - from, 0), (int32_t)a.chunk) / 128 * kRanked + (kRanked - tid);
         }
-        if (tid < kRanked) sizes[tid] = mine;
+        sizes[tid] = mine;
         __syncthreads();
         uint32_t rank = 0;
 #pragma unroll 8
         for (uint32_t i = 0; i < all; i += 4) {
             const u32x4 y = *reinterpret_cast<const u32x4*>(&sizes[i]);   // 0 past the parts
 #pragma unroll
-            for (uint32_t x = 0; x < 4; ++x) rank += y[x] > mine || (y[x] == mine && i + x < tid);
+            for (uint32_t x = 0; x < 4; ++x) rank += y[x] > mine;
         }
         if (tid < all && rank == which) chosen = tid;
         __syncthreads();
