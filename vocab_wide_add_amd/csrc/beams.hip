@@ -26,7 +26,7 @@
 //
 // Bound by the bytes for many rows; by the two launches and the chain of one workgroup
 // for few.  Measured (V = 152064, K = 8): 480 rows of 60 sequences with a bias 57 us for
-// the parts, 5.1 TB/s, and 7 for the join, most of it the logs and the lists' loads, each
+// the parts, 5.1 TB/s, and 10 for the join, most of it the logs and the lists' loads, each
 // waited for; 4 rows of one 8.2 and 7.3.  Their states (256 tokens and 4096 hidden values
 // a row) 5 and 3.0.  Two vectors of a thread on their way in place of four: 71 us for the
 // 68 of the whole; six 72; shorter parts 69.

@@ -31,8 +31,8 @@
 // change.
 //
 // A negative scale turns the queries' signs and a scale of zero the queries into zeros
-// (what is not finite of them into NaN, as 0 times it is), so that the largest score is the largest product, and weights are 2^(s scale - m) by
-// one fused step.
+// (what is not finite of them into NaN, as 0 times it is), so that the largest score is
+// the largest product, and weights are 2^(s scale - m) by one fused step.
 #include "attention.h"
 
 namespace {
