@@ -2,8 +2,8 @@
 // times query heads) a key-value head: 32 rows to a wave (gfx950, MFMA 32x32).
 //
 // As attention.h with LDS stages, but a wave has twice the rows, so that the operands
-// which it takes from LDS, and the values' transposition in registers, serve twice as
-// much; keys' places are found a few stages ahead in a ring of eight stages instead of a
+// which it takes from LDS serve twice as much; values are transposed on their way out of
+// LDS; keys' places are found a few stages ahead in a ring of eight stages instead of a
 // table, so that a part may be as long as it likes; and the parts are taken by size.  A
 // workgroup's four waves hold 128 rows.  With lane l = 32 g + c:
 //
@@ -11,9 +11,8 @@
 //                 (lane: row c).  The lane gets the scores of row c with keys
 //                 8 (i / 4) + 4 g + i % 4: a row's state lives in two lanes.
 //   O^T += V^T P  P^T is already in B's layout: slot 8 g + e of step h is key
-//                 16 h + 8 (e / 4) + 4 g + e % 4.  A = V^T: the lane reads dims
-//                 w c .. w c + w - 1 (w = DP / 32) of its eight keys and transposes
-//                 them; dim w c + j is row c of product j.
+//                 16 h + 8 (e / 4) + 4 g + e % 4.  A = V^T: dim 32 j + c of the lane's
+//                 eight keys for product j, by transposing loads (take_value).
 //
 // The loop's registers are full: whatever the compiler would have to fetch back from
 // memory inside it, and page ids in registers too, would wait for every copy on its way,
@@ -21,11 +20,12 @@
 // and page ids come by LDS.
 //
 // Measured (32 query and 8 key-value heads of 128, bf16): 64 nodes of 32 sequences up to
-// 4096 tokens 165 us and 11 for the join, where 16 rows a wave took 200: 0.7 PFLOP/s
+// 4096 tokens 162 us and 11 for the join, where 16 rows a wave took 200: 0.7 PFLOP/s
 // with the weights' second part, and 0.34 GB of cache that two workgroups each read.
 // Without products and weights the copies take 90, without copies the rest 125.  77 rows of heads
-// of 64 on an e4m3 cache, 48 sequences up to 6001: 66 and 5 (92 with 16 rows;
-// 77 while each value row's place in LDS was worked out by itself).  Tried: eight
+// of 64 on an e4m3 cache, 48 sequences up to 6001: 62 and 5 (92 with 16 rows;
+// 66 with the transposition in registers, and 77 with each value row's place in LDS
+// worked out by itself).  Tried: eight
 // waves of 32 rows, which read the cache once, 205 for the 187; weights of one tile
 // beside the products of the next 209; three workgroups a compute unit at 64 dims: no
 // change.
@@ -38,6 +38,10 @@
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i32x2 LocalI32x2;
+typedef __attribute__((address_space(3))) i16x4 LocalI16x4;
 
 constexpr uint32_t kRing = 8;      // stages whose keys' places are known
 constexpr uint32_t kRanked = kThreads;  // parts that are taken by size
@@ -54,6 +58,18 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
     }
 }
 
+// A value row's pieces (16 bytes) go to piece ^ value_turn(row) in LDS, so that the rows
+// of which 32 lanes read 32 dims at once (four in a row, e4m3 twice four, eight apart) lie
+// in different banks.
+template <bool E4M3, int DP>
+__device__ __forceinline__ uint32_t value_turn(uint32_t row)
+{
+    constexpr uint32_t kRow = DP * (E4M3 ? 1 : 2);   // 256 bytes: all banks
+    const uint32_t r = kRow >= 256 ? row & 3 : kRow == 128 ? row >> 1 & 1 : 0;
+    constexpr uint32_t kBits = kRow >= 256 ? 2 : kRow == 128 ? 1 : 0;
+    return E4M3 ? (r | (row >> 3 & 1) << kBits) * 2 : r * 4;
+}
+
 // The two lanes of a row.
 __device__ __forceinline__ float pair_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
 
@@ -63,8 +79,8 @@ struct WideTile {
     using S = Lines<E4M3, DP>;
     static constexpr int kSteps = DP / 16;              // products of the scores
     static constexpr int kLoads = E4M3 ? DP / 32 : DP / 16;   // 16-byte pieces of a key row per lane
-    static constexpr int kOuts = DP / 32;               // of the output, and dims of a value row per lane
-    static constexpr int kWords = E4M3 ? (kOuts + 3) / 4 : kOuts / 2;   // 32-bit words of those
+    static constexpr int kOuts = DP / 32;               // of the output
+    static constexpr int kWords = E4M3 ? 2 : 4;         // 32-bit words of eight keys' values
 
     const AttnArgs& a;
     uint32_t c, g;
@@ -198,46 +214,52 @@ struct WideTile {
             }
     }
 
-    // A operands of products (2 p, 2 p + 1) from the eight keys' words.
-    static __device__ __forceinline__ void value_parts(const uint32_t (&v)[8][kWords], int p, u32x4* even, u32x4* odd)
+    // The A operand of product j, step h, from LDS: dim 32 j + c of the lane's eight keys, by
+    // transposing loads.  Sixteen lanes give the addresses of 16 dims of four keys, eight
+    // bytes each (e4m3: of eight keys), and each gets one dim of all of them.  at: the
+    // lane's offset at j = 0, see value_at.
+    template <int W>
+    static __device__ __forceinline__ void take_value(uint32_t (&to)[W], const char* at)
     {
-        uint32_t x[8];
+        if constexpr (E4M3) {
+            const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LocalI32x2*)at);
+            to[0] = (uint32_t)x[0];
+            to[1] = (uint32_t)x[1];
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (E4M3) {
-                x[e] = p % 2 ? H::template from8<true>(v[e][p / 2]) : H::template from8<false>(v[e][p / 2]);
-            } else {
-                x[e] = v[e][p];
+            for (int i = 0; i < 2; ++i) {
+                const u32x2 x = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LocalI16x4*)(at + i * 8 * S::kRow)));
+                to[2 * i] = x[0];
+                to[2 * i + 1] = x[1];
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            (*even)[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
-            (*odd)[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
         }
     }
 
-    // The lane's dims of one key's values.
-    static __device__ __forceinline__ void load_value(uint32_t (&to)[kWords], const char* row, uint32_t at)
+    // Where the lane reads product 0's dims of step 0, from the tile's first value row;
+    // product j's are that ^ j kBlock, as the rows' blocks change places (value_turn).
+    static constexpr uint32_t kBlock = 32 * (E4M3 ? 1 : 2);   // bytes of 32 dims
+    static __device__ __forceinline__ uint32_t value_at(uint32_t lane)
     {
-        if constexpr (E4M3 && kOuts == 2) {
-            to[0] = *reinterpret_cast<const uint16_t*>(row + at);
-        } else if constexpr (kWords == 1) {
-            to[0] = *reinterpret_cast<const uint32_t*>(row + at);
-        } else if constexpr (kWords == 2) {
-            const u32x2 x = *reinterpret_cast<const u32x2*>(row + at);
-            to[0] = x[0];
-            to[1] = x[1];
+        const uint32_t i = lane & 15, half = lane >> 4 & 1, g = lane >> 5;
+        const uint32_t row = E4M3 ? i / 8 * 8 + g * 4 + i / 2 % 4 : g * 4 + i / 4;
+        const uint32_t byte = half * (kBlock / 2) + (E4M3 ? i % 2 : i % 4) * 8;
+        return row * S::kRow + (byte ^ value_turn<E4M3, DP>(row) * 16);
+    }
+
+    static __device__ __forceinline__ u32x4 operand(const uint32_t (&v)[kWords])
+    {
+        if constexpr (E4M3) {
+            return u32x4{H::template from8<false>(v[0]), H::template from8<true>(v[0]), H::template from8<false>(v[1]),
+                         H::template from8<true>(v[1])};
         } else {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(row + at);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) to[w] = x[w];
+            return u32x4{v[0], v[1], v[2], v[3]};
         }
     }
 
     // One tile whose rows are in LDS.  One path for all tiles: with two, the sums lay in
     // other registers in each and were moved between them.
-    __device__ __forceinline__ void tile(const char* ks, const char* vs, bool all, uint32_t exist, uint32_t on)
+    __device__ __forceinline__ void tile(const char* ks, const char* vs, bool all, uint32_t on)
     {
         // the lane's places in the tile, worked out here and not kept beside the sums
         uint32_t lane_c = c, lane_g = g;
@@ -272,37 +294,20 @@ struct WideTile {
             }
             s = mfma32<FP16>(y, q[i], s);
         }
-        // slot(row + 4 g) less slot(row) is 4, and where slot turns rows 1 more or less
-        const uint32_t at_c = lane_c * kOuts * (E4M3 ? 1 : 2), turned = S::kRow < 256 ? S::kRow : 0;
-        const uint32_t even_at = at_c + lane_g * (4 * S::kRow + turned), odd_at = at_c + lane_g * (4 * S::kRow - turned);
-        uint32_t v[2][8][kWords];
+        const uint32_t at0 = value_at(lane_g * 32 + lane_c);
+        uint32_t v[2][kOuts][kWords];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < kOuts; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // slot(16 h + key_of(e, lane_g)), where lane_g only turns its last bit: two
-                // lanes' offsets serve all rows
-                const uint32_t row = 16 * h + key_of(e, 0), slot = S::slot(row);
-                load_value(v[h][e], vs + slot * S::kRow, slot & 1 ? odd_at : even_at);
-            }
+            for (int h = 0; h < 2; ++h) take_value(v[h][j], vs + (at0 ^ (j * kBlock)) + h * 16 * S::kRow);
         __builtin_amdgcn_sched_barrier(0);
         u32x4 big[2], rest[2];
         weigh(s, all, on, big, rest);
-        if (exist != ~0u) {
-            asm volatile("");
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-#pragma unroll
-                    for (int w = 0; w < kWords; ++w) v[h][e][w] = exist >> (16 * h + key_of(e, g)) & 1 ? v[h][e][w] : 0;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int p = 0; p < kOuts / 2; ++p) {
-                u32x4 even, odd;
-                value_parts(v[h], p, &even, &odd);
+                const u32x4 even = operand(v[h][2 * p]), odd = operand(v[h][2 * p + 1]);
                 o[2 * p] = mfma32<FP16>(even, big[h], o[2 * p]);
                 o[2 * p + 1] = mfma32<FP16>(odd, big[h], o[2 * p + 1]);
                 o[2 * p] = mfma32<FP16>(even, rest[h], o[2 * p]);
@@ -342,14 +347,14 @@ struct WideTile {
         for (int32_t at = first; at <= last; ++at) {
             turn_to(at);
             const uint32_t its = seen(exist, key0);
-            // (two dims of the eight keys at a time: more at once would take registers from
-            // the loop over all tiles)
+            // (one product's values at a time: more at once would take registers from the
+            // loop over all tiles)
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 const u32x4 bh = h ? big[1] : big[0], rh = h ? rest[1] : rest[0];
 #pragma unroll
-                for (int p = 0; p < kOuts / 2; ++p) {
-                    const uint32_t d = c * kOuts + 2 * p;
+                for (int j = 0; j < kOuts; ++j) {
+                    const uint32_t d = 32 * j + c;
                     uint32_t v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -358,30 +363,27 @@ struct WideTile {
                         const bool on = d < a.D && (its >> k & 1);
                         const char* from = vbase + (on ? (int64_t)((uint64_t)hi << 32 | lo) + d * (E4M3 ? 1 : 2) : 0);
                         if constexpr (E4M3) {
-                            v[e] = H::template from8<false>(*reinterpret_cast<const uint16_t*>(from));
+                            v[e] = H::template from8<false>(*reinterpret_cast<const uint8_t*>(from));
                         } else {
-                            v[e] = *reinterpret_cast<const uint32_t*>(from);
+                            v[e] = *reinterpret_cast<const uint16_t*>(from);
                         }
                         v[e] = on ? v[e] : 0;
                     }
+                    // the weights' second part meets finite values only
+                    u32x4 x, z;
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        // the weights' second part meets finite values only
-                        u32x4 x, z;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t b = __builtin_amdgcn_perm(v[2 * w + 1], v[2 * w], y ? 0x07060302u : 0x05040100u);
-                            x[w] = b;
-                            z[w] = ((b & H::kExp & 0xFFFFu) == (H::kExp & 0xFFFFu) ? 0 : b & 0xFFFFu) |
-                                   ((b & H::kExp & 0xFFFF0000u) == (H::kExp & 0xFFFF0000u) ? 0 : b & 0xFFFF0000u);
-                        }
-                        f32x16 r;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = 0.0f;
-                        r = mfma32<FP16>(x, bh, r);
-                        r = mfma32<FP16>(z, rh, r);
-                        if (mine == at) o[2 * p + y] += r;
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t b = __builtin_amdgcn_perm(v[2 * w + 1], v[2 * w], 0x05040100u);
+                        x[w] = b;
+                        z[w] = ((b & H::kExp & 0xFFFFu) == (H::kExp & 0xFFFFu) ? 0 : b & 0xFFFFu) |
+                               ((b & H::kExp & 0xFFFF0000u) == (H::kExp & 0xFFFF0000u) ? 0 : b & 0xFFFF0000u);
                     }
+                    f32x16 r;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = 0.0f;
+                    r = mfma32<FP16>(x, bh, r);
+                    r = mfma32<FP16>(z, rh, r);
+                    if (mine == at) o[j] += r;
                 }
             }
         }
@@ -421,11 +423,10 @@ struct Ahead : Lines<E4M3, DP> {
 #pragma unroll
         for (uint32_t x = 0; x < kCopies; ++x) {
             const uint32_t at = x * kThreads + thread, row = at / L::kPieces, piece = at % L::kPieces;
-            const uint32_t kd = (piece ^ L::turn(row)) * 16, vd = piece * 16;
+            const uint32_t kd = (piece ^ L::turn(row)) * 16, vd = (piece ^ value_turn<E4M3, DP>(row)) * 16;
             const uint32_t here = to + x * (kThreads * 16) + wave_at;
             dma16<ONCE>(reinterpret_cast<const uint16_t*>(kbase + place[row] + (kd < used ? kd : 0)), here);
-            dma16<ONCE>(reinterpret_cast<const uint16_t*>(vbase + place[L::slot(row)] + (vd < used ? vd : 0)),
-                        here + kBytes);
+            dma16<ONCE>(reinterpret_cast<const uint16_t*>(vbase + place[row] + (vd < used ? vd : 0)), here + kBytes);
         }
     }
 };
@@ -507,7 +508,11 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
     };
     auto put_place = [&](uint32_t j, int64_t at) {   // by a whole wave, j = 64 stage + lane
         const uint64_t on = __ballot(at >= 0);
-        place[j % (kRing * kKeys)] = at < 0 ? 0 : at;
+        // a key that does not exist has the place of one that does, so that its value, which
+        // meets a weight of zero, is as finite as the others (zeroed in the loop, values took
+        // a move of every register)
+        const int64_t other = on ? __shfl(at, __builtin_ctzll(on)) : 0;
+        place[j % (kRing * kKeys)] = at < 0 ? other : at;
         if (lane < 2) there[j / 32 % (kRing * 2) + lane] = (uint32_t)(on >> (lane * 32));
     };
 #pragma unroll
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
             const bool all = all_seen(at, exist);
             uint32_t on = 0;
             if (!all) on = t.seen(exist, part0 + (int32_t)at);
-            t.tile(ks, vs, all, exist, on);
+            t.tile(ks, vs, all, on);
         }
     }
     if (some && __any(!t.finite())) {
@@ -632,25 +637,30 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
     const float inv = t.l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[hk] : 1.0f) / t.l;
     const int64_t at = ((int64_t)owner * a.rows + r) * a.splits + split;
     uint16_t* out = a.out + n * a.o_n + i * a.o_i + h * a.o_h;
-    // the lane's dims: for each b, 4 kOuts in a row from kOuts (8 b + 4 g) on; eight of
-    // them at a time
+    // the lane's dims: four in a row from 32 j + 8 b + 4 g on
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int j = 0; j < T::kOuts; ++j)
 #pragma unroll
-        for (int y = 0; y < 4 * T::kOuts; y += 8) {
-            const uint32_t d = (uint32_t)T::kOuts * (8 * b + 4 * t.g) + y;
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t d = 32 * j + 8 * b + 4 * t.g;
             if (d >= a.D) continue;
-            float z[8];
+            f32x4 z;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = t.o[(y + e) % T::kOuts][b * 4 + (y + e) / T::kOuts];
-            if (direct) {
+            for (int e = 0; e < 4; ++e) z[e] = t.o[j][4 * b + e];
+            if (!direct) {
+                *reinterpret_cast<f32x4*>(a.part + at * a.D + d) = z;
+                continue;
+            }
+            u32x2 w;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = t.l == 0.0f ? 0.0f : z[e] * inv;
-                store8(a, FP16, out + d, z);
+            for (int e = 0; e < 2; ++e) {
+                w[e] = H::pack(t.l == 0.0f ? 0.0f : z[2 * e] * inv, t.l == 0.0f ? 0.0f : z[2 * e + 1] * inv);
+            }
+            if (a.wide) {
+                *reinterpret_cast<u32x2*>(out + d) = w;
             } else {
-                f32x4* dst = reinterpret_cast<f32x4*>(a.part + at * a.D + d);
-                dst[0] = f32x4{z[0], z[1], z[2], z[3]};
-                dst[1] = f32x4{z[4], z[5], z[6], z[7]};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[d + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
             }
         }
     if (t.g == 0) {
