@@ -253,6 +253,17 @@ def test_long_contexts_under_many_rows(dtype, cache, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Q,dtype,cache", [(1, "bf16", "bf16"), (4, "fp16", "e4m3"), (9, "bf16", "bf16")])
+def test_parts_by_size_and_of_many_lengths(Q, dtype, cache):
+    """More workgroups than the chip holds, of parts between none and all of their keys: every
+    part is taken once, whatever its rank."""
+    lens = [(37 * i * i) % 2600 for i in range(38)] + [0, 2600]
+    (q, kc, vc, table, lens), scales, sees, _ = made(93, lens, Q, 16, 8, 64, 16, dtype, cache)
+    verify(q, kc, vc, table, lens, 2600, sees=sees, **scales)
+    verify(q, kc, vc, table, lens, 2600, **scales)
+
+
+@pytest.mark.gpu
 def test_more_sequences_than_are_ranked():
     say("300 sequences")
     rng = np.random.default_rng(4)

@@ -46,6 +46,10 @@
 // SPARSE is the form of a tree of new tokens and of a window with sinks: a masked
 // tile asks per key, and the sinks and the window's keys are numbered one after the
 // other, so that what lies between them costs nothing.  The dense form has none of it.
+// Measured (32 query and 8 key-value heads of 128, bf16): trees of 16 nodes on 32
+// sequences up to 4096 tokens 70 us and 6 for the join, 4.2 TB/s, the copies' pace as
+// for the dense block; 32 windows of 4096 behind 4 sinks 104 and 4, 5.2 TB/s; a tree of 8
+// on one sequence of 1009 9.5 and 3.4, latency.
 //
 // The waves' sums meet in LDS.  A sequence of one part is written out
 // directly; with more parts (chosen on the host from the number of rows'
@@ -736,6 +740,36 @@ constexpr int tiles_ahead()
     return DP * (E4M3 ? 1 : 2) <= 64 ? 3 : DP * (E4M3 ? 1 : 2) <= 128 ? 2 : 1;
 }
 
+constexpr uint32_t kRanked = kThreads;  // parts that are taken by size
+
+// Sequences' parts by size, the largest first: `which` is a rank among all (split,
+// sequence), kRanked or fewer, which every workgroup finds for itself.  Returns split * N
+// + sequence.  sizes: kRanked words of LDS, 16-byte aligned, which the workgroup may write
+// again after its next barrier.
+__device__ __forceinline__ uint32_t part_by_size(const AttnArgs& a, uint32_t which, uint32_t* sizes, uint32_t* chosen)
+{
+    const uint32_t tid = threadIdx.x, all = a.N * a.splits;
+    uint32_t mine = 0;
+    if (tid < all) {
+        const uint32_t x = tid / a.N;
+        const int32_t from = (int32_t)(x * a.chunk), hi = keys_of<true>(a, tid - x * a.N).hi;
+        // sizes in 128 keys, the first of equal ones first
+        mine = (uint32_t)min(max(hi - from, 0), (int32_t)a.chunk) / 128 * kRanked + (kRanked - tid);
+    }
+    sizes[tid] = mine;
+    __syncthreads();
+    uint32_t rank = 0;
+#pragma unroll 8
+    for (uint32_t i = 0; i < all; i += 4) {
+        const u32x4 y = *reinterpret_cast<const u32x4*>(&sizes[i]);   // 0 past the parts
+#pragma unroll
+        for (uint32_t x = 0; x < 4; ++x) rank += y[x] > mine;
+    }
+    if (tid < all && rank == which) *chosen = tid;
+    __syncthreads();
+    return *chosen;
+}
+
 // RW waves of the workgroup hold 16 rows each, KW = kWaves / RW waves share a
 // row's keys.  RW = 1: each wave loads its own tiles to registers, tiles_ahead()
 // of them ahead.  RW > 1: the waves' tiles come from LDS, two stages deep.  MANY: the
@@ -765,8 +799,21 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     const uint32_t id = a.first + blockIdx.x;
     const uint32_t unit = id / (8 * a.groups) * 8 + id % 8, group = id / 8 % a.groups;
     if (unit >= a.units) return;
-    const uint32_t owner = unit % (a.N * a.Hk), split = unit / (a.N * a.Hk);
-    const uint32_t n = owner / a.Hk, hk = owner % a.Hk;
+    uint32_t owner = unit % (a.N * a.Hk), split = unit / (a.N * a.Hk);
+    uint32_t n = owner / a.Hk;
+    const uint32_t hk = owner % a.Hk;
+    if constexpr (SPARSE) {
+        // Long parts first where not all fit the chip at once and lengths may differ (16
+        // nodes of 32 sequences up to 4096, heads of 128: the call 77 us, in the order of
+        // the sequences 87; of 64: 54 and 60)
+        if (a.N > 1 && a.window == 0 && a.N * a.splits <= kRanked && a.units * a.groups > 2 * kUnits) {
+            const uint32_t x = part_by_size(a, unit / a.Hk, reinterpret_cast<uint32_t*>(pool), &holes);
+            split = x / a.N;
+            n = x - split * a.N;
+            owner = n * a.Hk + hk;
+            __syncthreads();
+        }
+    }
     const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
     const uint32_t rw = wave % RW, kw = wave / RW;
     const Keys keys = keys_of<SPARSE>(a, n);

@@ -44,7 +44,6 @@ typedef __attribute__((address_space(3))) i32x2 LocalI32x2;
 typedef __attribute__((address_space(3))) i16x4 LocalI16x4;
 
 constexpr uint32_t kRing = 8;      // stages whose keys' places are known
-constexpr uint32_t kRanked = kThreads;  // parts that are taken by size
 
 template <bool FP16>
 __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
@@ -460,27 +459,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) wide_kernel(AttnA
     }
     uint32_t n = which % a.N, split = which / a.N;
     if (a.N > 1 && all <= kRanked) {
-        // the parts by size, the largest first: `which` is a rank among all (sequence,
-        // part), which every workgroup finds for itself
-        uint32_t mine = 0;
-        if (tid < all) {
-            const uint32_t x = tid / a.N;
-            const int32_t from = (int32_t)(x * a.chunk), hi = keys_of<true>(a, tid - x * a.N).hi;
-            // sizes in 128 keys, the first of equal ones first
-            mine = (uint32_t)min(max(hi - from, 0), (int32_t)a.chunk) / 128 * kRanked + (kRanked - tid);
-        }
-        sizes[tid] = mine;
-        __syncthreads();
-        uint32_t rank = 0;
-#pragma unroll 8
-        for (uint32_t i = 0; i < all; i += 4) {
-            const u32x4 y = *reinterpret_cast<const u32x4*>(&sizes[i]);   // 0 past the parts
-#pragma unroll
-            for (uint32_t x = 0; x < 4; ++x) rank += y[x] > mine;
-        }
-        if (tid < all && rank == which) chosen = tid;
-        __syncthreads();
-        const uint32_t x = chosen;
+        const uint32_t x = part_by_size(a, which, sizes, &chosen);
         split = x / a.N;
         n = x - split * a.N;
     }
