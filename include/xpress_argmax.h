@@ -615,7 +615,7 @@ int xpress_kv_compact(const xpress_kv_cache* cache, const int32_t* start, const 
  * largest score, in descending order: the score, the row r and the id v.  Among equal
  * scores the lower row comes first, in a row the larger logit, then the lower id.
  * Scores are formed in 64 bits from sums of 32-bit terms (relative error of the sum
- * about 1e-7 at most) and rounded once.
+ * below 6e-7, usually 3e-8) and rounded once.
  *
  * NaN logits and -inf are no candidates and add nothing to the sum; a +inf logit
  * leaves only the +inf ones, with equal shares.  A beam whose score is not finite
