@@ -33,6 +33,7 @@ class Beams(Decoder):
         self.tables = [torch.full((rows, width), -1, **i32) for _ in range(2)]
         self.lens = torch.zeros(rows, **i32)
         self.copies, self.missing = torch.zeros(rows, 3, **i32), torch.zeros(2, 1, **i32)
+        self.lacked = torch.zeros(1, **i32)   # of all calls since the start
         self.scores = torch.zeros(rows, device="cuda")
         self.best, self.rows = torch.zeros(N, beams, device="cuda"), torch.zeros(N, beams, **i32)
         self.ids = torch.zeros(N, beams, device="cuda", dtype=torch.int64)
@@ -60,6 +61,19 @@ class Beams(Decoder):
             self.history[0][i * self.beams:(i + 1) * self.beams, :len(p)] = torch.tensor(p, device="cuda")
         self.scores.fill_(float("-inf"))
         self.scores[::self.beams] = 0.0
+        self.lacked.zero_()
+        self.count_missing()
+        self.check()
+
+    def count_missing(self):
+        """Adds what the last xpress_kv_grow and xpress_kv_fork lacked, which the next ones write
+        over."""
+        self.lacked.add_(self.missing[0]).add_(self.missing[1])
+
+    def check(self):
+        """Tokens without a page are not stored, and hypotheses over them mean nothing."""
+        if int(self.lacked):
+            raise RuntimeError("the pool lacked %d pages" % int(self.lacked))
 
     def half(self, a, b):
         """One token for every beam, from buffers a to buffers b."""
@@ -77,6 +91,7 @@ class Beams(Decoder):
         native.xpress_kv_free(self.refs[a], self.table, longer, self.page, window=self.window, sinks=self.sinks)
         native.xpress_kv_fork(self.refs[a], self.table, longer, self.rows, self.refs[b], self.tables[b], self.copies,
                               self.page, missing=self.missing[1])
+        self.count_missing()
         native.xpress_kv_copy(self.k_cache, self.v_cache, self.copies)
         native.xpress_beam_reorder([(self.history[a], self.history[b])], self.rows)
         self.scores.copy_(self.best.view(-1))
@@ -104,6 +119,7 @@ class Beams(Decoder):
             for _ in range(pairs):
                 self.half(0, 1)
                 self.half(1, 0)
+        self.check()
         return self.history[0], self.scores
 
 

@@ -1,0 +1,34 @@
+"""What the beam search example does where it cannot go on: pages that run out."""
+import os
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+
+def made(pages=None):
+    import beams
+    return beams.Beams(3, 3, 80, window=24, sinks=3, page=8, hq=8, hk=2, dim=64, vocab=1000, pages=pages)
+
+
+def prompts(seed, lens=(40, 1, 17)):
+    r = torch.Generator().manual_seed(seed)
+    return [torch.randint(0, 1000, (n,), generator=r).tolist() for n in lens]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_search_that_lacked_pages_says_so(graph):
+    """Nine pages hold the prompts and the first parting of their beams; the first token of
+    the second sequence's beams needs more.  Steps after that lack none."""
+    d = made(9)
+    d.start(prompts(7))
+    with pytest.raises(RuntimeError, match="pages"):
+        d.search(4, graph=graph)
+    with pytest.raises(RuntimeError, match="pages"):
+        made(6).start(prompts(7))
+    d = made()
+    d.start(prompts(7))
+    d.search(4, graph=graph)
