@@ -44,7 +44,8 @@ class Beams(Decoder):
         are forked to the beams, of which the first alone counts at first."""
         lens = torch.tensor([len(p) - 1 for p in prompts], dtype=torch.int32, device="cuda")
         rows = torch.arange(self.seqs, dtype=torch.int32, device="cuda")
-        table = self.tables[1][:self.seqs].contiguous()
+        self.refs[1].zero_()                  # the pages of an earlier search are free
+        table = torch.full_like(self.tables[1][:self.seqs], -1)
         native.xpress_kv_grow(self.refs[1], table, torch.zeros_like(lens), lens, self.page, missing=self.missing[0])
         self.table = table
         ids = torch.tensor([i for p in prompts for i in p[:-1]], dtype=torch.int64, device="cuda")

@@ -1,4 +1,4 @@
-"""What the beam search example does where it cannot go on: pages that run out."""
+"""The beam search example where it cannot go on, as pages run out, and started again."""
 import os
 import sys
 
@@ -32,3 +32,18 @@ def test_a_search_that_lacked_pages_says_so(graph):
     d = made()
     d.start(prompts(7))
     d.search(4, graph=graph)
+
+
+@pytest.mark.gpu
+def test_a_second_search_is_as_a_fresh_one():
+    a, b = made(), made()
+    a.start(prompts(7))
+    a.search(12)
+    for d in (a, b):
+        d.start(prompts(8, (33, 9, 50)))
+    got, want = a.search(8), b.search(8)
+    torch.cuda.synchronize()
+    for row, n in enumerate((33, 9, 50)):
+        here = slice(3 * row, 3 * row + 3)
+        assert torch.equal(got[0][here, :n + 8], want[0][here, :n + 8])
+    assert torch.equal(got[1], want[1])
