@@ -42,6 +42,9 @@ class Beams(Decoder):
     def start(self, prompts):
         """Lists of token ids, one a sequence: all but each last one go into the cache once, and
         are forked to the beams, of which the first alone counts at first."""
+        self.longest = max(len(p) for p in prompts)
+        if len(prompts) != self.seqs or min(len(p) for p in prompts) < 1 or self.longest > self.max_len:
+            raise ValueError("%d prompts of 1 to %d tokens expected" % (self.seqs, self.max_len))
         lens = torch.tensor([len(p) - 1 for p in prompts], dtype=torch.int32, device="cuda")
         rows = torch.arange(self.seqs, dtype=torch.int32, device="cuda")
         self.refs[1].zero_()                  # the pages of an earlier search are free
@@ -100,7 +103,12 @@ class Beams(Decoder):
         self.history[b].scatter_(1, self.lens.long()[:, None], self.ids.view(-1, 1))
 
     def search(self, steps, graph=False):
-        """`steps` (even) tokens; the hypotheses [rows, max_len] and their scores."""
+        """`steps` (even, 2 or more) tokens; the hypotheses [rows, max_len] and their scores."""
+        # (past max_len a token's place in the history is out of range on the device)
+        if steps < 2 or steps % 2 or self.longest + steps > self.max_len:
+            raise ValueError("an even number of 2 or more steps expected, and %d tokens with the longest "
+                             "prompt's %d at most" % (self.max_len, self.longest))
+        self.longest += steps
         pairs = steps // 2
         if graph:
             self.half(0, 1)           # the libraries' first calls stay out of the graph
@@ -129,7 +137,7 @@ def main():
     p.add_argument("--seqs", type=int, default=4)
     p.add_argument("--beams", type=int, default=4)
     p.add_argument("--prompt", type=int, default=100, help="length of the longest prompt")
-    p.add_argument("--steps", type=int, default=32, help="even")
+    p.add_argument("--steps", type=int, default=32, help="even, 2 or more")
     p.add_argument("--graph", action="store_true")
     a = p.parse_args()
     d = Beams(a.seqs, a.beams, a.prompt + a.steps + 4)

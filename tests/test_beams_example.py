@@ -1,4 +1,5 @@
-"""The beam search example where it cannot go on, as pages run out, and started again."""
+"""The beam search example where it cannot go on, as pages run out or tokens would pass the
+buffers, and started again."""
 import os
 import sys
 
@@ -47,3 +48,33 @@ def test_a_second_search_is_as_a_fresh_one():
         here = slice(3 * row, 3 * row + 3)
         assert torch.equal(got[0][here, :n + 8], want[0][here, :n + 8])
     assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("steps", [-2, 0, 1, 7, 10, 1000])
+def test_steps_past_the_buffers_are_refused_before_any_gpu_call(steps):
+    import beams
+    d = beams.Beams.__new__(beams.Beams)
+    d.max_len, d.longest = 80, 72        # room for 8
+    for graph in (False, True):
+        with pytest.raises(ValueError, match="steps"):
+            d.search(steps, graph=graph)
+    assert d.longest == 72
+
+
+@pytest.mark.parametrize("lens", [(3, 4), (3, 4, 0), (3, 81, 4), (1, 2, 3, 4)])
+def test_prompts_that_do_not_fit_are_refused_before_any_gpu_call(lens):
+    import beams
+    d = beams.Beams.__new__(beams.Beams)
+    d.max_len, d.seqs = 80, 3
+    with pytest.raises(ValueError, match="prompts"):
+        d.start(prompts(1, lens))
+
+
+@pytest.mark.gpu
+def test_a_search_up_to_the_last_place():
+    d = made()
+    d.start(prompts(7, (70, 80 - 6, 1)))
+    d.search(6)
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError, match="steps"):
+        d.search(2)
