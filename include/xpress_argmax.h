@@ -500,7 +500,9 @@ int xpress_sink_attention(const xpress_paged_attention_args* args, int64_t sinks
  *         (itself only if its own bit is; the window does not apply).
  *
  * Any mask is accepted, not ancestors alone: a node that sees no key gives out = 0,
- * lse = -inf.  Nodes at negative places (len < Q) do not exist.
+ * lse = -inf.  There is no key at a negative place (len < Q), whatever names it; the row
+ * of a query whose own place is negative is computed like any other, from the nodes
+ * that its bits name and that there are (its bits 0: out = 0, lse = -inf).
  *
  *   tree     device pointer, int32 words [N, Q, ceil(Q / 32)], strides in words
  *            (not negative, 0 for one tree of all sequences), unit stride along the
