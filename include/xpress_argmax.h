@@ -532,11 +532,13 @@ int xpress_sparse_attention_reserve(int64_t N, int64_t Q, int64_t Hq, int64_t he
  * row), so that results do not depend on the order of the work.  Entries outside
  * [0, pages) name no page.  Tables are int32 [rows, width] with a row stride of at
  * least width (any with one row) and unit stride along width; width * page_size < 2^31.
- * Where pages run out, the entries that lack one are -1 and *missing (int32 on the
- * device, or null) receives their number; it is written by every call.  All
+ * Where pages run out, the entries that lack one name none (-1 in a fork; what they were
+ * in xpress_kv_grow) and *missing (int32 on the device, or null) receives their number;
+ * it is written by every call.  All
  * functions are asynchronous and use no workspace.  XPRESS_EINVAL: a size or
  * stride outside what is said here, a null or misaligned pointer, or an array that is
- * written sharing bytes with another; nothing is queued.
+ * written whose span, from its first byte to its last with the gaps between rows, meets
+ * another's; nothing is queued.
  *
  * xpress_kv_fork -- M new rows of a table from N old ones.  Row m continues source
  * n = src[m] (outside [0, N): an empty row, all -1) with its lens[n] tokens, clamped to
@@ -657,8 +659,11 @@ typedef struct xpress_beam_state {
 /*
  * xpress_beam_reorder -- every state's row src[m] of N goes to its row m of M; where
  * src[m] is outside [0, N), row m becomes zeros.  states is host memory, read during
- * the call; up to 4096 of them.  src is int32 [M] on the device.  What is written
- * must not share bytes with anything that the call reads or writes besides.
+ * the call; up to 4096 of them.  src is int32 [M] on the device.  The span that
+ * is written of a state, from row 0's first byte to row M - 1's last with the gaps
+ * between rows, must not meet that of anything which the call reads or writes
+ * besides: XPRESS_EINVAL (states that lie between each other's rows are one state of
+ * longer rows).
  * Asynchronous; one launch for every 8 states; accesses are of 16 bytes where rows and
  * steps allow it, else of 4 or 1.
  */
