@@ -543,9 +543,11 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n)
     }
 }
 
-// Rows behind the first dimension, each one after the other in memory.
+// Rows behind the first dimension, each one after the other in memory, which holds the
+// values themselves (not those whose conjugate or negative the tensor stands for).
 bool whole_rows(const Tensor& t)
 {
+    if (t.is_conj() || t.is_neg()) return false;
     int64_t step = 1;
     for (int64_t i = t.dim() - 1; i > 0; --i) {
         if (t.size(i) != 1 && t.stride(i) != step) return false;

@@ -993,6 +993,8 @@ def xpress_beam_reorder(states, src, stream=None) -> None:
                 _elsewhere(t, what, dev)
             if t.shape[0] > 0 and not t[0].is_contiguous():
                 raise ValueError("%s: contiguous rows expected, got strides %s" % (what, t.stride()))
+            if t.is_conj() or t.is_neg():   # their memory does not hold their values
+                raise ValueError("%s: conjugate and negative views are not taken (resolve_conj, resolve_neg)" % what)
         N, size = old.shape[0], old.element_size()
         row = size
         for x in old.shape[1:]:
