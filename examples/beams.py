@@ -24,7 +24,10 @@ class Beams(Decoder):
     """Beams of N sequences over a pool of `pages` pages."""
 
     def __init__(self, N, beams, max_len, window=64, sinks=4, page=16, pages=None, **kw):
-        super().__init__(N * beams, max_len, page=page, **kw)
+        # a page more a row than its tokens need: where all rows hold all of theirs, a fork takes
+        # new ones for the beams that part before those which it gives back are free
+        super().__init__(N * beams, max_len + page, page=page, **kw)
+        self.max_len = max_len
         self.seqs, self.beams, self.window, self.sinks, self.page = N, beams, window, sinks, page
         rows, width = N * beams, self.table.shape[1]
         pages = self.k_cache.shape[0] if pages is None else pages

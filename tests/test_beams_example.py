@@ -78,3 +78,15 @@ def test_a_search_up_to_the_last_place():
     torch.cuda.synchronize()
     with pytest.raises(ValueError, match="steps"):
         d.search(2)
+
+
+@pytest.mark.gpu
+def test_the_pool_holds_any_parting_of_full_rows():
+    """Nine rows of 79 tokens, no page shared, of which each sequence's first goes on as three."""
+    from vocab_wide_add_amd import native
+    d = made()
+    lens = torch.full((9,), 79, dtype=torch.int32, device="cuda")
+    native.xpress_kv_grow(d.refs[0], d.tables[0], torch.zeros_like(lens), lens, 8, missing=d.missing[0])
+    src = (torch.arange(9, device="cuda") // 3 * 3).to(torch.int32)
+    native.xpress_kv_fork(d.refs[0], d.tables[0], lens, src, d.refs[1], d.tables[1], d.copies, 8, missing=d.missing[1])
+    assert d.missing.tolist() == [[0], [0]] and int((d.copies[:, 1] >= 0).sum()) == 6
