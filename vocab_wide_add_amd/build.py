@@ -75,8 +75,8 @@ def build_marshal(verbose: bool = False) -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile the library and the host module; returns the library's path
-    (always recompiles).  The sources are compiled side by side: the two forms of
-    the attention take a minute and a half each."""
+    (always recompiles).  The sources are compiled side by side: the three forms of
+    the attention take one to two and a half minutes each."""
     with tempfile.TemporaryDirectory(dir=PKG, prefix="build_") as tmp, \
             concurrent.futures.ThreadPoolExecutor(JOBS) as pool:
         objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SRCS]

@@ -47,9 +47,11 @@
 // tile asks per key, and the sinks and the window's keys are numbered one after the
 // other, so that what lies between them costs nothing.  The dense form has none of it.
 // Measured (32 query and 8 key-value heads of 128, bf16): trees of 16 nodes on 32
-// sequences up to 4096 tokens 70 us and 6 for the join, 4.2 TB/s, the copies' pace as
-// for the dense block; 32 windows of 4096 behind 4 sinks 104 and 4, 5.2 TB/s; a tree of 8
-// on one sequence of 1009 9.5 and 3.4, latency.
+// sequences up to 4096 tokens 61 to 79 us by their lengths and 6 to 7 for the join, 4.0
+// TB/s, the copies' pace as for the dense block (on an e4m3 cache the whole call 74 for 75:
+// not by bytes, of which it has half); 32
+// windows of 4096 behind 4 sinks 104 and 5, 5.2 TB/s (e4m3 56 in all, 4.8 TB/s); a tree
+// of 8 on one sequence of 1009 9.2 and 3.9, latency.
 //
 // The waves' sums meet in LDS.  A sequence of one part is written out
 // directly; with more parts (chosen on the host from the number of rows'
@@ -804,8 +806,9 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attention_kernel(
     const uint32_t hk = owner % a.Hk;
     if constexpr (SPARSE) {
         // Long parts first where not all fit the chip at once and lengths may differ (16
-        // nodes of 32 sequences up to 4096, heads of 128: the call 77 us, in the order of
-        // the sequences 87; of 64: 54 and 60)
+        // nodes of 32 sequences up to 4096, heads of 128: the call 75 us, in the order of
+        // the sequences 87; of 48 up to 2700 75 and 84; 64 of 2 heads, 51 and 51).  Up to as
+        // many parts as the workgroup has threads; more were not looked at.
         if (a.N > 1 && a.window == 0 && a.N * a.splits <= kRanked && a.units * a.groups > 2 * kUnits) {
             const uint32_t x = part_by_size(a, unit / a.Hk, reinterpret_cast<uint32_t*>(pool), &holes);
             split = x / a.N;
@@ -1121,8 +1124,8 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a)
 
 // The sparse form's join of up to 16 parts: a workgroup belongs to one owner, whose
 // number of parts is the same for all its rows, and a thread takes four dims of a row
-// and asks for all their parts at once.  (A wave for a row: 22 us where this takes 13, for
-// 256 rows a head of 256 owners; its loads wait for each other.)
+// and asks for all their parts at once.  (A wave for a row: 22 us where this takes 11 to 13,
+// for 256 rows a head of 256 owners; its loads wait for each other.)
 template <bool FP16>
 __global__ void __launch_bounds__(256) join_few_kernel(AttnArgs a)
 {
@@ -1230,6 +1233,15 @@ struct Plan {
 // rows alone fill the chip four times over, and parts would only add their sums
 // (4096 queries over 32768 keys, 32 heads on 8: 4.3 ms, 7.1 in 32 parts; over 8192
 // keys 1.30 and 1.50 in 8).
+//
+// The sparse form goes to wide_attention.hip from 65 rows a head on.  Whole calls of
+// the form that is taken and of the other, trees on 32 sequences up to 4096, heads of 128,
+// bf16, by rows a head: 48: 72 and 79 us; 64: 75 and 79; 68: 85 and 104; 128: 98 and 117.
+// Heads of 64, e4m3, 48 sequences: 63 rows 68 and 68, 70 rows 69 and 100.  Heads of 256:
+// 64 rows 81 and 87, 68 rows 88 and 138.  A window with sinks, 35 heads of 80, fp16: 63
+// rows 35 and 44, 70 rows 44 and 46.  One sequence of 1009: 64 rows 14.4 and 16.9, 68 rows
+// 17.0 and 14.8; of 32768: 47 and 52, 54 and 52.  128 sequences up to 2000, 64 rows: 148 and
+// 132, as this form cuts them by its table of places.
 constexpr int64_t kMostWords = (int64_t)1 << 27;   // 1 GiB
 
 // Workspace words (8 bytes) of one part of every row: sums and (m, l).

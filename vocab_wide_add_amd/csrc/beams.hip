@@ -31,8 +31,10 @@
 // Bound by the bytes for many rows; by the two launches and the chain of one workgroup
 // for few.  Measured (V = 152064, K = 8): 480 rows of 60 sequences with a bias 57 us for
 // the parts, 5.1 TB/s, and 10 for the join, most of it the logs and the lists' loads, each
-// waited for; 4 rows of one 8.2 and 7.3.  Their states (256 tokens and 4096 hidden values
-// a row) 5 and 3.0.  Two vectors of a thread on their way in place of four: 71 us for the
+// waited for; 4 rows of one 8.3 and 7.6.  Their states (256 tokens and 4096 hidden values
+// a row) 5 and 3.0.  Whole calls for the 480 rows without a bias 52, by instructions a logit,
+// and in rows that are not on 16 bytes, whose logits are loaded one by one, 189 with a bias
+// and 128 without.  Two vectors of a thread on their way in place of four: 71 us for the
 // 68 of the whole; six 72; shorter parts 69.
 
 #include <hip/hip_runtime.h>
@@ -699,8 +701,10 @@ bool shape_ok(const Shape& s)
            s.K >= 1 && s.K <= kMostK && s.N <= (kMost / s.beams);
 }
 
-// Parts: two workgroups a compute unit where the rows alone are fewer, but no part of
-// fewer vectors than a workgroup has threads; and none that has more than kRuns.
+// Parts: up to two workgroups a compute unit where the rows alone are fewer, but no part of
+// fewer vectors than a workgroup has threads, nor of more than kRuns.  Parts of more are whole
+// rounds of the threads, and so fewer: 4 rows of 152064 in 37 parts would have 514 vectors
+// each, and are 19 of 1024.
 Plan plan_of(const Shape& s)
 {
     const int64_t vecs = (s.V + 7) / 8, rows = s.N * s.beams;

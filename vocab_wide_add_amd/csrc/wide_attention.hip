@@ -20,12 +20,16 @@
 // and page ids come by LDS.
 //
 // Measured (32 query and 8 key-value heads of 128, bf16): 64 nodes of 32 sequences up to
-// 4096 tokens 162 us and 11 for the join, where 16 rows a wave took 200: 0.7 PFLOP/s
+// 4096 tokens 158 to 190 us by their lengths and 11 to 13 for the join (16 rows a wave
+// 200 where this took 162): 0.7 PFLOP/s
 // with the weights' second part, and 0.34 GB of cache that two workgroups each read.
 // Without products and weights the copies take 90, without copies the rest 125.  77 rows of heads
-// of 64 on an e4m3 cache, 48 sequences up to 6001: 62 and 5 (92 with 16 rows;
-// 66 with the transposition in registers, and 77 with each value row's place in LDS
-// worked out by itself).  Tried: eight
+// of 64 on an e4m3 cache, 48 sequences up to 6001: 68 and 5 under the profiler, the whole
+// call 69 (100 with 16 rows; 73 with the transposition in registers, and 84 with each value
+// row's place in LDS worked out by itself).  4096 new tokens of one sequence under a window
+// and sinks: 438 us for a window of 4096, where their products take 107 at the library's
+// rate, and 459 for one of 1024, where they take 47: every 128 rows go through the keys of all.  Which
+// calls come here: see plan_of.  Tried: eight
 // waves of 32 rows, which read the cache once, 205 for the 187; weights of one tile
 // beside the products of the next 209; three workgroups a compute unit at 64 dims: no
 // change.
